@@ -54,6 +54,15 @@
  *     must then stay allocated and unused by other work.
  *   - Calls that share a workspace, or that update the same buffers, must be
  *     ordered by the caller (same stream, or events).
+ *
+ * Next to the step the library has the operators of the layers whose weights
+ * it updates, in the form in which such layers are trained on this GPU: 8-bit
+ * operands with a power-of-two scale for each block of 128, their products
+ * (forward, input gradient, weight gradient; dense, batched and over the
+ * ragged row groups of mixture-of-experts layers), the routing of rows to
+ * experts, and the weighted sum of the experts' outputs. A weight gradient can
+ * be written straight into the packed gradients that muon_step reads, and the
+ * 8-bit weights are quantised straight from its packed params.
  */
 #ifndef MUON_STEP_H
 #define MUON_STEP_H
@@ -347,6 +356,211 @@ int muon_plan_owners(const muon_param_t* params, int32_t n_params, int32_t n_own
  * Multiply by the element size of the wire format for bytes. Returns a
  * negative value for invalid input. */
 double muon_comm_elements(int64_t p_m, int32_t n_ranks, int32_t zero_stage, int32_t dedicated);
+
+/* ---- 8-bit operands ------------------------------------------------------
+ * A quantised operand holds `batch` matrices of rows x cols, contracted along
+ * cols by the products below. Row r's columns [128 b, 128 b + 128) are one
+ * block with one scale 2^e: element = value8 * 2^e, the value in e4m3 (no
+ * infinities, largest 448) or e5m2 (largest finite 57344), e stored as the
+ * byte e + 127. A power of two loses nothing to the scale itself, and the
+ * matrix instruction applies it exactly while it multiplies.
+ *   data   batch x rows x P bytes, P = cols rounded up to a multiple of 128;
+ *          columns [cols, P) hold zeros. 16-byte aligned.
+ *   scale  batch x rows x S bytes, S = P / 128 rounded up to a multiple of 4;
+ *          bytes [P / 128, S) hold 127. 4-byte aligned.
+ * The transposed operand of a rows x cols matrix is the quantised operand of
+ * its transpose: cols x rows, contracted along the former rows. */
+enum { MUON_FP8_E4M3 = 0, MUON_FP8_E5M2 = 1 };
+#define MUON_FP8_BLOCK 128
+
+/* Limits of the 8-bit operands and products: rows, cols <= MUON_FP8_MAX_SIDE,
+ * batch and groups <= MUON_FP8_MAX_BATCH. */
+#define MUON_FP8_MAX_SIDE (1 << 23)
+#define MUON_FP8_MAX_BATCH 1024
+
+typedef struct {
+  uint8_t* data;   /* device */
+  uint8_t* scale;  /* device */
+  int64_t batch;
+  int64_t rows;
+  int64_t cols;
+  int32_t format;  /* MUON_FP8_E4M3 | MUON_FP8_E5M2 */
+  int32_t reserved;
+} muon_fp8_t;
+
+/* The source of muon_fp8_quantize: `batch` matrices of rows x cols elements of
+ * `dtype`, element (r, c) of matrix i at data + i * batch_stride + r * ld + c
+ * (strides in elements).
+ * With row_index (device int32[out_rows], batch 1) row r of the quantised
+ * matrix is row row_index[r] / row_div of the source, and a row of zeros where
+ * row_index[r] is negative or beyond the source: muon_expert_order's `rows`
+ * with row_div = top_k gives each routed row its token's row. row_weight
+ * (device float32, n_weights elements, optional, with row_index only)
+ * multiplies row r by row_weight[row_index[r]] in fp32 first (rows of zeros
+ * where row_index[r] >= n_weights). */
+typedef struct {
+  const void* data;
+  int64_t batch_stride;
+  int64_t ld;
+  int64_t batch;
+  int64_t rows;
+  int64_t cols;
+  int32_t dtype;
+  int32_t row_div;           /* >= 1; 1 unless row_index is given */
+  const int32_t* row_index;  /* NULL: all rows in order */
+  int64_t out_rows;          /* rows of the quantised matrix (= rows without row_index) */
+  const float* row_weight;
+  int64_t n_weights;
+} muon_fp8_source_t;
+
+/* Quantise a matrix into `out` (out_rows x cols), into `out_t` (its transpose,
+ * cols x out_rows), or both in one pass over the source; either may be NULL.
+ * Per block: amax = the largest finite magnitude, e = the least integer >= -126
+ * with amax <= 448 * 2^e (57344 * 2^e), 0 for a block of zeros; the value is
+ * x * 2^-e rounded to the nearest, ties to even. A NaN stays NaN; an infinity
+ * becomes NaN in e4m3 and stays an infinity in e5m2; neither touches its
+ * block's other values. With `blocks` the scale is shared by 128 x 128
+ * elements, so that out and out_t hold the same values (weights); without it
+ * each row (out) or column (out_t) has its own. Errors: MUON_ERR_NULL,
+ * BAD_SHAPE (sizes outside the limits, out or out_t of another shape),
+ * UNSUPPORTED (dtype, format), ALIGN, OVERLAP. */
+int muon_fp8_quantize(const muon_fp8_source_t* src, int32_t blocks, const muon_fp8_t* out,
+                      const muon_fp8_t* out_t, void* stream);
+
+/* Where a product goes: rows x cols elements of `dtype` (F32, BF16, F16),
+ * element (i, j) of matrix g at data + g * batch_stride + i * ld + j. With
+ * `accumulate` the product is added to what is there (the sum formed in fp32
+ * and rounded once). */
+typedef struct {
+  void* data;
+  int64_t batch_stride;
+  int64_t ld;
+  int32_t dtype;
+  int32_t accumulate;
+} muon_fp8_result_t;
+
+/* Products of quantised operands, C[i][j] (+)= sum_k A[i][k] B[j][k], summed in
+ * fp32 and rounded once. a: M x K, b: N x K (same K). A BF16 or F16 result is
+ * formed by the 8-bit matrix instructions, which cut each product to 13 bits
+ * below the largest of its eight neighbours along k (about 1.3e-5 of the
+ * result's norm); an F32 result from exact products, at half their rate.
+ *   group_offsets NULL: a.batch == b.batch, one product per matrix.
+ *   group_offsets (device int32[b.batch + 1], ascending, a.batch == 1): rows
+ *   [offsets[g], offsets[g + 1]) of A meet matrix g of B and give the same rows
+ *   of C. Rows outside every group are not written. Offsets are clamped to
+ *   [0, M] and to the previous one.
+ * With the forward product Y = X W^T of W (N x K): the input gradient is the
+ * product of dY and W's transposed operand, the weight gradient that of the
+ * transposed operands of dY and X.
+ * workspace (device, 16-byte aligned, muon_fp8_matmul_workspace_size() bytes):
+ * partial sums when the contraction is split over workgroups, which a product
+ * of few tiles needs to fill the GPU; NULL with 0 bytes never splits. The
+ * result does not depend on timing, but its last bits do on the split.
+ * Errors: MUON_ERR_NULL, BAD_SHAPE, UNSUPPORTED, ALIGN (operands and result
+ * must be aligned to their element, data to 16 bytes), OVERLAP. */
+int muon_fp8_matmul(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* group_offsets,
+                    const muon_fp8_result_t* c, void* workspace, size_t workspace_bytes, void* stream);
+int muon_fp8_matmul_workspace_size(const muon_fp8_t* a, const muon_fp8_t* b, int32_t grouped,
+                                   size_t* bytes_out);
+
+/* Grouped contractions (the experts' weight gradients): matrix g of C, M x N,
+ * (+)= sum over k in [offsets[g], offsets[g + 1]) of A[i][k] B[j][k], for
+ * n_groups groups (device int32[n_groups + 1], ascending). a: M x K, b: N x K,
+ * batch 1. Offsets must be multiples of 128, as muon_expert_order gives them
+ * with align 128 (a group's sum runs over whole blocks, from offset / 128
+ * rounded down to the next offset / 128 rounded up), and are clamped to
+ * [0, K] and to the previous one. A group without columns gives zeros (with
+ * accumulate: leaves its matrix). */
+int muon_fp8_matmul_grouped_k(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* group_offsets,
+                              int32_t n_groups, const muon_fp8_result_t* c, void* stream);
+
+/* ---- Mixture of experts --------------------------------------------------- */
+
+/* Score functions of the router. */
+enum { MUON_ROUTE_SOFTMAX = 0, MUON_ROUTE_SIGMOID = 1 };
+
+/* Limits: experts <= MUON_ROUTE_MAX_EXPERTS, top_k <= MUON_ROUTE_MAX_TOP_K,
+ * n_groups <= MUON_ROUTE_MAX_GROUPS, tokens * top_k < 2^31. */
+#define MUON_ROUTE_MAX_EXPERTS 1024
+#define MUON_ROUTE_MAX_TOP_K 32
+#define MUON_ROUTE_MAX_GROUPS 64
+
+/* How a router chooses. Fill with muon_default_route_hyper() first. */
+typedef struct {
+  int32_t score;        /* MUON_ROUTE_SOFTMAX (default) | MUON_ROUTE_SIGMOID */
+  int32_t top_k;        /* experts per token; default 1 */
+  int32_t n_groups;     /* groups of consecutive experts, dividing their number; default 1 */
+  int32_t top_groups;   /* groups a token may choose from; default 1 (= all with one group) */
+  int32_t group_top;    /* 1 | 2: a group's score is the sum of its so many largest keys; default 2 */
+  int32_t renormalize;  /* default 1: divide the weights by their sum + 1e-20 */
+  float scale;          /* factor of the weights; default 1 */
+  int32_t reserved;
+} muon_route_hyper_t;
+
+void muon_default_route_hyper(muon_route_hyper_t* h);
+
+/* Route `tokens` rows to experts. logits: device, dtype, tokens x experts, row
+ * pitch ld elements. bias: device float32[experts] or NULL, added for the
+ * choice only. Per token, in 64 bits:
+ *   s = softmax(logits) or sigmoid(logits);  key = s + bias;
+ *   with n_groups > 1 only the top_groups groups of largest score are kept;
+ *   the top_k experts of largest key, in that order, ties to the lower index;
+ *   weight = scale * s, divided by the sum of the chosen s + 1e-20 with
+ *   renormalize.
+ * An expert whose logit or key is -inf is never chosen; with fewer experts left
+ * than top_k the remaining slots have id -1 and weight 0 (a row of -inf, such
+ * as a padding token's, chooses none). A NaN key orders below every number.
+ *   ids      device int32[tokens x top_k]
+ *   weights  device float32[tokens x top_k] */
+int muon_route(const void* logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t ld,
+               const float* bias, const muon_route_hyper_t* h, int32_t* ids, float* weights,
+               void* stream);
+
+/* The gradient of the weights with respect to the logits, for the chosen ids
+ * (choosing itself has none): dlogits (device, dtype, tokens x experts, pitch
+ * ld_d, every element written) from dweights (device float32[tokens x top_k]).
+ * Slots with an id outside [0, experts) have no gradient; a logit of -inf gets
+ * zero. Ids of one token must differ. h as in the forward call (its groups do
+ * not matter here). */
+int muon_route_backward(const float* dweights, const void* logits, int32_t dtype, int64_t tokens,
+                        int32_t experts, int64_t ld, const int32_t* ids, const muon_route_hyper_t* h,
+                        void* dlogits, int64_t ld_d, void* stream);
+
+/* Order of n flat slots (slot = token * top_k + j) by expert. Expert e's slots
+ * come in ascending order at rows [offsets[e], offsets[e] + counts[e]), and
+ * offsets[e + 1] = offsets[e] + counts[e] rounded up to a multiple of `align`
+ * (1 .. 1024).
+ *   ids      device int32[n]; a value outside [0, experts) is a slot without row
+ *   offsets  device int32[experts + 1]
+ *   counts   device int32[experts] (the load that a balance bias is steered by)
+ *   rows     device int32[capacity]: the slot of each row; -1 for padding and
+ *            for every row from offsets[experts] on
+ *   pos      device int32[n]: the row of each slot, -1 for none
+ *   capacity >= n + experts * (align - 1), so any routing fits, < 2^31
+ *   workspace device, muon_expert_order_workspace_size() bytes, 4-byte aligned
+ *            (NULL where that is 0) */
+int muon_expert_order(const int32_t* ids, int64_t n, int32_t experts, int32_t align, int32_t* offsets,
+                      int32_t* counts, int32_t* rows, int64_t capacity, int32_t* pos,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int muon_expert_order_workspace_size(int64_t n, int32_t experts, size_t* bytes_out);
+
+/* Weighted sum of the experts' outputs: y[t] = sum_j weights[t][j] * o[pos[t][j]],
+ * in fp32 in the order of j, rounded once. o: device, dtype, o_rows x cols; y:
+ * device, dtype, tokens x cols; both contiguous rows with pitches ld_o, ld_y.
+ * Slots whose pos is outside [0, o_rows) add nothing. top_k <=
+ * MUON_ROUTE_MAX_TOP_K. */
+int muon_combine(const void* o, int32_t dtype, int64_t o_rows, int64_t cols, int64_t ld_o,
+                 const int32_t* pos, const float* weights, int64_t tokens, int32_t top_k, void* y,
+                 int64_t ld_y, void* stream);
+
+/* Its gradients: dweights[t][j] = <dy[t], o[pos[t][j]]> (fp32 sums; 0 for a slot
+ * without row) and do[pos[t][j]] = weights[t][j] * dy[t] (rows that no slot
+ * points at are not written; positions must differ). Either output may be
+ * NULL; without dweights, o may be NULL too. */
+int muon_combine_backward(const void* dy, int32_t dtype, int64_t tokens, int64_t cols, int64_t ld_dy,
+                          const void* o, int64_t o_rows, int64_t ld_o, const int32_t* pos,
+                          const float* weights, int32_t top_k, float* dweights, void* d_o,
+                          int64_t ld_do, void* stream);
 
 /* Message for the last failing call on this thread ("" if none). Valid until the
  * next call on this thread. */

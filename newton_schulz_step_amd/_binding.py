@@ -25,12 +25,18 @@ STATUS_NAMES = {
 }
 DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
 NS_METHODS = {"standard": 0, "gram": 1}
+FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
+FP8_BLOCK = 128                        # MUON_FP8_BLOCK
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 EXPORTED = (
     "muon_default_hyper", "muon_default_adamw_hyper", "muon_workspace_size", "muon_step",
     "muon_step_window", "adamw_step", "muon_pack", "muon_unpack", "muon_last_error", "muon_release_plans",
     "muon_profile_begin", "muon_profile_end", "muon_version", "muon_ns_flops",
     "muon_plan_owners", "muon_comm_elements", "muon_step_noalloc",
+    "muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_workspace_size", "muon_fp8_matmul_grouped_k",
+    "muon_default_route_hyper", "muon_route", "muon_route_backward", "muon_expert_order",
+    "muon_expert_order_workspace_size", "muon_combine", "muon_combine_backward",
 )
 NOALLOC_WORKSPACE_BYTES = 64 << 20     # MUON_NOALLOC_WORKSPACE_BYTES
 
@@ -90,6 +96,30 @@ class KernelStat(ctypes.Structure):
                 ("total_ms", ctypes.c_double)]
 
 
+class Fp8Operand(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("batch", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Fp8Source(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("row_div", ctypes.c_int32), ("row_index", ctypes.c_void_p),
+                ("out_rows", ctypes.c_int64), ("row_weight", ctypes.c_void_p), ("n_weights", ctypes.c_int64)]
+
+
+class Fp8Result(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class RouteHyper(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -136,6 +166,24 @@ def load() -> ctypes.CDLL:
         lib.muon_last_error.restype = ctypes.c_char_p
         lib.muon_version.restype = ctypes.c_char_p
         lib.muon_profile_end.argtypes = [ctypes.POINTER(KernelStat), i32, ctypes.POINTER(i32)]
+        po, ps, pr = ctypes.POINTER(Fp8Operand), ctypes.POINTER(Fp8Source), ctypes.POINTER(Fp8Result)
+        ph = ctypes.POINTER(RouteHyper)
+        lib.muon_fp8_quantize.argtypes = [ps, i32, po, po, vp]
+        lib.muon_fp8_matmul.argtypes = [po, po, vp, pr, vp, sz, vp]
+        lib.muon_fp8_matmul_workspace_size.argtypes = [po, po, i32, ctypes.POINTER(sz)]
+        lib.muon_fp8_matmul_grouped_k.argtypes = [po, po, vp, i32, pr, vp]
+        lib.muon_default_route_hyper.argtypes = [ph]
+        lib.muon_default_route_hyper.restype = None
+        lib.muon_route.argtypes = [vp, i32, i64, i32, i64, vp, ph, vp, vp, vp]
+        lib.muon_route_backward.argtypes = [vp, vp, i32, i64, i32, i64, vp, ph, vp, i64, vp]
+        lib.muon_expert_order.argtypes = [vp, i64, i32, i32, vp, vp, vp, i64, vp, vp, sz, vp]
+        lib.muon_expert_order_workspace_size.argtypes = [i64, i32, ctypes.POINTER(sz)]
+        lib.muon_combine.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp]
+        lib.muon_combine_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp]
+        for name in ("muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_workspace_size",
+                     "muon_fp8_matmul_grouped_k", "muon_route", "muon_route_backward", "muon_expert_order",
+                     "muon_expert_order_workspace_size", "muon_combine", "muon_combine_backward"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("muon_workspace_size", "muon_step", "muon_step_noalloc", "muon_step_window", "muon_plan_owners",
                      "adamw_step", "muon_pack", "muon_unpack",
                      "muon_release_plans", "muon_profile_begin", "muon_profile_end"):
@@ -494,3 +542,354 @@ def profile_end() -> Dict[str, Tuple[int, float]]:
     n = ctypes.c_int32(0)
     _check(load().muon_profile_end(out, 64, ctypes.byref(n)))
     return {out[i].name.decode(): (out[i].launches, out[i].total_ms) for i in range(min(n.value, 64))}
+
+
+# ----------------------------------------------------------------------------- 8-bit operands and experts
+
+def _fp8_types():
+    torch = _torch()
+    return {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _last_dense(t, name):
+    """(pointer, row pitch, batch stride) of a 2-D or 3-D tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a matrix or a batch of matrices")
+    shape, stride = t.shape, t.stride()
+    if shape[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    ld = stride[-2] if shape[-2] > 1 else shape[-1]
+    bs = stride[0] if t.dim() == 3 and shape[0] > 1 else 0
+    return t.data_ptr(), ld, bs
+
+
+class _on:
+    """Runs a call on `dev` and `stream`: outputs and workspaces that the binding
+    allocates belong to that stream. A raw stream handle has no torch allocator,
+    so it takes calls whose outputs are given (`fresh` then refuses)."""
+
+    def __init__(self, dev, stream):
+        torch = _torch()
+        self.dev, self.raw = dev, stream is not None and not isinstance(stream, torch.cuda.Stream)
+        self._ctx = torch.cuda.stream(stream) if stream is not None and not self.raw else torch.cuda.device(dev)
+        self._same = stream is None and torch.cuda.current_device() == dev.index
+        if stream is not None and not self.raw and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self._stream = stream
+
+    def __enter__(self):
+        torch = _torch()
+        if not self._same:
+            self._ctx.__enter__()
+            if self.raw:
+                self.handle = int(self._stream)
+                return self
+        self.handle = torch.cuda.current_stream(self.dev).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if not self._same:
+            self._ctx.__exit__(*exc)
+
+    def fresh(self, *shape, dtype):
+        if self.raw:
+            raise ValueError("with a raw stream handle the outputs must be given")
+        return _torch().empty(shape, dtype=dtype, device=self.dev)
+
+    def scratch(self, nbytes):
+        """Workspace of a call: cached per (device, stream); under graph capture one of
+        its own, from the graph's memory, so that no two graphs share it."""
+        torch = _torch()
+        if nbytes == 0:
+            return None
+        if not self.raw and torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
+        return workspace(nbytes, self.dev, self._stream)
+
+
+class Fp8:
+    """A quantised operand (muon_fp8_t): float8 `data` [..., rows, cols padded to 128],
+    float8_e8m0fnu `scale` [..., rows, blocks of 128 padded to 4], and its number of
+    columns. One matrix, or a batch of them in the first dimension."""
+
+    __slots__ = ("data", "scale", "cols")
+
+    def __init__(self, data, scale, cols: int):
+        torch = _torch()
+        if data.dtype not in _fp8_types() or scale.dtype != torch.float8_e8m0fnu:
+            raise TypeError("data must be float8_e4m3fn or float8_e5m2, scale float8_e8m0fnu")
+        pitch = -(-cols // FP8_BLOCK) * FP8_BLOCK
+        want = tuple(data.shape[:-1]) + (-(-(pitch // FP8_BLOCK) // 4) * 4,)
+        if data.dim() not in (2, 3) or data.shape[-1] != pitch or tuple(scale.shape) != want:
+            raise ValueError(f"{cols} columns take data of {pitch} columns and scale of shape {want}, "
+                             f"got {tuple(data.shape)} and {tuple(scale.shape)}")
+        self.data, self.scale, self.cols = data, scale, cols
+
+    @property
+    def rows(self) -> int:
+        return self.data.shape[-2]
+
+    @property
+    def format(self) -> str:
+        return "e4m3" if _fp8_types()[self.data.dtype] == 0 else "e5m2"
+
+    def _c(self) -> Fp8Operand:
+        d = self.data
+        return Fp8Operand(_ptr(d), _ptr(self.scale), d.shape[0] if d.dim() == 3 else 1, d.shape[-2], self.cols,
+                          _fp8_types()[d.dtype], 0)
+
+
+def fp8_empty(rows: int, cols: int, fmt: str = "e4m3", device="cuda", batch: Optional[int] = None) -> Fp8:
+    """An uninitialised operand of rows x cols (a batch of them with `batch`)."""
+    torch = _torch()
+    if fmt not in FP8_FORMATS:
+        raise ValueError(f"format must be one of {sorted(FP8_FORMATS)}, got {fmt!r}")
+    lead = () if batch is None else (batch,)
+    pitch = -(-cols // FP8_BLOCK) * FP8_BLOCK
+    dt = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+    data = torch.empty(lead + (rows, pitch), dtype=dt, device=device)
+    scale = torch.empty(lead + (rows, -(-(pitch // FP8_BLOCK) // 4) * 4), dtype=torch.float8_e8m0fnu, device=device)
+    return Fp8(data, scale, cols)
+
+
+def fp8_quantize(x, fmt: str = "e4m3", blocks: bool = False, transposed="no", row_index=None, row_div: int = 1,
+                 row_weight=None, out: Optional[Fp8] = None, out_t: Optional[Fp8] = None, stream=None):
+    """Quantise x (muon_fp8_quantize): [rows, cols] or a batch of them, float32,
+    bfloat16 or float16, rows contiguous (any row pitch: a view into a packed
+    buffer will do). transposed: "no" returns the operand, "only" the transposed
+    one, "both" the pair. row_index (int32): row r of the result is x's row
+    row_index[r] // row_div, zeros for a negative one, times
+    row_weight[row_index[r]] where that is given. out / out_t: results of an
+    earlier call to write into."""
+    torch = _torch()
+    if transposed not in ("no", "only", "both"):
+        raise ValueError('transposed must be "no", "only" or "both"')
+    if fmt not in FP8_FORMATS:
+        raise ValueError(f"format must be one of {sorted(FP8_FORMATS)}, got {fmt!r}")
+    if (out is not None and transposed == "only") or (out_t is not None and transposed == "no"):
+        raise ValueError("an output was given that `transposed` does not ask for")
+    for t, dt, name in ((row_index, torch.int32, "row_index"), (row_weight, torch.float32, "row_weight")):
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}")
+    ptr, ld, bs = _last_dense(x, "x")
+    batch = x.shape[0] if x.dim() == 3 else None
+    cols = x.shape[-1]
+    rows = x.shape[-2] if row_index is None else row_index.numel()
+    dev = _device(x, row_index, row_weight, *(t for o in (out, out_t) if o is not None for t in (o.data, o.scale)))
+    with _on(dev, stream) as on:
+        def make(r, c):
+            if on.raw:
+                raise ValueError("with a raw stream handle the outputs must be given")
+            return fp8_empty(r, c, fmt, dev, batch)
+        q = None if transposed == "only" else out if out is not None else make(rows, cols)
+        qt = None if transposed == "no" else out_t if out_t is not None else make(cols, rows)
+        for o in (q, qt):
+            if o is not None and o.format != fmt:
+                raise ValueError(f"outputs are {o.format}, the call asks for {fmt}")
+        src = Fp8Source(ptr, bs, ld, 1 if batch is None else batch, x.shape[-2], cols, _dtype_code(x), row_div,
+                        _ptr(row_index), rows, _ptr(row_weight), 0 if row_weight is None else row_weight.numel())
+        _check(load().muon_fp8_quantize(ctypes.byref(src), int(bool(blocks)),
+                                        None if q is None else ctypes.byref(q._c()),
+                                        None if qt is None else ctypes.byref(qt._c()), on.handle))
+    return (q, qt) if transposed == "both" else qt if transposed == "only" else q
+
+
+def _result(out, shape, on, out_dtype, accumulate):
+    """(tensor, muon_fp8_result_t) of a product's result."""
+    torch = _torch()
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = on.fresh(*shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+    elif tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, the call asks for {out_dtype}")
+    ptr, ld, bs = _last_dense(out, "out")
+    return out, Fp8Result(ptr, bs, ld, _dtype_code(out), int(bool(accumulate)))
+
+
+def _int32(t, n, name):
+    torch = _torch()
+    if t.dtype != torch.int32 or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be int32" + ("" if n is None else f" with {n} elements"))
+
+
+def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=None, accumulate: bool = False, offsets=None, stream=None):
+    """a b^T (muon_fp8_matmul): [M, N] of a [M, K] and b [N, K], or batches of them.
+    With `offsets` (int32, groups + 1) rows offsets[g] .. offsets[g + 1] of a meet
+    matrix g of b [groups, N, K]; rows outside every group are not written.
+    out: a tensor or view to write into (e.g. a matrix of the packed gradients),
+    else a new one of out_dtype (bfloat16). accumulate adds to out."""
+    if offsets is not None:
+        if b.data.dim() != 3 or a.data.dim() != 2:
+            raise ValueError("a grouped product takes one matrix a and a batch b")
+        _int32(offsets, b.data.shape[0] + 1, "offsets")
+        shape = (a.rows, b.rows)
+    else:
+        if a.data.dim() != b.data.dim():
+            raise ValueError("a and b must both be single matrices or both be batches")
+        shape = tuple(a.data.shape[:-1]) + (b.rows,)
+    dev = _device(a.data, a.scale, b.data, b.scale, out, offsets)
+    lib = load()
+    with _on(dev, stream) as on:
+        ca, cb = a._c(), b._c()
+        need = ctypes.c_size_t(0)
+        _check(lib.muon_fp8_matmul_workspace_size(ctypes.byref(ca), ctypes.byref(cb), int(offsets is not None),
+                                                  ctypes.byref(need)))
+        out, c = _result(out, shape, on, out_dtype, accumulate)
+        ws = on.scratch(need.value)
+        _check(lib.muon_fp8_matmul(ctypes.byref(ca), ctypes.byref(cb), _ptr(offsets), ctypes.byref(c), _ptr(ws),
+                                   0 if ws is None else ws.numel(), on.handle))
+    return out
+
+
+def fp8_matmul_grouped_k(a: Fp8, b: Fp8, offsets, out=None, out_dtype=None, accumulate: bool = False, stream=None):
+    """Grouped contractions (muon_fp8_matmul_grouped_k): out[g] = the product of
+    columns offsets[g] .. offsets[g + 1] of a [M, K] and b [N, K], each offset a
+    multiple of 128: [groups, M, N]."""
+    _int32(offsets, None, "offsets")
+    groups = offsets.numel() - 1
+    if groups < 0 or a.data.dim() != 2 or b.data.dim() != 2:
+        raise ValueError("a grouped contraction takes single matrices and groups + 1 offsets")
+    dev = _device(a.data, a.scale, b.data, b.scale, out, offsets)
+    with _on(dev, stream) as on:
+        out, c = _result(out, (groups, a.rows, b.rows), on, out_dtype, accumulate)
+        _check(load().muon_fp8_matmul_grouped_k(ctypes.byref(a._c()), ctypes.byref(b._c()), _ptr(offsets), groups,
+                                                ctypes.byref(c), on.handle))
+    return out
+
+
+def route_hyper(**kw) -> RouteHyper:
+    """Router hyperparameters: the library defaults, then keyword overrides (score:
+    "softmax" | "sigmoid", top_k, n_groups, top_groups, group_top, renormalize, scale)."""
+    h = RouteHyper()
+    load().muon_default_route_hyper(ctypes.byref(h))
+    for k, v in kw.items():
+        if k == "score" and isinstance(v, str):
+            v = ROUTE_SCORES.get(v, -1)
+        if not hasattr(h, k) or k == "reserved":
+            raise TypeError(f"unknown router hyperparameter {k!r}")
+        setattr(h, k, v)
+    return h
+
+
+def _logits(t):
+    if t.dim() != 2:
+        raise ValueError("logits must be [tokens, experts]")
+    return _last_dense(t, "logits")
+
+
+def _given(t, shape, dtype, on, name):
+    if t is None:
+        return on.fresh(*shape, dtype=dtype)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
+    return t
+
+
+def route(logits, h: RouteHyper, bias=None, ids=None, weights=None, stream=None):
+    """Route rows to experts (muon_route): (ids int32, weights float32), both [tokens, top_k]."""
+    torch = _torch()
+    ptr, ld, _ = _logits(logits)
+    tokens, experts = logits.shape
+    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != experts):
+        raise ValueError("bias must be float32 with one element per expert")
+    dev = _device(logits, bias, ids, weights)
+    with _on(dev, stream) as on:
+        k = max(h.top_k, 0)
+        ids = _given(ids, (tokens, k), torch.int32, on, "ids")
+        weights = _given(weights, (tokens, k), torch.float32, on, "weights")
+        _check(load().muon_route(ptr, _dtype_code(logits), tokens, experts, ld, _ptr(bias), ctypes.byref(h), _ptr(ids),
+                                 _ptr(weights), on.handle))
+    return ids, weights
+
+
+def route_backward(dweights, logits, ids, h: RouteHyper, dlogits=None, stream=None):
+    """Gradient of route's weights with respect to the logits (muon_route_backward)."""
+    torch = _torch()
+    ptr, ld, _ = _logits(logits)
+    tokens, experts = logits.shape
+    if dweights.dtype != torch.float32 or tuple(dweights.shape) != (tokens, h.top_k):
+        raise ValueError(f"dweights must be float32 of shape {(tokens, h.top_k)}")
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (tokens, h.top_k):
+        raise ValueError(f"ids must be int32 of shape {(tokens, h.top_k)}")
+    dev = _device(dweights, logits, ids, dlogits)
+    with _on(dev, stream) as on:
+        dlogits = _given(dlogits, (tokens, experts), logits.dtype, on, "dlogits")
+        dptr, ldd, _ = _last_dense(dlogits, "dlogits")
+        _check(load().muon_route_backward(_ptr(dweights), ptr, _dtype_code(logits), tokens, experts, ld, _ptr(ids),
+                                          ctypes.byref(h), dptr, ldd, on.handle))
+    return dlogits
+
+
+def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=None, rows=None, pos=None, stream=None):
+    """Order of routed slots by expert (muon_expert_order): (offsets [experts + 1],
+    counts [experts], rows [capacity], pos like ids), all int32. The capacity
+    that any routing fits is ids.numel() + n_experts * (align - 1)."""
+    torch = _torch()
+    _int32(ids, None, "ids")
+    n = ids.numel()
+    dev = _device(ids, offsets, counts, rows, pos)
+    lib = load()
+    with _on(dev, stream) as on:
+        need = ctypes.c_size_t(0)
+        _check(lib.muon_expert_order_workspace_size(n, n_experts, ctypes.byref(need)))
+        offsets = _given(offsets, (n_experts + 1,), torch.int32, on, "offsets")
+        counts = _given(counts, (n_experts,), torch.int32, on, "counts")
+        if rows is None:
+            rows = on.fresh(max(n + n_experts * (align - 1), 0), dtype=torch.int32)
+        else:
+            _int32(rows, None, "rows")
+        pos = _given(pos, ids.shape, torch.int32, on, "pos")
+        ws = on.scratch(need.value)
+        _check(lib.muon_expert_order(_ptr(ids), n, n_experts, align, _ptr(offsets), _ptr(counts), _ptr(rows),
+                                     rows.numel(), _ptr(pos), _ptr(ws), 0 if ws is None else ws.numel(), on.handle))
+    return offsets, counts, rows, pos
+
+
+def _slots(o_or_dy, pos, weights):
+    torch = _torch()
+    if pos.dim() != 2 or pos.dtype != torch.int32:
+        raise ValueError("pos must be int32 [tokens, top_k]")
+    if weights.dtype != torch.float32 or weights.shape != pos.shape:
+        raise ValueError("weights must be float32 with pos's shape")
+    if o_or_dy.dim() != 2:
+        raise ValueError("expected a matrix of rows")
+
+
+def combine(o, pos, weights, out=None, stream=None):
+    """Weighted sum of each token's expert rows (muon_combine): [tokens, cols] of
+    o [rows, cols], pos and weights [tokens, top_k]."""
+    _slots(o, pos, weights)
+    optr, ldo, _ = _last_dense(o, "o")
+    tokens, k = pos.shape
+    dev = _device(o, pos, weights, out)
+    with _on(dev, stream) as on:
+        out = _given(out, (tokens, o.shape[1]), o.dtype, on, "out")
+        yptr, ldy, _ = _last_dense(out, "out")
+        _check(load().muon_combine(optr, _dtype_code(o), o.shape[0], o.shape[1], ldo, _ptr(pos), _ptr(weights), tokens,
+                                   k, yptr, ldy, on.handle))
+    return out
+
+
+def combine_backward(dy, o, pos, weights, dweights=None, do=None, stream=None):
+    """Gradients of combine (muon_combine_backward): (dweights, do). Rows of `do` that
+    no slot points at are not written (zeros in a new one)."""
+    torch = _torch()
+    _slots(dy, pos, weights)
+    if o.dim() != 2 or dy.dtype != o.dtype or tuple(dy.shape) != (pos.shape[0], o.shape[1]):
+        raise ValueError("dy must be [tokens, cols] with o's dtype")
+    tokens, k = pos.shape
+    dyptr, lddy, _ = _last_dense(dy, "dy")
+    optr, ldo, _ = _last_dense(o, "o")
+    dev = _device(dy, o, pos, weights, dweights, do)
+    with _on(dev, stream) as on:
+        dweights = _given(dweights, (tokens, k), torch.float32, on, "dweights")
+        do = on.fresh(*o.shape, dtype=o.dtype).zero_() if do is None else _given(do, o.shape, o.dtype, on, "do")
+        doptr, lddo, _ = _last_dense(do, "do")
+        _check(load().muon_combine_backward(dyptr, _dtype_code(dy), tokens, o.shape[1], lddy, optr, o.shape[0], ldo,
+                                            _ptr(pos), _ptr(weights), k, _ptr(dweights), doptr, lddo, on.handle))
+    return dweights, do

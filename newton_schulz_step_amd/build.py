@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuonstep.so")
 
-SOURCES = ["capi.hip", "plan.cpp", "planner.cpp", "gemm.hip", "elementwise.hip"]
+SOURCES = ["capi.hip", "capi_moe.hip", "plan.cpp", "planner.cpp", "gemm.hip", "elementwise.hip", "fp8.hip",
+           "fp8_gemm.hip", "moe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "capi_util.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 #include "plan.hpp"
@@ -21,10 +22,12 @@ namespace muon {
 
 static thread_local std::string g_err;
 
-static int fail(int code, const std::string& msg) {
+int fail(int code, const std::string& msg) {
   g_err = msg;
   return code;
 }
+
+void clear_error() { g_err.clear(); }
 
 // ---------------------------------------------------------------------------
 // kernel timing (measurement hooks)
@@ -38,21 +41,22 @@ static std::mutex g_prof_mu;
 static std::atomic<bool> g_prof_active{false};
 static std::vector<ProfRec> g_prof;
 
-template <typename F>
-static hipError_t timed(const char* kind, hipStream_t s, F&& launch) {
-  if (!g_prof_active.load(std::memory_order_acquire)) return launch();
-  hipEvent_t a = nullptr, b = nullptr;
-  if (hipEventCreate(&a) != hipSuccess) return hipErrorOutOfMemory;
-  if (hipEventCreate(&b) != hipSuccess) {
-    (void)hipEventDestroy(a);
+bool prof_active() { return g_prof_active.load(std::memory_order_acquire); }
+
+hipError_t prof_open(hipStream_t s, hipEvent_t* a, hipEvent_t* b) {
+  if (hipEventCreate(a) != hipSuccess) return hipErrorOutOfMemory;
+  if (hipEventCreate(b) != hipSuccess) {
+    (void)hipEventDestroy(*a);
     return hipErrorOutOfMemory;
   }
-  (void)hipEventRecord(a, s);
-  const hipError_t r = launch();
+  (void)hipEventRecord(*a, s);
+  return hipSuccess;
+}
+
+void prof_close(const char* kind, hipStream_t s, hipEvent_t a, hipEvent_t b) {
   (void)hipEventRecord(b, s);
   std::lock_guard<std::mutex> lk(g_prof_mu);
   g_prof.push_back({kind, a, b});
-  return r;
 }
 
 // A set of shape groups that share the tile edge; each NS product is one launch
@@ -131,31 +135,6 @@ static int get_plan(const muon_matrix_t* t, const muon_window_t* w, int32_t n, c
 
 // ---------------------------------------------------------------------------
 // helpers
-
-static bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
-struct Span {
-  const char* lo;
-  const char* hi;
-  const char* name;
-};
-
-static bool overlapping(const std::vector<Span>& v, std::string& which) {
-  for (size_t i = 0; i < v.size(); ++i)
-    for (size_t j = i + 1; j < v.size(); ++j)
-      if (v[i].lo < v[j].hi && v[j].lo < v[i].hi) {
-        which = std::string(v[i].name) + " and " + v[j].name;
-        return true;
-      }
-  return false;
-}
-
-#define MUON_LAUNCH(kind, stream, expr)                                                        \
-  do {                                                                                         \
-    const hipError_t _e = timed(kind, stream, [&]() { return (expr); });                      \
-    if (_e != hipSuccess)                                                                      \
-      return fail(MUON_ERR_HIP, std::string(kind) + " launch failed: " + hipGetErrorString(_e)); \
-  } while (0)
 
 static float gram_scale(int64_t m) {
   int e = 0;

@@ -1,0 +1,536 @@
+// Routing of rows to experts, the order of routed rows, and the weighted sum of the
+// experts' outputs (gfx950).
+#include "common.hpp"
+#include "fp8.hpp"
+
+namespace muon {
+
+template <int DT> __device__ __forceinline__ float load1(const void* p, int64_t i) { return grad_to_f32<DT>(p, i); }
+template <int DT> __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
+  if constexpr (DT == MUON_DTYPE_F32) static_cast<float*>(p)[i] = v;
+  else if constexpr (DT == MUON_DTYPE_BF16) static_cast<__bf16*>(p)[i] = static_cast<__bf16>(v);
+  else static_cast<_Float16*>(p)[i] = static_cast<_Float16>(v);
+}
+
+__device__ __forceinline__ double wave_max_d(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Routing: one wave per token, expert 64 i + lane in register i of a lane.
+//
+// Scores and keys are held in 64 bits: which experts a token gets is then the same
+// wherever it is computed in 64 bits, while 32-bit exponentials of different libraries
+// would order near neighbours differently.
+
+constexpr double kNone = -__builtin_huge_val();      // not available
+constexpr double kLowest = -1.7976931348623157e308;  // a NaN key: below every number
+
+// One softmax or sigmoid score per register; -inf logits score 0, a row of them too.
+template <int V>
+__device__ __forceinline__ void row_scores(const float (&l)[V], int score, double (&s)[V]) {
+  if (score == MUON_ROUTE_SOFTMAX) {
+    double m = kNone;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      m = fmax(m, static_cast<double>(l[i]));   // ignores NaN
+      nan = nan || l[i] != l[i];
+    }
+    m = wave_max_d(m);
+    nan = __any(nan);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s[i] = l[i] == -__builtin_huge_valf() ? 0.0 : exp(static_cast<double>(l[i]) - m);
+      sum += s[i];
+    }
+    sum = wave_sum_d(sum);
+    if (nan) sum = __builtin_nan("");
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = l[i] == -__builtin_huge_valf() ? 0.0 : s[i] / sum;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
+  }
+}
+
+// The lane-wise best (key, index) of the wave: largest key, ties to the lower index.
+__device__ __forceinline__ void wave_best(double& k, int& i) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const double ko = __shfl_xor(k, o, 64);
+    const int io = __shfl_xor(i, o, 64);
+    if (ko > k || (ko == k && io < i)) {
+      k = ko;
+      i = io;
+    }
+  }
+}
+
+template <int DT, int V>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  extern __shared__ double keys[];   // 4 x experts, where there are groups
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  if (token >= a.tokens) return;     // no barrier below: a wave is by itself
+  const int E = a.experts;
+  float l[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = i * 64 + lane;
+    l[i] = e < E ? load1<DT>(a.logits, token * a.ld + e) : -__builtin_huge_valf();
+  }
+  double s[V], key[V];
+  row_scores<V>(l, a.score, s);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = i * 64 + lane;
+    key[i] = s[i];
+    if (a.bias != nullptr && e < E) key[i] += static_cast<double>(a.bias[e]);
+    if (key[i] != key[i]) key[i] = kLowest;
+    if (e >= E || l[i] == -__builtin_huge_valf()) key[i] = kNone;
+  }
+  if (a.n_groups > 1) {
+    double* mine = keys + wave * E;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i * 64 + lane < E) mine[i * 64 + lane] = key[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    // lane g scores group g
+    const int per = E / a.n_groups;
+    double gk = kNone;
+    if (lane < a.n_groups) {
+      double t1 = kNone, t2 = kNone;
+      for (int j = 0; j < per; ++j) {
+        const double k = mine[lane * per + j];
+        if (k > t1) {
+          t2 = t1;
+          t1 = k;
+        } else if (k > t2) {
+          t2 = k;
+        }
+      }
+      gk = t1;
+      if (a.group_top > 1 && t2 > kNone) gk = t1 <= kLowest ? t1 : (t2 <= kLowest ? kLowest : t1 + t2);
+    }
+    unsigned long long kept = 0;
+    for (int j = 0; j < a.top_groups; ++j) {
+      double k = gk;
+      int g = lane;
+      wave_best(k, g);
+      if (k == kNone) break;
+      kept |= 1ull << g;
+      if (lane == g) gk = kNone;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 64 + lane;
+      if (e < E && !((kept >> (e / per)) & 1)) key[i] = kNone;
+    }
+  }
+  int my_id = -1;
+  double my_s = 0.0;
+  for (int j = 0; j < a.top_k; ++j) {
+    double k = kNone;
+    int e = lane;
+    double sc = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] > k) {
+        k = key[i];
+        e = i * 64 + lane;
+        sc = s[i];
+      }
+    const int own = e;
+    wave_best(k, e);
+    if (k == kNone) break;
+    sc = __shfl(sc, e & 63, 64);
+    if (lane == j) {
+      my_id = e;
+      my_s = sc;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (own == e && i * 64 + lane == e) key[i] = kNone;
+  }
+  double f = static_cast<double>(a.scale);
+  if (a.renormalize) f /= wave_sum_d(my_s) + 1e-20;
+  if (lane < a.top_k) {
+    a.ids[token * a.top_k + lane] = my_id;
+    a.weights[token * a.top_k + lane] = my_id < 0 ? 0.0f : static_cast<float>(my_s * f);
+  }
+}
+
+// The gradient: with T = sum of the chosen s + 1e-20 and w_j = scale s_j / T,
+//   ds_j = (scale dw_j - sum_i dw_i w_i) / T     (scale dw_j without renormalisation)
+//   sigmoid: dl_j = ds_j s_j (1 - s_j);  softmax: dl_i = s_i (ds_i - sum_j ds_j s_j).
+// The chosen slots' values are scattered to their experts' registers by a search over
+// the slots (at most 32), one broadcast each.
+template <int DT, int V>
+__global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  if (token >= a.tokens) return;
+  const int E = a.experts;
+  float l[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = i * 64 + lane;
+    l[i] = e < E ? load1<DT>(a.logits, token * a.ld + e) : -__builtin_huge_valf();
+  }
+  double s[V], ds[V];
+  row_scores<V>(l, a.score, s);
+  int id = -1;
+  double dw = 0.0;
+  if (lane < a.top_k) {
+    id = a.ids[token * a.top_k + lane];
+    if (id < 0 || id >= E) id = -1;
+    else dw = static_cast<double>(a.dweights[token * a.top_k + lane]);
+  }
+  bool hit[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    ds[i] = 0.0;
+    hit[i] = false;
+  }
+  double total = 0.0, dot = 0.0;
+  for (int j = 0; j < a.top_k; ++j) {
+    const int e = __shfl(id, j, 64);
+    const double d = __shfl(dw, j, 64);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e == i * 64 + lane) {
+        ds[i] = d;
+        hit[i] = true;
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (hit[i]) {
+      total += s[i];
+      dot += ds[i] * s[i];
+    }
+  total = wave_sum_d(total) + 1e-20;
+  dot = wave_sum_d(dot);
+  const double f = static_cast<double>(a.scale);
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (hit[i]) ds[i] = a.renormalize ? f * (ds[i] - dot / total) / total : f * ds[i];
+    sum += hit[i] ? ds[i] * s[i] : 0.0;
+  }
+  if (a.score == MUON_ROUTE_SOFTMAX) sum = wave_sum_d(sum);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = i * 64 + lane;
+    double d;
+    if (a.score == MUON_ROUTE_SOFTMAX) d = s[i] * (ds[i] - sum);
+    else d = hit[i] ? ds[i] * s[i] * (1.0 - s[i]) : 0.0;
+    if (l[i] == -__builtin_huge_valf()) d = 0.0;
+    if (e < E) store1<DT>(a.dlogits, token * a.ld_d + e, static_cast<float>(d));
+  }
+}
+
+template <int DT>
+static hipError_t route_dt(const RouteArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.tokens + 3) / 4));
+  const size_t lds = a.n_groups > 1 ? 4 * sizeof(double) * a.experts : 0;
+  if (a.experts <= 64) hipLaunchKernelGGL((route_kernel<DT, 1>), grid, dim3(256), lds, s, a);
+  else if (a.experts <= 128) hipLaunchKernelGGL((route_kernel<DT, 2>), grid, dim3(256), lds, s, a);
+  else if (a.experts <= 256) hipLaunchKernelGGL((route_kernel<DT, 4>), grid, dim3(256), lds, s, a);
+  else hipLaunchKernelGGL((route_kernel<DT, 16>), grid, dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_route(int dtype, const RouteArgs& a, hipStream_t s) {
+  if (a.tokens <= 0) return hipSuccess;
+  if (dtype == MUON_DTYPE_BF16) return route_dt<MUON_DTYPE_BF16>(a, s);
+  if (dtype == MUON_DTYPE_F16) return route_dt<MUON_DTYPE_F16>(a, s);
+  return route_dt<MUON_DTYPE_F32>(a, s);
+}
+
+template <int DT>
+static hipError_t route_backward_dt(const RouteBackArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.tokens + 3) / 4));
+  if (a.experts <= 64) hipLaunchKernelGGL((route_backward_kernel<DT, 1>), grid, dim3(256), 0, s, a);
+  else if (a.experts <= 128) hipLaunchKernelGGL((route_backward_kernel<DT, 2>), grid, dim3(256), 0, s, a);
+  else if (a.experts <= 256) hipLaunchKernelGGL((route_backward_kernel<DT, 4>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((route_backward_kernel<DT, 16>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_route_backward(int dtype, const RouteBackArgs& a, hipStream_t s) {
+  if (a.tokens <= 0) return hipSuccess;
+  if (dtype == MUON_DTYPE_BF16) return route_backward_dt<MUON_DTYPE_BF16>(a, s);
+  if (dtype == MUON_DTYPE_F16) return route_backward_dt<MUON_DTYPE_F16>(a, s);
+  return route_backward_dt<MUON_DTYPE_F32>(a, s);
+}
+
+// ---------------------------------------------------------------------------
+// Expert order: a stable counting sort. Block b owns slots [b P, (b + 1) P). The first
+// launch counts each block's slots per expert; in the second every block sums the
+// counts of all blocks (the padded offsets) and of the blocks before it (its first row
+// of each expert), then places its slots in order. Small inputs take one block and one
+// launch. Counting uses integer LDS atomics, whose order does not matter; placing ranks
+// the 64 slots of a wave step with ballots, so rows come out in slot order.
+constexpr int kOrderThreads = 512, kOrderWaves = kOrderThreads / 64;
+constexpr int64_t kOrderBlock = 1024;   // slots of a block, unless that makes too many blocks
+constexpr int32_t kOrderBlocks = 256;
+
+int32_t order_blocks(int64_t n) {
+  if (n <= 4 * kOrderBlock) return 1;
+  return static_cast<int32_t>(std::min<int64_t>((n + kOrderBlock - 1) / kOrderBlock, kOrderBlocks));
+}
+
+__device__ __forceinline__ int slot_expert(const OrderArgs& a, int64_t i) {
+  const int e = a.ids[i];
+  return e >= 0 && e < a.experts ? e : -1;
+}
+
+__global__ __launch_bounds__(kOrderThreads) void order_hist_kernel(OrderArgs a) {
+  __shared__ int h[MUON_ROUTE_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < a.experts; e += kOrderThreads) h[e] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kOrderThreads) {
+    const int e = slot_expert(a, i);
+    if (e >= 0) atomicAdd(&h[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kOrderThreads)
+    a.hist[static_cast<int64_t>(blockIdx.x) * a.experts + e] = h[e];
+}
+
+__global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a) {
+  __shared__ int total[MUON_ROUTE_MAX_EXPERTS];              // slots of each expert
+  __shared__ int next[kOrderWaves][MUON_ROUTE_MAX_EXPERTS];  // next row of each expert, per wave
+  __shared__ int scan[kOrderWaves];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int E = a.experts;
+  const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
+  // each wave places a contiguous part of the block's slots
+  const int64_t part = ((hi - lo + kOrderWaves - 1) / kOrderWaves + 63) / 64 * 64;
+  const int64_t wlo = min(hi, lo + wave * part), whi = min(hi, wlo + part);
+  for (int e = t; e < E; e += kOrderThreads)
+    for (int w = 0; w < kOrderWaves; ++w) next[w][e] = 0;
+  __syncthreads();
+  for (int64_t i = wlo + lane; i < whi; i += 64) {
+    const int e = slot_expert(a, i);
+    if (e >= 0) atomicAdd(&next[wave][e], 1);
+  }
+  __syncthreads();
+  // totals, slots before this block and before each wave
+  for (int e = t; e < E; e += kOrderThreads) {
+    int all = 0, before = 0;
+    if (a.blocks > 1) {
+      for (int b = 0; b < a.blocks; ++b) {
+        const int c = a.hist[static_cast<int64_t>(b) * E + e];
+        if (b < static_cast<int>(blockIdx.x)) before += c;
+        all += c;
+      }
+    } else {
+      for (int w = 0; w < kOrderWaves; ++w) all += next[w][e];
+    }
+    total[e] = all;
+    for (int w = 0; w < kOrderWaves; ++w) {
+      const int c = next[w][e];
+      next[w][e] = before;
+      before += c;
+    }
+  }
+  __syncthreads();
+  // padded offsets: exclusive scan over the experts, kOrderThreads at a time
+  int64_t base = 0;
+  for (int e0 = 0; e0 < E; e0 += kOrderThreads) {
+    const int e = e0 + t;
+    const int n = e < E ? (total[e] + a.align - 1) / a.align * a.align : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 63) scan[wave] = incl;
+    __syncthreads();
+    int64_t first = base + incl - n;
+    int64_t sum = 0;
+    for (int w = 0; w < kOrderWaves; ++w) {
+      if (w < wave) first += scan[w];
+      sum += scan[w];
+    }
+    if (e < E) {
+      for (int w = 0; w < kOrderWaves; ++w) next[w][e] += static_cast<int>(first);
+      if (blockIdx.x == 0) {
+        a.offsets[e] = static_cast<int>(first);
+        a.counts[e] = total[e];
+      }
+      // the expert's padding rows
+      if (e % a.blocks == static_cast<int>(blockIdx.x))
+        for (int r = total[e]; r < n; ++r) a.rows[first + r] = -1;
+    }
+    base += sum;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && t == 0) a.offsets[E] = static_cast<int>(base);
+  for (int64_t r = base + static_cast<int64_t>(blockIdx.x) * kOrderThreads + t; r < a.capacity;
+       r += static_cast<int64_t>(a.blocks) * kOrderThreads)
+    a.rows[r] = -1;
+  // placing, 64 slots of the wave at a time
+  for (int64_t i0 = wlo; i0 < whi; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const int e = i < whi ? slot_expert(a, i) : -1;
+    unsigned long long same = __ballot(e >= 0);
+    for (int bit = 0; (1 << bit) < E; ++bit) {
+      const unsigned long long m = __ballot((e >> bit) & 1);
+      same &= ((e >> bit) & 1) ? m : ~m;
+    }
+    int row = -1;
+    if (e >= 0) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      row = next[wave][e] + rank;
+      a.rows[row] = static_cast<int>(i);
+    }
+    if (i < whi) a.pos[i] = row;
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0 && (same >> lane) == 1ull) next[wave][e] = row + 1;   // the last of its expert
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+hipError_t launch_order_hist(const OrderArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(order_hist_kernel, dim3(a.blocks), dim3(kOrderThreads), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_order_place(const OrderArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(order_place_kernel, dim3(a.blocks), dim3(kOrderThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Combination: one workgroup per token, eight columns per thread and pass.
+
+template <int DT>
+__device__ __forceinline__ void read8(const void* p, int64_t i, int n, bool vec, float (&v)[8]) {
+  if (vec && n == 8) {
+    if constexpr (DT == MUON_DTYPE_F32) {
+      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+      const f32x4 a = q[0], b = q[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+    } else {
+      const u16x8 u = *reinterpret_cast<const u16x8*>(static_cast<const unsigned short*>(p) + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = DT == MUON_DTYPE_BF16 ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < n ? load1<DT>(p, i + e) : 0.0f;
+}
+
+template <int DT>
+__device__ __forceinline__ void write8(void* p, int64_t i, int n, bool vec, const float (&v)[8]) {
+  if (vec && n == 8) {
+    if constexpr (DT == MUON_DTYPE_F32) {
+      f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+      q[0] = f32x4{v[0], v[1], v[2], v[3]};
+      q[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      using T = std::conditional_t<DT == MUON_DTYPE_BF16, __bf16, _Float16>;
+      T o[8];
+      rne<T, 8>(v, o);
+      u16x8 u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = __builtin_bit_cast(unsigned short, o[e]);
+      *reinterpret_cast<u16x8*>(static_cast<unsigned short*>(p) + i) = u;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) store1<DT>(p, i + e, v[e]);
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+  const int64_t t = blockIdx.x;
+  const int32_t* pos = a.pos + t * a.top_k;
+  const float* w = a.weights + t * a.top_k;
+  for (int64_t c = threadIdx.x * 8; c < a.cols; c += 256 * 8) {
+    const int n = static_cast<int>(min<int64_t>(8, a.cols - c));
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+    for (int j = 0; j < a.top_k; ++j) {
+      const int r = pos[j];
+      if (r < 0 || r >= a.o_rows) continue;
+      float v[8];
+      read8<DT>(a.o, r * a.ld_o + c, n, a.vec != 0, v);
+      const float wj = w[j];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] += wj * v[e];
+    }
+    write8<DT>(a.y, t * a.ld_y + c, n, a.vec != 0, y);
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void combine_backward_kernel(CombineArgs a) {
+  __shared__ float red[4];
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int j = 0; j < a.top_k; ++j) {
+    const int r = a.pos[t * a.top_k + j];
+    const bool has = r >= 0 && r < a.o_rows;
+    float sum = 0.0f;
+    if (has) {
+      const float wj = a.weights[t * a.top_k + j];
+      for (int64_t c = threadIdx.x * 8; c < a.cols; c += 256 * 8) {
+        const int n = static_cast<int>(min<int64_t>(8, a.cols - c));
+        float d[8];
+        read8<DT>(a.dy, t * a.ld_dy + c, n, a.vec != 0, d);
+        if (a.dweights != nullptr) {
+          float v[8];
+          read8<DT>(a.o, r * a.ld_o + c, n, a.vec != 0, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum += d[e] * v[e];
+        }
+        if (a.d_o != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] *= wj;
+          write8<DT>(a.d_o, r * a.ld_do + c, n, a.vec != 0, d);
+        }
+      }
+    }
+    if (a.dweights != nullptr) {
+      sum = wave_sum(sum);
+      if (lane == 0) red[wave] = sum;
+      __syncthreads();
+      if (threadIdx.x == 0) a.dweights[t * a.top_k + j] = has ? (red[0] + red[1]) + (red[2] + red[3]) : 0.0f;
+      __syncthreads();
+    }
+  }
+}
+
+#define MUON_BY_DTYPE(kernel, grid, a)                                                                      \
+  do {                                                                                                      \
+    if (dtype == MUON_DTYPE_BF16) hipLaunchKernelGGL((kernel<MUON_DTYPE_BF16>), grid, dim3(256), 0, s, a);  \
+    else if (dtype == MUON_DTYPE_F16) hipLaunchKernelGGL((kernel<MUON_DTYPE_F16>), grid, dim3(256), 0, s, a); \
+    else hipLaunchKernelGGL((kernel<MUON_DTYPE_F32>), grid, dim3(256), 0, s, a);                            \
+  } while (0)
+
+hipError_t launch_combine(int dtype, const CombineArgs& a, hipStream_t s) {
+  if (a.tokens <= 0 || a.cols <= 0) return hipSuccess;
+  MUON_BY_DTYPE(combine_kernel, dim3(static_cast<unsigned>(a.tokens)), a);
+  return hipGetLastError();
+}
+hipError_t launch_combine_backward(int dtype, const CombineArgs& a, hipStream_t s) {
+  if (a.tokens <= 0) return hipSuccess;
+  MUON_BY_DTYPE(combine_backward_kernel, dim3(static_cast<unsigned>(a.tokens)), a);
+  return hipGetLastError();
+}
+
+}  // namespace muon
