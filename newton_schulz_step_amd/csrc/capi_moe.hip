@@ -217,6 +217,8 @@ static Fp8Gemm gemm_of(const muon_fp8_t* a, const muon_fp8_t* b, const muon_fp8_
   g.ldc = c->ld;
   g.c_dtype = c->dtype;
   g.accumulate = c->accumulate != 0;
+  const int esz = element_size(c->dtype);
+  g.c_vec = !misaligned(c->data, 16) && (c->ld * esz) % 16 == 0 && (c->batch_stride * esz) % 16 == 0;
   g.splits = 1;
   return g;
 }

@@ -46,6 +46,7 @@ struct Fp8Gemm {
   void* c;
   int64_t c_batch, ldc;          // elements
   int32_t c_dtype, accumulate;
+  int32_t c_vec;                 // rows of 16-byte aligned groups of 8 results
   float* partial;                // splits x batch x M x N sums, where splits > 1
   int32_t splits;
 };

@@ -20,6 +20,9 @@
 // result the operands are converted to bf16 in registers, scale included (exact: 8-bit
 // values have at most 4 significant bits), and multiplied by the bf16 instructions,
 // whose sums keep 24 bits: 2e-7 of the norm, at half the rate.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.hpp"
 #include "fp8.hpp"
 
@@ -32,16 +35,16 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // Group of a row tile. Every wave of the workgroup finds it by itself: 64 groups at a
 // time, a prefix sum of their tile counts. Returns false for a tile beyond the last
 // group's.
-__device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups, int64_t limit, int tile_rows, int tile,
-                                           int& group, int64_t& first, int64_t& end) {
+__device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups, int limit, int tile_rows, int tile,
+                                           int& group, int& first, int& end) {
   const int lane = threadIdx.x & 63;
   int base = 0;
   for (int g0 = 0; g0 < n_groups; g0 += 64) {
     const int g = g0 + lane;
     int lo = 0, hi = 0;
     if (g < n_groups) {
-      lo = static_cast<int>(min<int64_t>(max(offsets[g], 0), limit));
-      hi = static_cast<int>(min<int64_t>(max(offsets[g + 1], lo), limit));
+      lo = min(max(offsets[g], 0), limit);
+      hi = min(max(offsets[g + 1], lo), limit);
     }
     const int n = (hi - lo + tile_rows - 1) / tile_rows;
     int incl = n;
@@ -50,15 +53,12 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups,
       const int up = __shfl_up(incl, o, 64);
       if (lane >= o) incl += up;
     }
-    const int total = __shfl(incl, 63, 64);
+    const int total = __builtin_amdgcn_readlane(incl, 63);
     if (tile < base + total) {
-      const unsigned long long past = __ballot(base + incl > tile);
-      const int l = __builtin_ctzll(past);
+      const int l = __builtin_ctzll(__ballot(base + incl > tile));
       group = g0 + l;
-      const int before = base + __shfl(incl - n, l, 64);
-      const int glo = __shfl(lo, l, 64), ghi = __shfl(hi, l, 64);
-      first = glo + static_cast<int64_t>(tile - before) * tile_rows;
-      end = ghi;
+      first = __builtin_amdgcn_readlane(lo, l) + (tile - base - __builtin_amdgcn_readlane(incl - n, l)) * tile_rows;
+      end = __builtin_amdgcn_readlane(hi, l);
       return true;
     }
     base += total;
@@ -66,10 +66,10 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups,
   return false;
 }
 
-// What a workgroup computes: rows [m0, mend) of A (a tile of them), matrix `mat` of B
-// and C, blocks [kb0, kb1) of the contraction.
+// What a workgroup computes (the same in all its lanes): rows [m0, mend) of A (a tile of
+// them), matrix `mat` of B and C, blocks [kb0, kb1) of the contraction.
 struct Work {
-  int64_t m0, mend;
+  int m0, mend;
   int mat, amat, bmat;
   int kb0, kb1;
 };
@@ -78,21 +78,20 @@ template <int TM>
 __device__ __forceinline__ bool find_work(const Fp8Gemm& g, int mtile, int z, Work& w) {
   w.kb0 = 0;
   w.kb1 = g.kb;
-  w.m0 = static_cast<int64_t>(mtile) * TM;
-  w.mend = g.M;
+  w.m0 = mtile * TM;
+  w.mend = static_cast<int>(g.M);
   w.mat = w.amat = w.bmat = z;
   if (g.mode == FP8_GROUP_ROWS) {
     w.amat = 0;
-    if (!find_group(g.offsets, g.batch, g.M, TM, mtile, w.mat, w.m0, w.mend)) return false;
-    w.mat = __builtin_amdgcn_readfirstlane(w.mat);
+    if (!find_group(g.offsets, g.batch, static_cast<int>(g.M), TM, mtile, w.mat, w.m0, w.mend)) return false;
     w.bmat = w.mat;
   } else if (g.mode == FP8_GROUP_K) {
     w.amat = w.bmat = 0;
-    const int64_t limit = static_cast<int64_t>(g.kb) * 128;
-    const int lo = static_cast<int>(min<int64_t>(max(g.offsets[z], 0), limit));
-    const int hi = static_cast<int>(min<int64_t>(max(g.offsets[z + 1], lo), limit));
-    w.kb0 = lo / 128;
-    w.kb1 = hi > lo ? (hi + 127) / 128 : w.kb0;
+    const int limit = g.kb * 128;
+    const int lo = min(max(g.offsets[z], 0), limit);
+    const int hi = min(max(g.offsets[z + 1], lo), limit);
+    w.kb0 = __builtin_amdgcn_readfirstlane(lo / 128);
+    w.kb1 = __builtin_amdgcn_readfirstlane(hi > lo ? (hi + 127) / 128 : lo / 128);
   }
   return true;
 }
@@ -218,32 +217,382 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
   }
 }
 
-Fp8Plan plan_fp8_gemm(int64_t, int64_t, int64_t, int32_t, int64_t, bool) { return {0, 1}; }
+// ---------------------------------------------------------------------------
+// Tiles: TILE x TILE outputs per workgroup (256 or 128), four waves in a 2 x 2 grid, each
+// owning (TILE / 2)^2 outputs as 32 x 32 blocks in registers.
+//
+// The contraction advances in periods of 64 bytes per row, one 32 x 32 x 64 instruction
+// per block pair. Slices of both operands go straight from memory to LDS (no registers)
+// into a ring of four: during period t a wave multiplies slice t from one set of
+// registers, reads slice t + 1 from LDS into the other set, and issues the loads of slice
+// t + 4 into the ring place of slice t, which every wave has read by then. A load thus has
+// two to three periods (256-tiles: 2000 to 3000 cycles) to arrive, and one barrier per
+// period publishes the next slice. Beyond the last slice the loads repeat it (in bounds,
+// never used), so that the number of loads in flight is the same everywhere.
+//
+// LDS rows of a slice are 64 bytes, four 16-byte chunks; chunk c of row r is stored at
+// place c ^ ((r / 2) % 4), so eight lanes that read one chunk of eight rows touch all
+// banks. A direct load writes consecutive lanes to consecutive places, so the lanes fetch
+// permuted chunks instead.
+//
+// The loop body is two blocks, four periods: the ring's places are then known at compile
+// time. An odd last block is paired with a repeated one whose scales are set to 2^-127,
+// 2^-254 together, which adds nothing (8-bit products are below 2^33).
+//
+// Scales: one word per row holds four blocks, also by direct loads, into a ring of four
+// words; a body takes its two bytes out of two neighbouring words (a group's contraction
+// may start anywhere in a word).
+//
+// Four waves of 128 x 128 read 32 KB of a 256-tile's slice per 1024 matrix cycles each:
+// 75% of the LDS rate with the writes. Smaller wave tiles would be bound by LDS.
 
-template <int FA, int FB>
-static hipError_t launch(const Fp8Plan&, const Fp8Gemm& g, hipStream_t s) {
-  const int64_t nt = (g.N + 15) / 16;
-  int64_t mt = (g.M + 15) / 16, z = g.batch;
-  if (g.mode == FP8_GROUP_ROWS) {
-    mt = std::min<int64_t>(g.M, g.M / 16 + g.batch);
+template <int V> using Int = std::integral_constant<int, V>;
+
+#define MUON_GLDS(rsrc, lds, size, voff, soff)                                                              \
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(lds), size, voff, soff, 0, 0)
+
+// 8 neighbouring results in one row, 16-byte aligned (WIDE: fp32 results).
+template <bool WIDE>
+__device__ __forceinline__ void store_row8(const Fp8Gemm& g, int64_t at, float (&v)[8]) {
+  if constexpr (WIDE) {
+    f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(g.c) + at);
+    f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    if (g.accumulate) {
+      a += p[0];
+      b += p[1];
+    }
+    p[0] = a;
+    p[1] = b;
+  } else {
+    u16x8* p = reinterpret_cast<u16x8*>(static_cast<unsigned short*>(g.c) + at);
+    if (g.accumulate) {
+      const u16x8 u = *p;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += g.c_dtype == MUON_DTYPE_BF16 ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
+    }
+    u16x8 u;
+    if (g.c_dtype == MUON_DTYPE_BF16) {
+      __bf16 o[8];
+      rne<__bf16, 8>(v, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = __builtin_bit_cast(unsigned short, o[e]);
+    } else {
+      _Float16 o[8];
+      rne<_Float16, 8>(v, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = __builtin_bit_cast(unsigned short, o[e]);
+    }
+    *p = u;
+  }
+}
+
+template <int FA, int FB, bool WIDE, int TILE>
+__device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int ntiles, int total) {
+  constexpr int HALF = TILE / 2, WB = HALF / 32;
+  constexpr int SLICE = TILE * 64;              // bytes of one operand's slice
+  constexpr int LOADS = TILE / 64;              // 1-KB loads per wave, operand and slice
+  __shared__ __align__(1024) char ring0[2 * SLICE], ring1[2 * SLICE], ring2[2 * SLICE], ring3[2 * SLICE];
+  __shared__ __align__(16) int words[4][2 * TILE];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+
+  // Workgroups are dealt round-robin over the eight XCDs. In every round of the chip each
+  // XCD takes consecutive tiles (its own last-level cache then sees neighbours), and all
+  // XCDs stay close together. Within a matrix, bands of four tile columns are walked row
+  // by row.
+  constexpr int ROUND = TILE == 256 ? 256 : 512;
+  const int chunk = blockIdx.x / ROUND, inside = blockIdx.x % ROUND;
+  const int size = min(ROUND, total - chunk * ROUND);
+  const int b = chunk * ROUND + (inside & 7) * (size / 8) + min(inside & 7, size % 8) + (inside >> 3);
+  const int per = mtiles * ntiles;
+  const int z = b / per;
+  const int rest = b - z * per;
+  const int band = rest / (4 * mtiles);
+  const int first = band * 4, width = min(4, ntiles - first);
+  const int in = rest - band * 4 * mtiles;
+  const int mt = in / width, nt = first + in % width;
+  Work w;
+  if (!find_work<TILE>(g, mt, z, w)) return;
+  const int64_t m0 = w.m0, n0 = static_cast<int64_t>(nt) * TILE;
+  const int mrows = static_cast<int>(min<int64_t>(TILE, w.mend - m0)), nrows = static_cast<int>(min<int64_t>(TILE, g.N - n0));
+
+  // resources of the tile's rows and per-lane offsets (rows beyond the tile repeat its last)
+  const int pitch = static_cast<int>(g.pitch), sp = static_cast<int>(g.s_pitch);
+  const uint8_t* pa = g.a + w.amat * g.a_batch + m0 * g.pitch;
+  const uint8_t* pb = g.b + w.bmat * g.b_batch + n0 * g.pitch;
+  const uint8_t* psa = g.sa + w.amat * g.sa_batch + m0 * g.s_pitch;
+  const uint8_t* psb = g.sb + w.bmat * g.sb_batch + n0 * g.s_pitch;
+  const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pa), 0, mrows * pitch, 0x00027000);
+  const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pb), 0, nrows * pitch, 0x00027000);
+  const auto rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(psa), 0, mrows * sp, 0x00027000);
+  const auto rsb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(psb), 0, nrows * sp, 0x00027000);
+  int va[LOADS], vb[LOADS];
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const int r = (wave * LOADS + i) * 16 + (lane >> 2);
+    const int c = ((lane & 3) ^ ((r >> 1) & 3)) * 16;
+    va[i] = min(r, mrows - 1) * pitch + c;
+    vb[i] = min(r, nrows - 1) * pitch + c;
+  }
+  const int nk = 2 * (w.kb1 - w.kb0);                   // periods
+  const int k0 = w.kb0 * 128;
+  const int qlast = (sp >> 2) - 1;                      // last scale word of a row
+  // scales, 64 rows per load: of a 256-tile each wave fetches 64 rows of both operands, of
+  // a 128-tile waves 0 and 1 rows of A, 2 and 3 of B
+  const bool sfirst = TILE == 256 || wave < 2;
+  const int srow = (TILE == 256 ? wave : wave & 1) * 64;
+  const int vs0 = min(srow + lane, (sfirst ? mrows : nrows) - 1) * sp;
+  const int vs1 = min(srow + lane, nrows - 1) * sp;
+
+  // per-lane read offsets within a slice: two neighbouring chunks of row lane % 32
+  const int r = lane & 31, h = lane >> 5;
+  const int chunk0 = ((2 * h) ^ ((r >> 1) & 3)) * 16;
+  const int ao = (wm * HALF + r) * 64 + chunk0, bo = SLICE + (wn * HALF + r) * 64 + chunk0;
+
+  f32x16 acc[WB][WB];
+#pragma unroll
+  for (int i = 0; i < WB; ++i)
+#pragma unroll
+    for (int j = 0; j < WB; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  auto load_slice = [&](char* to, int t) {
+    const int so = k0 + min(t, nk - 1) * 64;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) MUON_GLDS(ra, to + (wave * LOADS + i) * 1024, 16, va[i], so);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) MUON_GLDS(rb, to + SLICE + (wave * LOADS + i) * 1024, 16, vb[i], so);
+  };
+  auto load_word = [&](int q) {
+    const int so = min(q, qlast) * 4;
+    int* to = words[q & 3];
+    if (sfirst) MUON_GLDS(rsa, to + srow, 4, vs0, so);
+    else MUON_GLDS(rsb, to + TILE + srow, 4, vs0, so);
+    if constexpr (TILE == 256) MUON_GLDS(rsb, to + TILE + srow, 4, vs1, so);
+  };
+  i32x4 fa[2][WB][2], fb[2][WB][2];
+  auto read = [&](int set, const char* from) {
+#pragma unroll
+    for (int i = 0; i < WB; ++i) {
+      fa[set][i][0] = *reinterpret_cast<const i32x4*>(from + ao + i * 2048);
+      fa[set][i][1] = *reinterpret_cast<const i32x4*>(from + (ao ^ 16) + i * 2048);
+    }
+#pragma unroll
+    for (int i = 0; i < WB; ++i) {
+      fb[set][i][0] = *reinterpret_cast<const i32x4*>(from + bo + i * 2048);
+      fb[set][i][1] = *reinterpret_cast<const i32x4*>(from + (bo ^ 16) + i * 2048);
+    }
+  };
+  // scale bytes of blocks kb and kb + 1 of the lane's rows of A, then of B: the words are
+  // read a period before they are combined
+  int sc[2 * WB], lo[2 * WB], hi[2 * WB];
+  auto read_words = [&](int kb) {
+    const int* x = words[(kb >> 2) & 3];
+    const int* y = words[((kb >> 2) + 1) & 3];
+#pragma unroll
+    for (int i = 0; i < WB; ++i) {
+      lo[i] = x[wm * HALF + i * 32 + r];
+      hi[i] = y[wm * HALF + i * 32 + r];
+      lo[WB + i] = x[TILE + wn * HALF + i * 32 + r];
+      hi[WB + i] = y[TILE + wn * HALF + i * 32 + r];
+    }
+  };
+  auto set_scales = [&](int kb) {
+    const int mask = kb + 1 < w.kb1 ? 0xffff : 0xff;
+#pragma unroll
+    for (int i = 0; i < 2 * WB; ++i) sc[i] = static_cast<int>(__builtin_amdgcn_alignbyte(hi[i], lo[i], kb & 3)) & mask;
+  };
+  auto publish = [&]() {       // the slice after next may still be in flight, the next one is there
+    if constexpr (TILE == 256) asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  if (nk > 0) {
+    const int w0 = w.kb0 >> 2;
+    load_word(w0);
+    load_word(w0 + 1);
+    load_word(w0 + 2);
+    load_slice(ring0, 0);
+    load_slice(ring1, 1);
+    load_slice(ring2, 2);
+    load_slice(ring3, 3);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_words(w.kb0);
+    read(0, ring0);
+    set_scales(w.kb0);
+
+#define MUON_PERIOD(P, CUR, NEXT)                                                                          \
+  {                                                                                                        \
+    publish();                                                                                             \
+    if constexpr (P == 0) load_word((kb >> 2) + 3);                                                        \
+    if constexpr (P == 2) read_words(kb + 2);                                                              \
+    read((P & 1) ^ 1, NEXT);                                                                               \
+    load_slice(CUR, t + P + 4);                                                                            \
+    multiply(Int<P & 1>{}, Int<P / 2>{});                                                                  \
+    schedule();                                                                                            \
+  }
+    auto multiply = [&](auto set, auto byte) {
+      constexpr int SET = decltype(set)::value, U = decltype(byte)::value;
+      if constexpr (WIDE) {
+        float fs[2 * WB];
+#pragma unroll
+        for (int i = 0; i < 2 * WB; ++i) fs[i] = scale_value(sc[i], U);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          bf16x8 xa[WB], xb[WB];
+#pragma unroll
+          for (int i = 0; i < WB; ++i) {
+            xa[i] = to_bf16x8<FA>(fa[SET][i][s >> 1][2 * (s & 1)], fa[SET][i][s >> 1][2 * (s & 1) + 1], fs[i]);
+            xb[i] = to_bf16x8<FB>(fb[SET][i][s >> 1][2 * (s & 1)], fb[SET][i][s >> 1][2 * (s & 1) + 1], fs[WB + i]);
+          }
+#pragma unroll
+          for (int i = 0; i < WB; ++i)
+#pragma unroll
+            for (int j = 0; j < WB; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[j], xa[i], acc[i][j], 0, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < WB; ++i)
+#pragma unroll
+          for (int j = 0; j < WB; ++j) {
+            const i32x8 x = __builtin_shufflevector(fa[SET][i][0], fa[SET][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const i32x8 y = __builtin_shufflevector(fb[SET][j][0], fb[SET][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], FB, FA, U, sc[WB + j], U, sc[i]);
+          }
+      }
+    };
+    auto schedule = [&]() {
+      if constexpr (!WIDE) {
+#pragma unroll
+        for (int i = 0; i < 2 * LOADS; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);               // LDS reads
+          __builtin_amdgcn_sched_group_barrier(0x008, WB * WB / (2 * LOADS) > 1 ? 1 : 0, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);               // load to LDS
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int kb = w.kb0;
+    for (int t = 0; t < nk; t += 4, kb += 2) {
+      MUON_PERIOD(0, ring0, ring1)
+      MUON_PERIOD(1, ring1, ring2)
+      MUON_PERIOD(2, ring2, ring3)
+      MUON_PERIOD(3, ring3, ring0)
+      set_scales(kb + 2);
+    }
+#undef MUON_PERIOD
+    // the last loads land before the ring is used again
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+
+  // Results: 32 rows of a wave at a time through its own part of LDS, then whole rows,
+  // 16 bytes per lane where the rows are aligned for it.
+  constexpr int SP = HALF + 4;
+  float* stage = reinterpret_cast<float*>(wave == 0 ? ring0 : wave == 1 ? ring1 : wave == 2 ? ring2 : ring3);
+  static_assert(32 * SP * 4 <= 2 * SLICE, "staging fits");
+  const int64_t cbase = g.mode == FP8_GROUP_ROWS ? 0 : w.mat * g.c_batch;
+  const int64_t nw = n0 + wn * HALF;
+  const int ncols = static_cast<int>(max<int64_t>(0, min<int64_t>(HALF, g.N - nw)));
+#pragma unroll
+  for (int i = 0; i < WB; ++i) {
+    const int64_t mw = m0 + wm * HALF + i * 32;
+    const int rows = static_cast<int>(max<int64_t>(0, min<int64_t>(32, w.mend - mw)));
+#pragma unroll
+    for (int j = 0; j < WB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x4*>(stage + r * SP + j * 32 + 8 * e + 4 * h) =
+            f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (g.c_vec && ncols == HALF) {
+      constexpr int LPR = HALF / 8, RPP = 64 / LPR;
+      const int col = (lane % LPR) * 8;
+#pragma unroll
+      for (int p = 0; p < 32 / RPP; ++p) {
+        const int row = p * RPP + lane / LPR;
+        if (row < rows) {
+          float v[8];
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + row * SP + col);
+          const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + row * SP + col + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) { v[e] = lo[e]; v[4 + e] = hi[e]; }
+          store_row8<WIDE>(g, cbase + (mw + row) * g.ldc + nw + col, v);
+        }
+      }
+    } else {
+      for (int row = 0; row < rows; ++row) {
+        const int64_t at = cbase + (mw + row) * g.ldc + nw;
+        for (int col = lane; col < ncols; col += 64) {
+          float v = stage[row * SP + col];
+          if (g.accumulate) v += load_c(g.c, g.c_dtype, at + col);
+          store_c(g.c, g.c_dtype, at + col, v);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int FA, int FB, bool WIDE, int TILE>
+__global__ __launch_bounds__(256, TILE == 256 ? 1 : 2) void fp8_tile_kernel(Fp8Gemm g, int mtiles, int ntiles,
+                                                                           int total) {
+  tile_product<FA, FB, WIDE, TILE>(g, mtiles, ntiles, total);
+}
+
+// Which kernel a product takes.
+enum { FP8_FEW_ROWS = 0, FP8_TILE_128 = 1, FP8_TILE_256 = 2 };
+
+Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t, int32_t mode, int64_t batch, bool) {
+  const int64_t mats = mode == FP8_GROUP_ROWS ? 1 : batch;
+  auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t) * mats; };
+  if (M <= 32 || N <= 16) return {FP8_FEW_ROWS, 1};
+  if (tiles(256) >= 128) return {FP8_TILE_256, 1};
+  return {FP8_TILE_128, 1};
+}
+
+template <int FA, int FB, bool WIDE>
+static hipError_t launch(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
+  const int tm = p.kind == FP8_FEW_ROWS ? 16 : p.kind == FP8_TILE_128 ? 128 : 256;
+  const int64_t nt = (g.N + tm - 1) / tm;
+  int64_t mt = (g.M + tm - 1) / tm, z = g.batch;
+  if (g.mode == FP8_GROUP_ROWS) {   // every group may end in a part of a tile
+    mt = std::min<int64_t>(g.M, g.M / tm + g.batch);
     z = 1;
   }
   const int64_t total = mt * nt * z;
   if (total <= 0) return hipSuccess;
   if (total > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(total)), block(64 * kFewWaves);
-  if (g.c_dtype == MUON_DTYPE_F32)
-    hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, true>), grid, block, 0, s, g, static_cast<int>(mt),
-                       static_cast<int>(nt));
+  const dim3 grid(static_cast<unsigned>(total));
+  const int m = static_cast<int>(mt), n = static_cast<int>(nt);
+  if (p.kind == FP8_FEW_ROWS)
+    hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, WIDE>), grid, dim3(64 * kFewWaves), 0, s, g, m, n);
+  else if (p.kind == FP8_TILE_128)
+    hipLaunchKernelGGL((fp8_tile_kernel<FA, FB, WIDE, 128>), grid, dim3(256), 0, s, g, m, n, static_cast<int>(total));
   else
-    hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, false>), grid, block, 0, s, g, static_cast<int>(mt),
-                       static_cast<int>(nt));
+    hipLaunchKernelGGL((fp8_tile_kernel<FA, FB, WIDE, 256>), grid, dim3(256), 0, s, g, m, n, static_cast<int>(total));
   return hipGetLastError();
 }
 
+template <int FA, int FB>
+static hipError_t launch_dtype(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
+  return g.c_dtype == MUON_DTYPE_F32 ? launch<FA, FB, true>(p, g, s) : launch<FA, FB, false>(p, g, s);
+}
+
 hipError_t launch_fp8_gemm(int fmt_a, int fmt_b, const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
-  if (fmt_a == MUON_FP8_E4M3) return fmt_b == MUON_FP8_E4M3 ? launch<0, 0>(p, g, s) : launch<0, 1>(p, g, s);
-  return fmt_b == MUON_FP8_E4M3 ? launch<1, 0>(p, g, s) : launch<1, 1>(p, g, s);
+  if (fmt_a == MUON_FP8_E4M3) return fmt_b == MUON_FP8_E4M3 ? launch_dtype<0, 0>(p, g, s) : launch_dtype<0, 1>(p, g, s);
+  return fmt_b == MUON_FP8_E4M3 ? launch_dtype<1, 0>(p, g, s) : launch_dtype<1, 1>(p, g, s);
 }
 
 hipError_t launch_fp8_reduce(const Fp8Gemm&, hipStream_t) { return hipSuccess; }

@@ -409,3 +409,66 @@ def test_product_gradients_by_differences(lib):
         hi = (vd * (vx @ v.T)).sum()
         mag = (np.abs(vd[:, n]) * np.abs(vx[:, k])).sum()
         assert abs((hi - lo) - dw[n, k]) <= (T + 16) * 2.0 ** -23 * mag + 1e-9 * (abs(hi) + abs(lo))
+
+
+# products large enough for the widest tiles: many small matrices, ragged groups and
+# contractions, in every mode, both kinds of result
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(300, 260, 300), (256, 512, 128), (257, 511, 1)])
+def test_many_wide_tiles_batch(lib, M, N, K, dtype):
+    import torch
+    rng = np.random.default_rng([M, N])
+    B = 40
+    a, va = operand(lib, rng, M, K, "e4m3", B)
+    b, vb = operand(lib, rng, N, K, "e5m2", B)
+    buf = torch.full((B, M + 1, N + 3), 7.0, dtype=dt(torch, dtype), device="cuda")
+    out = buf[:, :M, 3:]
+    for acc in (False, True):
+        base = host(out) if acc else None
+        lib.fp8_matmul(a, b, out=out, accumulate=acc)
+        torch.cuda.synchronize()
+        got = host(out)
+        for i in range(0, B, 3):
+            check_product(got[i], va[i], vb[i], dtype, None if base is None else base[i])
+    assert torch.all(buf[:, M] == 7.0) and torch.all(buf[:, :, :3] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_many_wide_tiles_grouped_rows(lib, dtype):
+    import torch
+    rng = np.random.default_rng(21)
+    counts = [0, 700, 1, 0, 255, 257, 256, 0, 40, 590, 0]
+    N, K = 3700, 136
+    G, off = len(counts), np.concatenate([[0], np.cumsum(counts)])
+    M = int(off[-1]) + 500
+    a, va = operand(lib, rng, M, K, "e4m3")
+    b, vb = operand(lib, rng, N, K, "e4m3", G)
+    s = 2.0 ** -8
+    a = lib.fp8_quantize(torch.from_numpy((va * s).astype(np.float32)).cuda())
+    va = values(a)
+    out = torch.full((M, N), 7.0, dtype=dt(torch, dtype), device="cuda")
+    lib.fp8_matmul(a, b, out=out, offsets=torch.from_numpy(off.astype(np.int32)).cuda())
+    torch.cuda.synchronize()
+    assert torch.all(out[int(off[-1]):] == 7.0)
+    got = host(out)
+    for g in range(G):
+        lo, hi = off[g], off[g + 1]
+        for n in range(0, N, 740):      # a part of the columns at a time
+            check_product(got[lo:hi, n:n + 200], va[lo:hi], vb[g][n:n + 200], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_wide_tiles_grouped_contraction(lib, dtype):
+    import torch
+    rng = np.random.default_rng(22)
+    blocks = [0, 1, 3, 0, 2, 5, 1, 4] * 6
+    off = 128 * np.concatenate([[0], np.cumsum(blocks)])
+    M, N, K = 260, 300, int(off[-1]) + 1
+    a, va = operand(lib, rng, M, K, "e5m2")
+    b, vb = operand(lib, rng, N, K, "e4m3")
+    out = lib.fp8_matmul_grouped_k(a, b, torch.from_numpy(off.astype(np.int32)).cuda(), out_dtype=dt(torch, dtype))
+    torch.cuda.synchronize()
+    got = host(out)
+    for g in range(len(blocks)):
+        check_product(got[g], va[:, off[g]:off[g + 1]], vb[:, off[g]:off[g + 1]], dtype)
