@@ -221,30 +221,37 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
 // Tiles: TILE x TILE outputs per workgroup (256 or 128), four waves in a 2 x 2 grid, each
 // owning (TILE / 2)^2 outputs as 32 x 32 blocks in registers.
 //
-// The contraction advances in periods of 64 bytes per row, one 32 x 32 x 64 instruction
-// per block pair. Slices of both operands go straight from memory to LDS (no registers)
-// into a ring of four: during period t a wave multiplies slice t from one set of
-// registers, reads slice t + 1 from LDS into the other set, and issues the loads of slice
-// t + 4 into the ring place of slice t, which every wave has read by then. A load thus has
-// two to three periods (256-tiles: 2000 to 3000 cycles) to arrive, and one barrier per
-// period publishes the next slice. Beyond the last slice the loads repeat it (in bounds,
-// never used), so that the number of loads in flight is the same everywhere.
+// Slices of both operands, one block (128 bytes) of every row, go straight from memory to
+// LDS (no registers) into two buffers. A slice is multiplied in two periods of 64 bytes,
+// one 32 x 32 x 64 instruction per block pair each. During a period a wave multiplies
+// from one set of registers and reads the next period's operands from LDS into the other
+// set, so a slice's buffer has been read by the end of its first period; one barrier
+// then frees it and publishes the next slice, and the loads of the slice after next are
+// issued into it, spread over the second period. They have one to two periods (256-tiles:
+// 1000 to 2000 matrix cycles) to arrive. Rows are fetched 128 bytes at a time because
+// requests, not bytes, bound the way from the last-level cache: with four buffers of 64
+// bytes per row the same loop was 10% slower, resident data or not.
 //
-// LDS rows of a slice are 64 bytes, four 16-byte chunks; chunk c of row r is stored at
-// place c ^ ((r / 2) % 4), so eight lanes that read one chunk of eight rows touch all
+// LDS rows of a slice are 128 bytes, eight 16-byte chunks; chunk c of row r is stored at
+// place c ^ swz(r), so lanes that read one chunk of neighbouring rows spread over the
 // banks. A direct load writes consecutive lanes to consecutive places, so the lanes fetch
-// permuted chunks instead.
+// permuted chunks instead. Beyond the last slice the loads repeat it (in bounds, never
+// used).
 //
-// The loop body is two blocks, four periods: the ring's places are then known at compile
-// time. An odd last block is paired with a repeated one whose scales are set to 2^-127,
-// 2^-254 together, which adds nothing (8-bit products are below 2^33).
+// The loop body is two slices: their buffers are then known at compile time (and the
+// compiler waits for exactly the loads of the buffer that is read). An odd last slice is
+// paired with a repeated one whose scales are set to 2^-127, 2^-254 together, which adds
+// nothing (8-bit products are below 2^33).
 //
-// Scales: one word per row holds four blocks, also by direct loads, into a ring of four
-// words; a body takes its two bytes out of two neighbouring words (a group's contraction
-// may start anywhere in a word).
+// Scales: 16 bytes (16 blocks) of every row at a time, also by direct loads, in two parts
+// of LDS: while one is used the other is fetched, once in 16 slices. (One word at a time
+// fetches 64 cache lines for 256 bytes; with that in every fourth slice the loop was 12%
+// slower.) Reads behind the operand's last scale give zeros: the resource's bounds.
 //
-// Four waves of 128 x 128 read 32 KB of a 256-tile's slice per 1024 matrix cycles each:
-// 75% of the LDS rate with the writes. Smaller wave tiles would be bound by LDS.
+// Four waves of 128 x 128 read 32 KB of a 256-tile's LDS per 1024 matrix cycles each: 75%
+// of the LDS rate with the writes. Smaller wave tiles would be bound by LDS.
+
+__device__ __forceinline__ int row_swizzle(int r) { return (r ^ ((r >> 3) & 3)) & 7; }   // of r modulo 32
 
 template <int V> using Int = std::integral_constant<int, V>;
 
@@ -289,10 +296,10 @@ __device__ __forceinline__ void store_row8(const Fp8Gemm& g, int64_t at, float (
 template <int FA, int FB, bool WIDE, int TILE>
 __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int ntiles, int total) {
   constexpr int HALF = TILE / 2, WB = HALF / 32;
-  constexpr int SLICE = TILE * 64;              // bytes of one operand's slice
-  constexpr int LOADS = TILE / 64;              // 1-KB loads per wave, operand and slice
-  __shared__ __align__(1024) char ring0[2 * SLICE], ring1[2 * SLICE], ring2[2 * SLICE], ring3[2 * SLICE];
-  __shared__ __align__(16) int words[4][2 * TILE];
+  constexpr int SLICE = TILE * 128;             // bytes of one operand's slice
+  constexpr int LOADS = TILE / 32;              // 1-KB loads per wave, operand and slice
+  __shared__ __align__(1024) char buf0[2 * SLICE], buf1[2 * SLICE];
+  __shared__ __align__(16) unsigned char scales[2][2 * TILE * 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -330,14 +337,13 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   int va[LOADS], vb[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
-    const int r = (wave * LOADS + i) * 16 + (lane >> 2);
-    const int c = ((lane & 3) ^ ((r >> 1) & 3)) * 16;
+    const int r = (wave * LOADS + i) * 8 + (lane >> 3);
+    const int c = ((lane & 7) ^ row_swizzle(r)) * 16;
     va[i] = min(r, mrows - 1) * pitch + c;
     vb[i] = min(r, nrows - 1) * pitch + c;
   }
-  const int nk = 2 * (w.kb1 - w.kb0);                   // periods
+  const int nk = w.kb1 - w.kb0;                         // slices
   const int k0 = w.kb0 * 128;
-  const int qlast = (sp >> 2) - 1;                      // last scale word of a row
   // scales, 64 rows per load: of a 256-tile each wave fetches 64 rows of both operands, of
   // a 128-tile waves 0 and 1 rows of A, 2 and 3 of B
   const bool sfirst = TILE == 256 || wave < 2;
@@ -345,10 +351,12 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   const int vs0 = min(srow + lane, (sfirst ? mrows : nrows) - 1) * sp;
   const int vs1 = min(srow + lane, nrows - 1) * sp;
 
-  // per-lane read offsets within a slice: two neighbouring chunks of row lane % 32
+  // per-lane read offsets within a slice, period 0: two neighbouring chunks of row lane %
+  // 32 (the second one at ^ 16, those of period 1 at ^ 64; the swizzle only depends on the
+  // row modulo 32)
   const int r = lane & 31, h = lane >> 5;
-  const int chunk0 = ((2 * h) ^ ((r >> 1) & 3)) * 16;
-  const int ao = (wm * HALF + r) * 64 + chunk0, bo = SLICE + (wn * HALF + r) * 64 + chunk0;
+  const int chunk0 = ((2 * h) ^ row_swizzle(r)) * 16;
+  const int ao = (wm * HALF + r) * 128 + chunk0, bo = SLICE + (wn * HALF + r) * 128 + chunk0;
 
   f32x16 acc[WB][WB];
 #pragma unroll
@@ -359,90 +367,62 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   auto load_slice = [&](char* to, int t) {
-    const int so = k0 + min(t, nk - 1) * 64;
+    const int so = k0 + min(t, nk - 1) * 128;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) MUON_GLDS(ra, to + (wave * LOADS + i) * 1024, 16, va[i], so);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) MUON_GLDS(rb, to + SLICE + (wave * LOADS + i) * 1024, 16, vb[i], so);
   };
-  auto load_word = [&](int q) {
-    const int so = min(q, qlast) * 4;
-    int* to = words[q & 3];
-    if (sfirst) MUON_GLDS(rsa, to + srow, 4, vs0, so);
-    else MUON_GLDS(rsb, to + TILE + srow, 4, vs0, so);
-    if constexpr (TILE == 256) MUON_GLDS(rsb, to + TILE + srow, 4, vs1, so);
+  auto load_scales = [&](int c) {   // blocks 16 c .. 16 c + 15
+    unsigned char* to = scales[c & 1];
+    if (sfirst) MUON_GLDS(rsa, to + srow * 16, 16, vs0, c * 16);
+    else MUON_GLDS(rsb, to + (TILE + srow) * 16, 16, vs0, c * 16);
+    if constexpr (TILE == 256) MUON_GLDS(rsb, to + (TILE + srow) * 16, 16, vs1, c * 16);
   };
   i32x4 fa[2][WB][2], fb[2][WB][2];
-  auto read = [&](int set, const char* from) {
+  auto read = [&](int set, const char* from) {   // set = period of the slice
 #pragma unroll
     for (int i = 0; i < WB; ++i) {
-      fa[set][i][0] = *reinterpret_cast<const i32x4*>(from + ao + i * 2048);
-      fa[set][i][1] = *reinterpret_cast<const i32x4*>(from + (ao ^ 16) + i * 2048);
+      fa[set][i][0] = *reinterpret_cast<const i32x4*>(from + (ao ^ (set * 64)) + i * 4096);
+      fa[set][i][1] = *reinterpret_cast<const i32x4*>(from + (ao ^ (set * 64 + 16)) + i * 4096);
     }
 #pragma unroll
     for (int i = 0; i < WB; ++i) {
-      fb[set][i][0] = *reinterpret_cast<const i32x4*>(from + bo + i * 2048);
-      fb[set][i][1] = *reinterpret_cast<const i32x4*>(from + (bo ^ 16) + i * 2048);
+      fb[set][i][0] = *reinterpret_cast<const i32x4*>(from + (bo ^ (set * 64)) + i * 4096);
+      fb[set][i][1] = *reinterpret_cast<const i32x4*>(from + (bo ^ (set * 64 + 16)) + i * 4096);
     }
   };
-  // scale bytes of blocks kb and kb + 1 of the lane's rows of A, then of B: the words are
-  // read a period before they are combined
-  int sc[2 * WB], lo[2 * WB], hi[2 * WB];
-  auto read_words = [&](int kb) {
-    const int* x = words[(kb >> 2) & 3];
-    const int* y = words[((kb >> 2) + 1) & 3];
+  // scale bytes of the lane's rows of A, then of B, for the two slices of a body
+  int sc[2][2 * WB];
+  auto read_scales = [&](int set, int kb) {
+    const unsigned char* from = scales[(kb >> 4) & 1] + (kb & 15);
+    const int mask = kb < w.kb1 ? 255 : 0;
 #pragma unroll
     for (int i = 0; i < WB; ++i) {
-      lo[i] = x[wm * HALF + i * 32 + r];
-      hi[i] = y[wm * HALF + i * 32 + r];
-      lo[WB + i] = x[TILE + wn * HALF + i * 32 + r];
-      hi[WB + i] = y[TILE + wn * HALF + i * 32 + r];
+      sc[set][i] = from[(wm * HALF + i * 32 + r) * 16] & mask;
+      sc[set][WB + i] = from[(TILE + wn * HALF + i * 32 + r) * 16] & mask;
     }
   };
-  auto set_scales = [&](int kb) {
-    const int mask = kb + 1 < w.kb1 ? 0xffff : 0xff;
-#pragma unroll
-    for (int i = 0; i < 2 * WB; ++i) sc[i] = static_cast<int>(__builtin_amdgcn_alignbyte(hi[i], lo[i], kb & 3)) & mask;
-  };
-  auto publish = [&]() {       // the slice after next may still be in flight, the next one is there
-    if constexpr (TILE == 256) asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+  auto publish = [&]() {   // own reads and loads are done, then everybody's
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
 
   if (nk > 0) {
-    const int w0 = w.kb0 >> 2;
-    load_word(w0);
-    load_word(w0 + 1);
-    load_word(w0 + 2);
-    load_slice(ring0, 0);
-    load_slice(ring1, 1);
-    load_slice(ring2, 2);
-    load_slice(ring3, 3);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    read_words(w.kb0);
-    read(0, ring0);
-    set_scales(w.kb0);
+    load_scales(w.kb0 >> 4);
+    load_slice(buf0, 0);
+    load_slice(buf1, 1);
+    publish();
+    read_scales(0, w.kb0);
+    read(0, buf0);
 
-#define MUON_PERIOD(P, CUR, NEXT)                                                                          \
-  {                                                                                                        \
-    publish();                                                                                             \
-    if constexpr (P == 0) load_word((kb >> 2) + 3);                                                        \
-    if constexpr (P == 2) read_words(kb + 2);                                                              \
-    read((P & 1) ^ 1, NEXT);                                                                               \
-    load_slice(CUR, t + P + 4);                                                                            \
-    multiply(Int<P & 1>{}, Int<P / 2>{});                                                                  \
-    schedule();                                                                                            \
-  }
-    auto multiply = [&](auto set, auto byte) {
-      constexpr int SET = decltype(set)::value, U = decltype(byte)::value;
+    auto multiply = [&](auto set, auto slice) {
+      constexpr int SET = decltype(set)::value, U = decltype(slice)::value;
       if constexpr (WIDE) {
         float fs[2 * WB];
 #pragma unroll
-        for (int i = 0; i < 2 * WB; ++i) fs[i] = scale_value(sc[i], U);
+        for (int i = 0; i < 2 * WB; ++i) fs[i] = scale_value(sc[U][i], 0);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           bf16x8 xa[WB], xb[WB];
@@ -464,32 +444,53 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
           for (int j = 0; j < WB; ++j) {
             const i32x8 x = __builtin_shufflevector(fa[SET][i][0], fa[SET][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
             const i32x8 y = __builtin_shufflevector(fb[SET][j][0], fb[SET][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], FB, FA, U, sc[WB + j], U, sc[i]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], FB, FA, 0, sc[U][WB + j], 0, sc[U][i]);
           }
       }
     };
-    auto schedule = [&]() {
+    // reads and loads spread over the period's matrix instructions
+    auto schedule = [&](auto loads) {
       if constexpr (!WIDE) {
+        constexpr int NM = WB * WB, NR = 4 * WB, NL = decltype(loads)::value ? 2 * LOADS : 0;
 #pragma unroll
-        for (int i = 0; i < 2 * LOADS; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);               // LDS reads
-          __builtin_amdgcn_sched_group_barrier(0x008, WB * WB / (2 * LOADS) > 1 ? 1 : 0, 0);
-          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);               // load to LDS
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
+        for (int i = 0; i < NM; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x100, NR / NM > 1 ? NR / NM : 1, 0);   // LDS reads
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                           // MFMA
+          if constexpr (NL > 0) __builtin_amdgcn_sched_group_barrier(0x020, NL / NM, 0);  // loads to LDS
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    int kb = w.kb0;
-    for (int t = 0; t < nk; t += 4, kb += 2) {
-      MUON_PERIOD(0, ring0, ring1)
-      MUON_PERIOD(1, ring1, ring2)
-      MUON_PERIOD(2, ring2, ring3)
-      MUON_PERIOD(3, ring3, ring0)
-      set_scales(kb + 2);
+    int t = 0, kb = w.kb0;
+    while (t < nk) {
+      // the scales behind this part's; their place was last read before the last barrier
+      const int part = kb >> 4;
+      load_scales(part + 1);
+      for (; t < nk && (kb >> 4) == part; t += 2, kb += 2) {
+        // slice t, first period
+        read(1, buf0);
+        multiply(Int<0>{}, Int<0>{});
+        schedule(Int<0>{});
+        publish();
+        // second period: slice t + 1 is there, buf0 is free
+        read_scales(1, kb + 1);
+        read(0, buf1);
+        load_slice(buf0, t + 2);
+        multiply(Int<1>{}, Int<0>{});
+        schedule(Int<1>{});
+        // slice t + 1
+        read(1, buf1);
+        multiply(Int<0>{}, Int<1>{});
+        schedule(Int<0>{});
+        publish();
+        read_scales(0, kb + 2);
+        read(0, buf0);
+        load_slice(buf1, t + 3);
+        multiply(Int<1>{}, Int<1>{});
+        schedule(Int<1>{});
+      }
     }
-#undef MUON_PERIOD
-    // the last loads land before the ring is used again
+    // the last loads land before the buffers are used again
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -498,8 +499,8 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   // Results: 32 rows of a wave at a time through its own part of LDS, then whole rows,
   // 16 bytes per lane where the rows are aligned for it.
   constexpr int SP = HALF + 4;
-  float* stage = reinterpret_cast<float*>(wave == 0 ? ring0 : wave == 1 ? ring1 : wave == 2 ? ring2 : ring3);
-  static_assert(32 * SP * 4 <= 2 * SLICE, "staging fits");
+  float* stage = reinterpret_cast<float*>((wave < 2 ? buf0 : buf1) + (wave & 1) * SLICE);
+  static_assert(32 * SP * 4 <= SLICE, "staging fits");
   const int64_t cbase = g.mode == FP8_GROUP_ROWS ? 0 : w.mat * g.c_batch;
   const int64_t nw = n0 + wn * HALF;
   const int ncols = static_cast<int>(max<int64_t>(0, min<int64_t>(HALF, g.N - nw)));
