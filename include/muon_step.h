@@ -375,7 +375,7 @@ enum { MUON_FP8_E4M3 = 0, MUON_FP8_E5M2 = 1 };
 
 /* Limits of the 8-bit operands and products: rows, cols <= MUON_FP8_MAX_SIDE,
  * batch and groups <= MUON_FP8_MAX_BATCH. */
-#define MUON_FP8_MAX_SIDE (1 << 23)
+#define MUON_FP8_MAX_SIDE ((1 << 23) - 128)
 #define MUON_FP8_MAX_BATCH 1024
 
 typedef struct {

@@ -32,68 +32,75 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------------------
-// Group of a row tile. Every wave of the workgroup finds it by itself: 64 groups at a
-// time, a prefix sum of their tile counts. Returns false for a tile beyond the last
-// group's.
-__device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups, int limit, int tile_rows, int tile,
-                                           int& group, int& first, int& end) {
+// Groups of rows. Every wave finds a tile's group by itself: 64 groups at a time, a prefix
+// sum of their tile counts. The first 64 groups stay in registers.
+
+__device__ __forceinline__ int wave_inclusive_sum(int v) {
   const int lane = threadIdx.x & 63;
-  int base = 0;
-  for (int g0 = 0; g0 < n_groups; g0 += 64) {
-    const int g = g0 + lane;
-    int lo = 0, hi = 0;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(v, o, 64);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+struct Groups {
+  int lo, hi, incl;   // of group `lane` of the 64: rows, tiles of it and the ones before it
+  int first;          // the first of the 64
+
+  __device__ __forceinline__ void fetch(const int32_t* offsets, int n_groups, int limit, int tile_rows, int g0) {
+    const int g = g0 + (threadIdx.x & 63);
+    lo = hi = 0;
     if (g < n_groups) {
       lo = min(max(offsets[g], 0), limit);
       hi = min(max(offsets[g + 1], lo), limit);
     }
-    const int n = (hi - lo + tile_rows - 1) / tile_rows;
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += up;
-    }
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    if (tile < base + total) {
-      const int l = __builtin_ctzll(__ballot(base + incl > tile));
-      group = g0 + l;
-      first = __builtin_amdgcn_readlane(lo, l) + (tile - base - __builtin_amdgcn_readlane(incl - n, l)) * tile_rows;
-      end = __builtin_amdgcn_readlane(hi, l);
-      return true;
-    }
-    base += total;
+    incl = wave_inclusive_sum((hi - lo + tile_rows - 1) / tile_rows);
+    first = g0;
   }
-  return false;
-}
-
-// What a workgroup computes (the same in all its lanes): rows [m0, mend) of A (a tile of
-// them), matrix `mat` of B and C, blocks [kb0, kb1) of the contraction.
-struct Work {
-  int m0, mend;
-  int mat, amat, bmat;
-  int kb0, kb1;
+  __device__ __forceinline__ int tiles() const { return __builtin_amdgcn_readlane(incl, 63); }
 };
 
-template <int TM>
-__device__ __forceinline__ bool find_work(const Fp8Gemm& g, int mtile, int z, Work& w) {
-  w.kb0 = 0;
-  w.kb1 = g.kb;
-  w.m0 = mtile * TM;
-  w.mend = static_cast<int>(g.M);
-  w.mat = w.amat = w.bmat = z;
-  if (g.mode == FP8_GROUP_ROWS) {
-    w.amat = 0;
-    if (!find_group(g.offsets, g.batch, static_cast<int>(g.M), TM, mtile, w.mat, w.m0, w.mend)) return false;
-    w.bmat = w.mat;
-  } else if (g.mode == FP8_GROUP_K) {
-    w.amat = w.bmat = 0;
-    const int limit = g.kb * 128;
-    const int lo = min(max(g.offsets[z], 0), limit);
-    const int hi = min(max(g.offsets[z + 1], lo), limit);
-    w.kb0 = __builtin_amdgcn_readfirstlane(lo / 128);
-    w.kb1 = __builtin_amdgcn_readfirstlane(hi > lo ? (hi + 127) / 128 : lo / 128);
+// Row tiles of all groups.
+__device__ __forceinline__ int count_group_tiles(const int32_t* offsets, int n_groups, int limit, int tile_rows,
+                                                 Groups& cache) {
+  cache.fetch(offsets, n_groups, limit, tile_rows, 0);
+  int n = cache.tiles();
+  for (int g0 = 64; g0 < n_groups; g0 += 64) {
+    Groups more;
+    more.fetch(offsets, n_groups, limit, tile_rows, g0);
+    n += more.tiles();
   }
+  return n;
+}
+
+// The group and rows of row tile `tile`; false for one beyond the last group's.
+__device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups, int limit, int tile_rows,
+                                           const Groups& cache, int tile, int& group, int& first, int& end) {
+  Groups g = cache;
+  while (tile >= g.tiles()) {
+    tile -= g.tiles();
+    if (g.first + 64 >= n_groups) return false;
+    g.fetch(offsets, n_groups, limit, tile_rows, g.first + 64);
+  }
+  const int l = __builtin_ctzll(__ballot(g.incl > tile));
+  const int lo = __builtin_amdgcn_readlane(g.lo, l), hi = __builtin_amdgcn_readlane(g.hi, l);
+  const int before = __builtin_amdgcn_readlane(g.incl, l) - (hi - lo + tile_rows - 1) / tile_rows;
+  group = g.first + l;
+  first = lo + (tile - before) * tile_rows;
+  end = hi;
   return true;
+}
+
+// Blocks [kb0, kb1) of group z of a grouped contraction (scalar loads: z is uniform).
+__device__ __forceinline__ void group_blocks(const Fp8Gemm& g, int z, int& kb0, int& kb1) {
+  const auto* off = (const __attribute__((address_space(4))) int32_t*)(g.offsets);
+  const int limit = g.kb * 128;
+  const int lo = min(max(off[z], 0), limit);
+  const int hi = min(max(off[z + 1], lo), limit);
+  kb0 = lo / 128;
+  kb1 = hi > lo ? (hi + 127) / 128 : kb0;
 }
 
 __device__ __forceinline__ float load_c(const void* c, int dtype, int64_t i) {
@@ -172,8 +179,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
   const int z = blockIdx.x / per;
   const int rest = blockIdx.x - z * per;
   const int nt = rest / mtiles, mt = rest - nt * mtiles;
-  Work w;
-  if (!find_work<16>(g, mt, z, w)) return;
+  // rows [m0, mend) of A (a tile of them), matrix `mat` of B and C, blocks [kb0, kb1)
+  struct { int m0, mend, mat, amat, bmat, kb0, kb1; } w = {mt * 16, static_cast<int>(g.M), z, z, z, 0, g.kb};
+  if (g.mode == FP8_GROUP_ROWS) {
+    Groups groups;
+    groups.fetch(g.offsets, g.batch, static_cast<int>(g.M), 16, 0);
+    if (!find_group(g.offsets, g.batch, static_cast<int>(g.M), 16, groups, mt, w.mat, w.m0, w.mend)) return;
+    w.amat = 0;
+    w.bmat = w.mat;
+  } else if (g.mode == FP8_GROUP_K) {
+    w.amat = w.bmat = 0;
+    group_blocks(g, z, w.kb0, w.kb1);
+  }
   const int r = lane & 15, p = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(nt) * 16;
   const int64_t ra = min(w.m0 + r, w.mend - 1), rb = min(n0 + r, g.N - 1);
@@ -218,8 +235,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
 }
 
 // ---------------------------------------------------------------------------
-// Tiles: TILE x TILE outputs per workgroup (256 or 128), four waves in a 2 x 2 grid, each
-// owning (TILE / 2)^2 outputs as 32 x 32 blocks in registers.
+// Tiles: TILE x TILE outputs (256 or 128) by four waves in a 2 x 2 grid, each owning
+// (TILE / 2)^2 outputs as 32 x 32 blocks in registers. A workgroup walks over tiles
+// (one workgroup per CU with 256-tiles, two with 128-tiles).
 //
 // Slices of both operands, one block (128 bytes) of every row, go straight from memory to
 // LDS (no registers) into two buffers. A slice is multiplied in two periods of 64 bytes,
@@ -232,124 +250,129 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
 // requests, not bytes, bound the way from the last-level cache: with four buffers of 64
 // bytes per row the same loop was 10% slower, resident data or not.
 //
+// The slices of a workgroup's tiles form one stream: the last slices of a tile are
+// followed by the first ones of the next, which arrive while the results of the tile are
+// stored. Results therefore pass through a part of LDS of their own (4 KB per wave).
+//
 // LDS rows of a slice are 128 bytes, eight 16-byte chunks; chunk c of row r is stored at
 // place c ^ swz(r), so lanes that read one chunk of neighbouring rows spread over the
-// banks. A direct load writes consecutive lanes to consecutive places, so the lanes fetch
-// permuted chunks instead. Beyond the last slice the loads repeat it (in bounds, never
-// used).
+// banks (no conflicts counted). A direct load writes consecutive lanes to consecutive
+// places, so the lanes fetch permuted chunks instead. Rows and slices beyond the operand
+// or the group are fetched as zeros: the buffer resource's bounds.
 //
-// The loop body is two slices: their buffers are then known at compile time (and the
-// compiler waits for exactly the loads of the buffer that is read). An odd last slice is
-// paired with a repeated one whose scales are set to 2^-127, 2^-254 together, which adds
-// nothing (8-bit products are below 2^33).
+// The loop body is two slices: their buffers are then known at compile time, and the
+// compiler waits for exactly the loads of the buffer that is read. An odd last slice is
+// paired with one of zeros, whose scales are set to 2^-127.
 //
 // Scales: 16 bytes (16 blocks) of every row at a time, also by direct loads, in two parts
 // of LDS: while one is used the other is fetched, once in 16 slices. (One word at a time
 // fetches 64 cache lines for 256 bytes; with that in every fourth slice the loop was 12%
-// slower.) Reads behind the operand's last scale give zeros: the resource's bounds.
-//
-// Four waves of 128 x 128 read 32 KB of a 256-tile's LDS per 1024 matrix cycles each: 75%
-// of the LDS rate with the writes. Smaller wave tiles would be bound by LDS.
+// slower.)
 
 __device__ __forceinline__ int row_swizzle(int r) { return (r ^ ((r >> 3) & 3)) & 7; }   // of r modulo 32
 
 template <int V> using Int = std::integral_constant<int, V>;
 
-#define MUON_GLDS(rsrc, lds, size, voff, soff)                                                              \
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(lds), size, voff, soff, 0, 0)
+// 16 bytes of results at any element-aligned place
+typedef u16x8 u16x8_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
-// 8 neighbouring results in one row, 16-byte aligned (WIDE: fp32 results).
-template <bool WIDE>
-__device__ __forceinline__ void store_row8(const Fp8Gemm& g, int64_t at, float (&v)[8]) {
-  if constexpr (WIDE) {
-    f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(g.c) + at);
-    f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-    if (g.accumulate) {
-      a += p[0];
-      b += p[1];
-    }
-    p[0] = a;
-    p[1] = b;
-  } else {
-    u16x8* p = reinterpret_cast<u16x8*>(static_cast<unsigned short*>(g.c) + at);
-    if (g.accumulate) {
-      const u16x8 u = *p;
+// What a tile does with its results: rounds them to bf16 or fp16, adds them to 16-bit ones,
+// or (WIDE products) stores or adds fp32.
+enum { OUT_BF16 = 0, OUT_F16 = 1, OUT_ADD_16 = 2, OUT_F32 = 3 };
+
+template <typename T>
+__device__ __forceinline__ u16x4 round4(float a, float b, float c, float d) {
+  const float v[4] = {a, b, c, d};
+  T o[4];
+  rne<T, 4>(v, o);
+  u16x4 u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += g.c_dtype == MUON_DTYPE_BF16 ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
-    }
-    u16x8 u;
-    if (g.c_dtype == MUON_DTYPE_BF16) {
-      __bf16 o[8];
-      rne<__bf16, 8>(v, o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = __builtin_bit_cast(unsigned short, o[e]);
-    } else {
-      _Float16 o[8];
-      rne<_Float16, 8>(v, o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = __builtin_bit_cast(unsigned short, o[e]);
-    }
-    *p = u;
-  }
+  for (int e = 0; e < 4; ++e) u[e] = __builtin_bit_cast(unsigned short, o[e]);
+  return u;
 }
 
-template <int FA, int FB, bool WIDE, int TILE>
-__device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int ntiles, int total) {
+// A tile: rows [m0, mend) of A and C (its own TILE of them), columns from n0, matrix `mat`
+// of C, blocks [kb0, kb1) of the contraction; its operands' first rows and the bytes of
+// their rows (what lies behind reads as zeros).
+struct Tile {
+  int m0, mend, n0, mat;
+  int kb0, kb1;
+  const uint8_t *a, *b;
+  int na, nb;
+};
+
+template <int FA, int FB, int OUT, int TILE>
+__device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int ntiles) {
+  constexpr bool WIDE = OUT == OUT_F32;
   constexpr int HALF = TILE / 2, WB = HALF / 32;
   constexpr int SLICE = TILE * 128;             // bytes of one operand's slice
   constexpr int LOADS = TILE / 32;              // 1-KB loads per wave, operand and slice
+  constexpr int STAGE = TILE * 16;              // bytes of a wave's results in LDS
   __shared__ __align__(1024) char buf0[2 * SLICE], buf1[2 * SLICE];
   __shared__ __align__(16) unsigned char scales[2][2 * TILE * 16];
+  __shared__ __align__(16) char stages[4 * STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
+  const int pitch = static_cast<int>(g.pitch), sp = static_cast<int>(g.s_pitch);
+
+  Groups groups{};
+  if (g.mode == FP8_GROUP_ROWS)
+    mtiles = count_group_tiles(g.offsets, g.batch, static_cast<int>(g.M), TILE, groups);
+  const int total = mtiles * ntiles * (g.mode == FP8_GROUP_ROWS ? 1 : g.batch);
 
   // Workgroups are dealt round-robin over the eight XCDs. In every round of the chip each
   // XCD takes consecutive tiles (its own last-level cache then sees neighbours), and all
   // XCDs stay close together. Within a matrix, bands of four tile columns are walked row
   // by row.
   constexpr int ROUND = TILE == 256 ? 256 : 512;
-  const int chunk = blockIdx.x / ROUND, inside = blockIdx.x % ROUND;
-  const int size = min(ROUND, total - chunk * ROUND);
-  const int b = chunk * ROUND + (inside & 7) * (size / 8) + min(inside & 7, size % 8) + (inside >> 3);
-  const int per = mtiles * ntiles;
-  const int z = b / per;
-  const int rest = b - z * per;
-  const int band = rest / (4 * mtiles);
-  const int first = band * 4, width = min(4, ntiles - first);
-  const int in = rest - band * 4 * mtiles;
-  const int mt = in / width, nt = first + in % width;
-  Work w;
-  if (!find_work<TILE>(g, mt, z, w)) return;
-  const int64_t m0 = w.m0, n0 = static_cast<int64_t>(nt) * TILE;
-  const int mrows = static_cast<int>(min<int64_t>(TILE, w.mend - m0)), nrows = static_cast<int>(min<int64_t>(TILE, g.N - n0));
+  auto tile_at = [&](int index) {
+    const int chunk = index / ROUND, inside = index % ROUND;
+    const int size = min(ROUND, total - chunk * ROUND);
+    const int b = chunk * ROUND + (inside & 7) * (size / 8) + min(inside & 7, size % 8) + (inside >> 3);
+    const int per = mtiles * ntiles;
+    const int z = b / per;
+    const int rest = b - z * per;
+    const int band = rest / (4 * mtiles);
+    const int width = min(4, ntiles - band * 4);
+    const int in = rest - band * 4 * mtiles;
+    const int mt = in / width;
+    Tile t;
+    t.n0 = (band * 4 + in - mt * width) * TILE;
+    t.m0 = mt * TILE;
+    t.mend = static_cast<int>(g.M);
+    t.mat = z;
+    t.kb0 = 0;
+    t.kb1 = g.kb;
+    if (g.mode == FP8_GROUP_ROWS)
+      find_group(g.offsets, g.batch, static_cast<int>(g.M), TILE, groups, mt, t.mat, t.m0, t.mend);
+    else if (g.mode == FP8_GROUP_K)
+      group_blocks(g, z, t.kb0, t.kb1);
+    t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+    t.mend = __builtin_amdgcn_readfirstlane(t.mend);
+    t.mat = __builtin_amdgcn_readfirstlane(t.mat);
+    t.a = g.a + (g.mode == FP8_DENSE ? t.mat * g.a_batch : 0) + t.m0 * g.pitch;
+    t.b = g.b + (g.mode == FP8_GROUP_K ? 0 : t.mat * g.b_batch) + t.n0 * g.pitch;
+    t.na = min(TILE, t.mend - t.m0) * pitch;
+    t.nb = static_cast<int>(min<int64_t>(TILE, g.N - t.n0)) * pitch;
+    return t;
+  };
+  // slices of a tile, counted in pairs
+  auto slices_of = [](const Tile& t) { return max(2, (t.kb1 - t.kb0 + 1) & ~1); };
 
-  // resources of the tile's rows and per-lane offsets (rows beyond the tile repeat its last)
-  const int pitch = static_cast<int>(g.pitch), sp = static_cast<int>(g.s_pitch);
-  const uint8_t* pa = g.a + w.amat * g.a_batch + m0 * g.pitch;
-  const uint8_t* pb = g.b + w.bmat * g.b_batch + n0 * g.pitch;
-  const uint8_t* psa = g.sa + w.amat * g.sa_batch + m0 * g.s_pitch;
-  const uint8_t* psb = g.sb + w.bmat * g.sb_batch + n0 * g.s_pitch;
-  const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pa), 0, mrows * pitch, 0x00027000);
-  const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pb), 0, nrows * pitch, 0x00027000);
-  const auto rsa = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(psa), 0, mrows * sp, 0x00027000);
-  const auto rsb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(psb), 0, nrows * sp, 0x00027000);
-  int va[LOADS], vb[LOADS];
+  // per-lane offsets: operand rows (both operands have the same), scale rows (64 per load:
+  // of a 256-tile each wave fetches 64 rows of both operands, of a 128-tile waves 0 and 1
+  // rows of A, 2 and 3 of B)
+  int vo[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
     const int r = (wave * LOADS + i) * 8 + (lane >> 3);
-    const int c = ((lane & 7) ^ row_swizzle(r)) * 16;
-    va[i] = min(r, mrows - 1) * pitch + c;
-    vb[i] = min(r, nrows - 1) * pitch + c;
+    vo[i] = r * pitch + ((lane & 7) ^ row_swizzle(r)) * 16;
   }
-  const int nk = w.kb1 - w.kb0;                         // slices
-  const int k0 = w.kb0 * 128;
-  // scales, 64 rows per load: of a 256-tile each wave fetches 64 rows of both operands, of
-  // a 128-tile waves 0 and 1 rows of A, 2 and 3 of B
   const bool sfirst = TILE == 256 || wave < 2;
   const int srow = (TILE == 256 ? wave : wave & 1) * 64;
-  const int vs0 = min(srow + lane, (sfirst ? mrows : nrows) - 1) * sp;
-  const int vs1 = min(srow + lane, nrows - 1) * sp;
+  const int vs = (srow + lane) * sp;
 
   // per-lane read offsets within a slice, period 0: two neighbouring chunks of row lane %
   // 32 (the second one at ^ 16, those of period 1 at ^ 64; the swizzle only depends on the
@@ -358,27 +381,41 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   const int chunk0 = ((2 * h) ^ row_swizzle(r)) * 16;
   const int ao = (wm * HALF + r) * 128 + chunk0, bo = SLICE + (wn * HALF + r) * 128 + chunk0;
 
-  f32x16 acc[WB][WB];
+#define MUON_RSRC(p, n) __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, n, 0x00027000)
+#define MUON_GLDS(rsrc, lds, size, voff, soff)                                                              \
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(lds), size, voff, soff, 0, 0)
+  // slice `s` of a tile (zeros behind its last one)
+  auto load_slice = [&](char* to, const uint8_t* a, const uint8_t* b, int na, int nb, int kb0, int kb1, int s) {
+    const bool there = kb0 + s < kb1;
+    const auto ra = MUON_RSRC(a, there ? na : 0), rb = MUON_RSRC(b, there ? nb : 0);
+    const int so = there ? (kb0 + s) * 128 : 0;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) MUON_GLDS(ra, to + (wave * LOADS + i) * 1024, 16, vo[i], so);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) MUON_GLDS(rb, to + SLICE + (wave * LOADS + i) * 1024, 16, vo[i], so);
+  };
+  // 16 blocks of scales of a tile's rows, by (first row, rows) of both operands
+  auto load_scales = [&](int slot, int mat, int m0, int rows_a, int n0, int rows_b, int part) {
+    unsigned char* to = scales[slot];
+    const uint8_t* sa = g.sa + (g.mode == FP8_DENSE ? mat * g.sa_batch : 0) + m0 * g.s_pitch;
+    const uint8_t* sb = g.sb + (g.mode == FP8_GROUP_K ? 0 : mat * g.sb_batch) + n0 * g.s_pitch;
+    const auto ra = MUON_RSRC(sa, rows_a * sp), rb = MUON_RSRC(sb, rows_b * sp);
+    if (sfirst) MUON_GLDS(ra, to + srow * 16, 16, vs, part * 16);
+    else MUON_GLDS(rb, to + (TILE + srow) * 16, 16, vs, part * 16);
+    if constexpr (TILE == 256) MUON_GLDS(rb, to + (TILE + srow) * 16, 16, vs, part * 16);
+  };
+  auto scales_of = [&](int slot, const Tile& t, int part, bool any) {
+    load_scales(slot, t.mat, t.m0, any ? min(TILE, t.mend - t.m0) : 0, t.n0,
+                any ? static_cast<int>(min<int64_t>(TILE, g.N - t.n0)) : 0, part);
+  };
+
+  f32x16 acc[WB][WB];   // zeros again once a tile is stored
 #pragma unroll
   for (int i = 0; i < WB; ++i)
 #pragma unroll
     for (int j = 0; j < WB; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-
-  auto load_slice = [&](char* to, int t) {
-    const int so = k0 + min(t, nk - 1) * 128;
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) MUON_GLDS(ra, to + (wave * LOADS + i) * 1024, 16, va[i], so);
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) MUON_GLDS(rb, to + SLICE + (wave * LOADS + i) * 1024, 16, vb[i], so);
-  };
-  auto load_scales = [&](int c) {   // blocks 16 c .. 16 c + 15
-    unsigned char* to = scales[c & 1];
-    if (sfirst) MUON_GLDS(rsa, to + srow * 16, 16, vs0, c * 16);
-    else MUON_GLDS(rsb, to + (TILE + srow) * 16, 16, vs0, c * 16);
-    if constexpr (TILE == 256) MUON_GLDS(rsb, to + (TILE + srow) * 16, 16, vs1, c * 16);
-  };
   i32x4 fa[2][WB][2], fb[2][WB][2];
   auto read = [&](int set, const char* from) {   // set = period of the slice
 #pragma unroll
@@ -392,164 +429,269 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
       fb[set][i][1] = *reinterpret_cast<const i32x4*>(from + (bo ^ (set * 64 + 16)) + i * 4096);
     }
   };
-  // scale bytes of the lane's rows of A, then of B, for the two slices of a body
+  // scale bytes of the lane's rows of A, then of B, for the two slices of a body. They are
+  // read in the period before their slice's first one and masked in that one (0, 2^-127,
+  // for a slice behind the last: its zeros must not meet another group's NaN scale).
   int sc[2][2 * WB];
-  auto read_scales = [&](int set, int kb) {
-    const unsigned char* from = scales[(kb >> 4) & 1] + (kb & 15);
-    const int mask = kb < w.kb1 ? 255 : 0;
+  auto read_scales = [&](int set, int slot, int kb) {
+    const unsigned char* from = scales[slot] + (kb & 15);
 #pragma unroll
     for (int i = 0; i < WB; ++i) {
-      sc[set][i] = from[(wm * HALF + i * 32 + r) * 16] & mask;
-      sc[set][WB + i] = from[(TILE + wn * HALF + i * 32 + r) * 16] & mask;
+      sc[set][i] = from[(wm * HALF + i * 32 + r) * 16];
+      sc[set][WB + i] = from[(TILE + wn * HALF + i * 32 + r) * 16];
     }
+  };
+  auto mask_scales = [&](int set, bool there) {
+    const int mask = there ? 255 : 0;
+#pragma unroll
+    for (int i = 0; i < 2 * WB; ++i) sc[set][i] &= mask;
   };
   auto publish = [&]() {   // own reads and loads are done, then everybody's
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-
-  if (nk > 0) {
-    load_scales(w.kb0 >> 4);
-    load_slice(buf0, 0);
-    load_slice(buf1, 1);
-    publish();
-    read_scales(0, w.kb0);
-    read(0, buf0);
-
-    auto multiply = [&](auto set, auto slice) {
-      constexpr int SET = decltype(set)::value, U = decltype(slice)::value;
-      if constexpr (WIDE) {
-        float fs[2 * WB];
+  auto multiply = [&](auto set, auto slice) {
+    constexpr int SET = decltype(set)::value, U = decltype(slice)::value;
+    if constexpr (WIDE) {
+      float fs[2 * WB];
 #pragma unroll
-        for (int i = 0; i < 2 * WB; ++i) fs[i] = scale_value(sc[U][i], 0);
+      for (int i = 0; i < 2 * WB; ++i) fs[i] = scale_value(sc[U][i], 0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          bf16x8 xa[WB], xb[WB];
+      for (int s = 0; s < 4; ++s) {
+        bf16x8 xa[WB], xb[WB];
 #pragma unroll
-          for (int i = 0; i < WB; ++i) {
-            xa[i] = to_bf16x8<FA>(fa[SET][i][s >> 1][2 * (s & 1)], fa[SET][i][s >> 1][2 * (s & 1) + 1], fs[i]);
-            xb[i] = to_bf16x8<FB>(fb[SET][i][s >> 1][2 * (s & 1)], fb[SET][i][s >> 1][2 * (s & 1) + 1], fs[WB + i]);
-          }
-#pragma unroll
-          for (int i = 0; i < WB; ++i)
-#pragma unroll
-            for (int j = 0; j < WB; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[j], xa[i], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < WB; ++i) {
+          xa[i] = to_bf16x8<FA>(fa[SET][i][s >> 1][2 * (s & 1)], fa[SET][i][s >> 1][2 * (s & 1) + 1], fs[i]);
+          xb[i] = to_bf16x8<FB>(fb[SET][i][s >> 1][2 * (s & 1)], fb[SET][i][s >> 1][2 * (s & 1) + 1], fs[WB + i]);
         }
-      } else {
 #pragma unroll
         for (int i = 0; i < WB; ++i)
 #pragma unroll
-          for (int j = 0; j < WB; ++j) {
-            const i32x8 x = __builtin_shufflevector(fa[SET][i][0], fa[SET][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            const i32x8 y = __builtin_shufflevector(fb[SET][j][0], fb[SET][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], FB, FA, 0, sc[U][WB + j], 0, sc[U][i]);
-          }
+          for (int j = 0; j < WB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb[j], xa[i], acc[i][j], 0, 0, 0);
       }
-    };
-    // reads and loads spread over the period's matrix instructions
-    auto schedule = [&](auto loads) {
-      if constexpr (!WIDE) {
-        constexpr int NM = WB * WB, NR = 4 * WB, NL = decltype(loads)::value ? 2 * LOADS : 0;
+    } else {
 #pragma unroll
-        for (int i = 0; i < NM; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x100, NR / NM > 1 ? NR / NM : 1, 0);   // LDS reads
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                           // MFMA
-          if constexpr (NL > 0) __builtin_amdgcn_sched_group_barrier(0x020, NL / NM, 0);  // loads to LDS
+      for (int i = 0; i < WB; ++i)
+#pragma unroll
+        for (int j = 0; j < WB; ++j) {
+          const i32x8 x = __builtin_shufflevector(fa[SET][i][0], fa[SET][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          const i32x8 y = __builtin_shufflevector(fb[SET][j][0], fb[SET][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y, x, acc[i][j], FB, FA, 0, sc[U][WB + j], 0, sc[U][i]);
+        }
+    }
+  };
+  // reads and loads spread over the period's matrix instructions
+  auto schedule = [&](auto loads) {
+    if constexpr (!WIDE) {
+      constexpr int NM = WB * WB;
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        if constexpr (decltype(loads)::value) {
+          // 4 WB operand and 2 WB scale reads, 2 LOADS loads
+          __builtin_amdgcn_sched_group_barrier(0x100, NM == 16 ? 2 : 3, 0);        // LDS reads
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // MFMA
+          __builtin_amdgcn_sched_group_barrier(0x020, 2 * LOADS / NM, 0);          // loads to LDS
+        } else {
+          __builtin_amdgcn_sched_group_barrier(0x100, 4 * WB / NM, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    int t = 0, kb = w.kb0;
-    while (t < nk) {
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // Results of a tile, a few blocks at a time through the wave's part of LDS, in 16-byte
+  // chunks swizzled by the row, so that they leave as 64 or 128 neighbouring bytes of a
+  // row. Register 4 q + e of block (i, j) in lane l is row l % 32, column 8 q + 4 (l / 32)
+  // + e of the block. 16-bit results are rounded before (TILE / 128 blocks together), fp32
+  // ones and sums with what is there pass in fp32, 32 rows of a block (128-tiles: 16) at a
+  // time.
+  char* stage = stages + wave * STAGE;
+  auto store = [&](const Tile& t) {
+    constexpr bool ROUNDED = OUT == OUT_BF16 || OUT == OUT_F16;
+    constexpr int NB = ROUNDED ? TILE / 128 : 1;          // blocks at a time
+    constexpr int RS = ROUNDED ? 32 : STAGE / 128;        // rows at a time
+    constexpr int CH = ROUNDED ? 4 * NB : 8;              // chunks of a staged row
+    constexpr int LPR = ROUNDED ? CH : 4, RPP = 64 / LPR; // lanes per row (8 columns each), rows per pass
+    constexpr int ESZ = WIDE ? 4 : 2;
+    const int col = (lane % LPR) * 8;
+    const int rows = t.mend - (t.m0 + wm * HALF) - lane / LPR;          // beyond the lane's first row
+    const int cols = static_cast<int>(g.N - (t.n0 + wn * HALF)) - col;  // beyond the lane's first column
+    char* c = static_cast<char*>(g.c) +
+              ((g.mode == FP8_GROUP_ROWS ? 0 : t.mat * g.c_batch) + (t.m0 + wm * HALF + lane / LPR) * g.ldc + t.n0 +
+               wn * HALF + col) * ESZ;
+    const int64_t step = RPP * g.ldc * ESZ;   // bytes from pass to pass
+#pragma unroll
+    for (int i = 0; i < WB; ++i) {
+#pragma unroll
+      for (int s = 0; s < 32 / RS; ++s) {
+#pragma unroll
+        for (int j = 0; j < WB; j += NB) {
+          // the blocks stay in accumulation registers until here
+          if constexpr (TILE == 256) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) asm volatile("" : "+a"(acc[i][j + b]));
+          }
+          if (RS == 32 || (r >> 4) == s) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const f32x16& x = acc[i][j + b];
+                if constexpr (ROUNDED) {
+                  using T = std::conditional_t<OUT == OUT_BF16, __bf16, _Float16>;
+                  *reinterpret_cast<u16x4*>(stage + r * (CH * 16) + (((b * 4 + q) ^ (r & (CH - 1))) * 16) + h * 8) =
+                      round4<T>(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                } else {
+                  *reinterpret_cast<f32x4*>(stage + (r % RS) * 128 + (((2 * q + h) ^ (r & 7)) * 16)) =
+                      f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                }
+              }
+          }
+          __builtin_amdgcn_wave_barrier();
+          if (s == 32 / RS - 1) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[i][j + b][e] = 0.0f;
+          }
+          char* to = c;
+#pragma unroll
+          for (int p = 0; p < RS / RPP; ++p, to += step) {
+            const int row = p * RPP + lane / LPR, done = i * 32 + s * RS + p * RPP;
+            if (done >= rows || j * 32 >= cols) continue;
+            char* at = to + j * 32 * ESZ;
+            if constexpr (ROUNDED) {
+              const char* from = stage + row * (CH * 16) + (((lane % LPR) ^ (row & (CH - 1))) * 16);
+              if (j * 32 + 8 <= cols) {
+                *reinterpret_cast<u16x8_any*>(at) = *reinterpret_cast<const u16x8*>(from);
+              } else {
+#pragma unroll 1
+                for (int e = 0; e < cols - j * 32; ++e)
+                  reinterpret_cast<unsigned short*>(at)[e] = reinterpret_cast<const unsigned short*>(from)[e];
+              }
+            } else {
+              const char* f0 = stage + row * 128 + (((2 * (lane % LPR)) ^ (row & 7)) * 16);
+              const char* f1 = stage + row * 128 + (((2 * (lane % LPR) + 1) ^ (row & 7)) * 16);
+              if (j * 32 + 8 <= cols) {
+                f32x4 lo = *reinterpret_cast<const f32x4*>(f0), hi = *reinterpret_cast<const f32x4*>(f1);
+                if constexpr (WIDE) {
+                  f32x4_any* d = reinterpret_cast<f32x4_any*>(at);
+                  if (g.accumulate) {
+                    lo += d[0];
+                    hi += d[1];
+                  }
+                  d[0] = lo;
+                  d[1] = hi;
+                } else {
+                  u16x8_any* d = reinterpret_cast<u16x8_any*>(at);
+                  const u16x8 u = *d;
+                  const bool bf = g.c_dtype == MUON_DTYPE_BF16;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    lo[e] += bf ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
+                    hi[e] += bf ? bf16_bits_to_f32(u[4 + e]) : f16_bits_to_f32(u[4 + e]);
+                  }
+                  const u16x4 x = bf ? round4<__bf16>(lo[0], lo[1], lo[2], lo[3]) : round4<_Float16>(lo[0], lo[1], lo[2], lo[3]);
+                  const u16x4 y = bf ? round4<__bf16>(hi[0], hi[1], hi[2], hi[3]) : round4<_Float16>(hi[0], hi[1], hi[2], hi[3]);
+                  *d = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+                }
+              } else {
+#pragma unroll 1
+                for (int e = 0; e < cols - j * 32; ++e) {
+                  float x = reinterpret_cast<const float*>(e < 4 ? f0 : f1)[e & 3];
+                  if (g.accumulate) x += load_c(at, g.c_dtype, e);
+                  store_c(at, g.c_dtype, e, x);
+                }
+              }
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        c += step * (RS / RPP);
+        asm volatile("" : "+v"(c));   // one row's address at a time: computed ahead they fill the registers
+      }
+    }
+  };
+
+  int index = blockIdx.x;
+  if (index >= total) return;
+  Tile cur = tile_at(index);
+  int slot = 0;   // the part of `scales` in use
+  scales_of(slot, cur, cur.kb0 >> 4, true);
+  load_slice(buf0, cur.a, cur.b, cur.na, cur.nb, cur.kb0, cur.kb1, 0);
+  load_slice(buf1, cur.a, cur.b, cur.na, cur.nb, cur.kb0, cur.kb1, 1);
+  publish();
+  read_scales(0, slot, cur.kb0);
+  read(0, buf0);
+  for (;;) {
+    index += gridDim.x;
+    const bool more = index < total;
+    Tile nxt = cur;
+    if (more) nxt = tile_at(index);
+    else nxt.na = nxt.nb = 0;   // fetched as zeros, never used
+    const int n = slices_of(cur);
+    int t = 0, kb = cur.kb0;
+    bool fetched = false;   // the next tile's first scales
+    while (t < n) {
       // the scales behind this part's; their place was last read before the last barrier
       const int part = kb >> 4;
-      load_scales(part + 1);
-      for (; t < nk && (kb >> 4) == part; t += 2, kb += 2) {
+      fetched = ((cur.kb0 + n - 1) >> 4) == part;
+      if (fetched) scales_of(slot ^ 1, nxt, nxt.kb0 >> 4, more);
+      else scales_of(slot ^ 1, cur, part + 1, true);
+      for (; t < n && (kb >> 4) == part; t += 2, kb += 2) {
+        // the slices after next: the next tile's behind the last ones
+        const bool last = t + 2 >= n;
+        const uint8_t* la = last ? nxt.a : cur.a;
+        const uint8_t* lb = last ? nxt.b : cur.b;
+        const int lna = last ? nxt.na : cur.na, lnb = last ? nxt.nb : cur.nb;
+        const int lk0 = last ? nxt.kb0 : cur.kb0, lk1 = last ? nxt.kb1 : cur.kb1, ls = last ? 0 : t + 2;
         // slice t, first period
         read(1, buf0);
+        mask_scales(0, kb < cur.kb1);
         multiply(Int<0>{}, Int<0>{});
         schedule(Int<0>{});
         publish();
         // second period: slice t + 1 is there, buf0 is free
-        read_scales(1, kb + 1);
+        read_scales(1, ((kb + 1) >> 4) == part ? slot : slot ^ 1, kb + 1);
         read(0, buf1);
-        load_slice(buf0, t + 2);
+        load_slice(buf0, la, lb, lna, lnb, lk0, lk1, ls);
         multiply(Int<1>{}, Int<0>{});
         schedule(Int<1>{});
         // slice t + 1
         read(1, buf1);
+        mask_scales(1, kb + 1 < cur.kb1);
         multiply(Int<0>{}, Int<1>{});
         schedule(Int<0>{});
         publish();
-        read_scales(0, kb + 2);
+        read_scales(0, !last && ((kb + 2) >> 4) == part ? slot : slot ^ 1, last ? nxt.kb0 : kb + 2);
         read(0, buf0);
-        load_slice(buf1, t + 3);
+        load_slice(buf1, la, lb, lna, lnb, lk0, lk1, ls + 1);
         multiply(Int<1>{}, Int<1>{});
         schedule(Int<1>{});
       }
+      slot ^= 1;
     }
-    // the last loads land before the buffers are used again
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  }
-
-  // Results: 32 rows of a wave at a time through its own part of LDS, then whole rows,
-  // 16 bytes per lane where the rows are aligned for it.
-  constexpr int SP = HALF + 4;
-  float* stage = reinterpret_cast<float*>((wave < 2 ? buf0 : buf1) + (wave & 1) * SLICE);
-  static_assert(32 * SP * 4 <= SLICE, "staging fits");
-  const int64_t cbase = g.mode == FP8_GROUP_ROWS ? 0 : w.mat * g.c_batch;
-  const int64_t nw = n0 + wn * HALF;
-  const int ncols = static_cast<int>(max<int64_t>(0, min<int64_t>(HALF, g.N - nw)));
-#pragma unroll
-  for (int i = 0; i < WB; ++i) {
-    const int64_t mw = m0 + wm * HALF + i * 32;
-    const int rows = static_cast<int>(max<int64_t>(0, min<int64_t>(32, w.mend - mw)));
-#pragma unroll
-    for (int j = 0; j < WB; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<f32x4*>(stage + r * SP + j * 32 + 8 * e + 4 * h) =
-            f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (g.c_vec && ncols == HALF) {
-      constexpr int LPR = HALF / 8, RPP = 64 / LPR;
-      const int col = (lane % LPR) * 8;
-#pragma unroll
-      for (int p = 0; p < 32 / RPP; ++p) {
-        const int row = p * RPP + lane / LPR;
-        if (row < rows) {
-          float v[8];
-          const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + row * SP + col);
-          const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + row * SP + col + 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) { v[e] = lo[e]; v[4 + e] = hi[e]; }
-          store_row8<WIDE>(g, cbase + (mw + row) * g.ldc + nw + col, v);
-        }
-      }
-    } else {
-      for (int row = 0; row < rows; ++row) {
-        const int64_t at = cbase + (mw + row) * g.ldc + nw;
-        for (int col = lane; col < ncols; col += 64) {
-          float v = stage[row * SP + col];
-          if (g.accumulate) v += load_c(g.c, g.c_dtype, at + col);
-          store_c(g.c, g.c_dtype, at + col, v);
-        }
-      }
+    if (!fetched) {   // the last slice alone reached into a new part (which is in `slot`)
+      scales_of(slot ^ 1, nxt, nxt.kb0 >> 4, more);
+      publish();
+      slot ^= 1;
+      read_scales(0, slot, nxt.kb0);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    // no load may be on its way into LDS when the workgroup ends
+    if (!more) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    store(cur);
+    if (!more) return;
+    cur = nxt;
   }
 }
 
-template <int FA, int FB, bool WIDE, int TILE>
-__global__ __launch_bounds__(256, TILE == 256 ? 1 : 2) void fp8_tile_kernel(Fp8Gemm g, int mtiles, int ntiles,
-                                                                           int total) {
-  tile_product<FA, FB, WIDE, TILE>(g, mtiles, ntiles, total);
+template <int FA, int FB, int OUT, int TILE>
+__global__ __launch_bounds__(256, TILE == 256 ? 1 : 2) void fp8_tile_kernel(Fp8Gemm g, int mtiles, int ntiles) {
+  tile_product<FA, FB, OUT, TILE>(g, mtiles, ntiles);
 }
 
 // Which kernel a product takes.
@@ -563,7 +705,15 @@ Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t, int32_t mode, int64_t batch
   return {FP8_TILE_128, 1};
 }
 
-template <int FA, int FB, bool WIDE>
+template <int FA, int FB, int OUT>
+static void launch_tiles(const Fp8Plan& p, const Fp8Gemm& g, int64_t total, int m, int n, hipStream_t s) {
+  if (p.kind == FP8_TILE_128)   // two workgroups per CU, walking over the tiles
+    hipLaunchKernelGGL((fp8_tile_kernel<FA, FB, OUT, 128>), dim3(std::min<int64_t>(total, 512)), dim3(256), 0, s, g, m, n);
+  else                          // one per CU
+    hipLaunchKernelGGL((fp8_tile_kernel<FA, FB, OUT, 256>), dim3(std::min<int64_t>(total, 256)), dim3(256), 0, s, g, m, n);
+}
+
+template <int FA, int FB>
 static hipError_t launch(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
   const int tm = p.kind == FP8_FEW_ROWS ? 16 : p.kind == FP8_TILE_128 ? 128 : 256;
   const int64_t nt = (g.N + tm - 1) / tm;
@@ -575,25 +725,27 @@ static hipError_t launch(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
   const int64_t total = mt * nt * z;
   if (total <= 0) return hipSuccess;
   if (total > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(total));
   const int m = static_cast<int>(mt), n = static_cast<int>(nt);
-  if (p.kind == FP8_FEW_ROWS)
-    hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, WIDE>), grid, dim3(64 * kFewWaves), 0, s, g, m, n);
-  else if (p.kind == FP8_TILE_128)
-    hipLaunchKernelGGL((fp8_tile_kernel<FA, FB, WIDE, 128>), grid, dim3(256), 0, s, g, m, n, static_cast<int>(total));
-  else
-    hipLaunchKernelGGL((fp8_tile_kernel<FA, FB, WIDE, 256>), grid, dim3(256), 0, s, g, m, n, static_cast<int>(total));
+  const bool wide = g.c_dtype == MUON_DTYPE_F32;
+  if (p.kind == FP8_FEW_ROWS) {
+    const dim3 grid(static_cast<unsigned>(total)), block(64 * kFewWaves);
+    if (wide) hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, true>), grid, block, 0, s, g, m, n);
+    else hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, false>), grid, block, 0, s, g, m, n);
+  } else if (wide) {
+    launch_tiles<FA, FB, OUT_F32>(p, g, total, m, n, s);
+  } else if (g.accumulate) {
+    launch_tiles<FA, FB, OUT_ADD_16>(p, g, total, m, n, s);
+  } else if (g.c_dtype == MUON_DTYPE_BF16) {
+    launch_tiles<FA, FB, OUT_BF16>(p, g, total, m, n, s);
+  } else {
+    launch_tiles<FA, FB, OUT_F16>(p, g, total, m, n, s);
+  }
   return hipGetLastError();
 }
 
-template <int FA, int FB>
-static hipError_t launch_dtype(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
-  return g.c_dtype == MUON_DTYPE_F32 ? launch<FA, FB, true>(p, g, s) : launch<FA, FB, false>(p, g, s);
-}
-
 hipError_t launch_fp8_gemm(int fmt_a, int fmt_b, const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
-  if (fmt_a == MUON_FP8_E4M3) return fmt_b == MUON_FP8_E4M3 ? launch_dtype<0, 0>(p, g, s) : launch_dtype<0, 1>(p, g, s);
-  return fmt_b == MUON_FP8_E4M3 ? launch_dtype<1, 0>(p, g, s) : launch_dtype<1, 1>(p, g, s);
+  if (fmt_a == MUON_FP8_E4M3) return fmt_b == MUON_FP8_E4M3 ? launch<0, 0>(p, g, s) : launch<0, 1>(p, g, s);
+  return fmt_b == MUON_FP8_E4M3 ? launch<1, 0>(p, g, s) : launch<1, 1>(p, g, s);
 }
 
 hipError_t launch_fp8_reduce(const Fp8Gemm&, hipStream_t) { return hipSuccess; }
