@@ -273,6 +273,14 @@ __device__ __forceinline__ int row_swizzle(int r) { return (r ^ ((r >> 3) & 3)) 
 
 template <int V> using Int = std::integral_constant<int, V>;
 
+template <int N, typename F>
+__device__ __forceinline__ void each_step(F&& f) {
+  if constexpr (N > 0) {
+    each_step<N - 1>(f);
+    f(Int<N - 1>{});
+  }
+}
+
 // 16 bytes of results at any element-aligned place
 typedef u16x8 u16x8_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
@@ -409,13 +417,15 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
                 any ? static_cast<int>(min<int64_t>(TILE, g.N - t.n0)) : 0, part);
   };
 
-  f32x16 acc[WB][WB];   // zeros again once a tile is stored
+  f32x16 acc[WB][WB];
+  auto clear = [&]() {
 #pragma unroll
-  for (int i = 0; i < WB; ++i)
+    for (int i = 0; i < WB; ++i)
 #pragma unroll
-    for (int j = 0; j < WB; ++j)
+      for (int j = 0; j < WB; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  };
   i32x4 fa[2][WB][2], fb[2][WB][2];
   auto read = [&](int set, const char* from) {   // set = period of the slice
 #pragma unroll
@@ -507,15 +517,75 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   // row. Register 4 q + e of block (i, j) in lane l is row l % 32, column 8 q + 4 (l / 32)
   // + e of the block. 16-bit results are rounded before (TILE / 128 blocks together), fp32
   // ones and sums with what is there pass in fp32, 32 rows of a block (128-tiles: 16) at a
-  // time.
+  // time. LDS keeps a wave's order, so the next blocks are written behind the reads of
+  // these without a wait. Whole tiles take no masks: with a branch per store, each waiting
+  // for its own read, a tile took 7 us to leave.
+  constexpr bool ROUNDED = OUT == OUT_BF16 || OUT == OUT_F16;
+  constexpr int NB = ROUNDED ? TILE / 128 : 1;          // blocks at a time
+  constexpr int RS = ROUNDED ? 32 : STAGE / 128;        // rows at a time
+  constexpr int CH = ROUNDED ? 4 * NB : 8;              // chunks of a staged row
+  constexpr int LPR = ROUNDED ? CH : 4, RPP = 64 / LPR; // lanes per row (8 columns each), rows per pass
+  constexpr int NP = RS / RPP;                          // passes
+  constexpr int ESZ = WIDE ? 4 : 2;
+  constexpr int NS = 32 / RS, NJ = WB / NB;             // steps: rows of a row of blocks, groups of blocks
   char* stage = stages + wave * STAGE;
+  auto stage_write = [&](auto step) {
+    constexpr int I = decltype(step)::value / (NS * NJ), S = decltype(step)::value / NJ % NS,
+                  J = decltype(step)::value % NJ * NB;
+    // the blocks stay in accumulation registers until here
+    if constexpr (TILE == 256) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) asm volatile("" : "+a"(acc[I][J + b]));
+    }
+    if (RS == 32 || (r >> 4) == S) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& x = acc[I][J + b];
+          if constexpr (ROUNDED) {
+            using T = std::conditional_t<OUT == OUT_BF16, __bf16, _Float16>;
+            *reinterpret_cast<u16x4*>(stage + r * (CH * 16) + (((b * 4 + q) ^ (r & (CH - 1))) * 16) + h * 8) =
+                round4<T>(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+          } else {
+            *reinterpret_cast<f32x4*>(stage + (r % RS) * 128 + (((2 * q + h) ^ (r & 7)) * 16)) =
+                f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+          }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  // what a lane takes out of LDS per pass: 8 rounded results, or 8 in fp32
+  struct Taken {
+    u16x8 u;
+    f32x4 lo, hi;
+  };
+  auto stage_read = [&](Taken (&to)[NP]) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const int row = p * RPP + lane / LPR;
+      if constexpr (ROUNDED) {
+        to[p].u = *reinterpret_cast<const u16x8*>(stage + row * (CH * 16) + (((lane % LPR) ^ (row & (CH - 1))) * 16));
+      } else {
+        to[p].lo = *reinterpret_cast<const f32x4*>(stage + row * 128 + (((2 * (lane % LPR)) ^ (row & 7)) * 16));
+        to[p].hi = *reinterpret_cast<const f32x4*>(stage + row * 128 + (((2 * (lane % LPR) + 1) ^ (row & 7)) * 16));
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  // 16-bit values of C added to 8 fp32 results
+  auto add_16 = [&](Taken& x, const u16x8& u) {
+    const bool bf = g.c_dtype == MUON_DTYPE_BF16;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x.lo[e] += bf ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
+      x.hi[e] += bf ? bf16_bits_to_f32(u[4 + e]) : f16_bits_to_f32(u[4 + e]);
+    }
+    const u16x4 y = bf ? round4<__bf16>(x.lo[0], x.lo[1], x.lo[2], x.lo[3]) : round4<_Float16>(x.lo[0], x.lo[1], x.lo[2], x.lo[3]);
+    const u16x4 z = bf ? round4<__bf16>(x.hi[0], x.hi[1], x.hi[2], x.hi[3]) : round4<_Float16>(x.hi[0], x.hi[1], x.hi[2], x.hi[3]);
+    x.u = __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
   auto store = [&](const Tile& t) {
-    constexpr bool ROUNDED = OUT == OUT_BF16 || OUT == OUT_F16;
-    constexpr int NB = ROUNDED ? TILE / 128 : 1;          // blocks at a time
-    constexpr int RS = ROUNDED ? 32 : STAGE / 128;        // rows at a time
-    constexpr int CH = ROUNDED ? 4 * NB : 8;              // chunks of a staged row
-    constexpr int LPR = ROUNDED ? CH : 4, RPP = 64 / LPR; // lanes per row (8 columns each), rows per pass
-    constexpr int ESZ = WIDE ? 4 : 2;
     const int col = (lane % LPR) * 8;
     const int rows = t.mend - (t.m0 + wm * HALF) - lane / LPR;          // beyond the lane's first row
     const int cols = static_cast<int>(g.N - (t.n0 + wn * HALF)) - col;  // beyond the lane's first column
@@ -523,98 +593,94 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
               ((g.mode == FP8_GROUP_ROWS ? 0 : t.mat * g.c_batch) + (t.m0 + wm * HALF + lane / LPR) * g.ldc + t.n0 +
                wn * HALF + col) * ESZ;
     const int64_t step = RPP * g.ldc * ESZ;   // bytes from pass to pass
+    const bool whole = t.mend - t.m0 >= TILE && g.N - t.n0 >= TILE;
+    const bool add = OUT == OUT_ADD_16 || (WIDE && g.accumulate);
+    stage_write(Int<0>{});
+    auto steps = [&](auto masked) {
+      constexpr bool MASKED = decltype(masked)::value != 0;
+      each_step<WB * NS * NJ>([&](auto number) {
+        constexpr int K = decltype(number)::value, J = K % NJ * NB, ROW = K / (NS * NJ) * 32 + K / NJ % NS * RS;
+        Taken v[NP];
+        // whole tiles: what is added comes while LDS is read
+        [[maybe_unused]] f32x4 plo[NP], phi[NP];
+        [[maybe_unused]] u16x8 pu[NP];
+        if constexpr (!MASKED && !ROUNDED) {
+          if (add) {
+            const char* from = c + J * 32 * ESZ;
 #pragma unroll
-    for (int i = 0; i < WB; ++i) {
-#pragma unroll
-      for (int s = 0; s < 32 / RS; ++s) {
-#pragma unroll
-        for (int j = 0; j < WB; j += NB) {
-          // the blocks stay in accumulation registers until here
-          if constexpr (TILE == 256) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) asm volatile("" : "+a"(acc[i][j + b]));
-          }
-          if (RS == 32 || (r >> 4) == s) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const f32x16& x = acc[i][j + b];
-                if constexpr (ROUNDED) {
-                  using T = std::conditional_t<OUT == OUT_BF16, __bf16, _Float16>;
-                  *reinterpret_cast<u16x4*>(stage + r * (CH * 16) + (((b * 4 + q) ^ (r & (CH - 1))) * 16) + h * 8) =
-                      round4<T>(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-                } else {
-                  *reinterpret_cast<f32x4*>(stage + (r % RS) * 128 + (((2 * q + h) ^ (r & 7)) * 16)) =
-                      f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-                }
+            for (int p = 0; p < NP; ++p, from += step) {
+              if constexpr (WIDE) {
+                plo[p] = reinterpret_cast<const f32x4_any*>(from)[0];
+                phi[p] = reinterpret_cast<const f32x4_any*>(from)[1];
+              } else {
+                pu[p] = *reinterpret_cast<const u16x8_any*>(from);
               }
+            }
           }
-          __builtin_amdgcn_wave_barrier();
-          if (s == 32 / RS - 1) {
+        }
+        stage_read(v);
+        if constexpr (!MASKED && K + 1 < WB * NS * NJ) stage_write(Int<K + 1>{});
+        char* to = c + J * 32 * ESZ;
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) acc[i][j + b][e] = 0.0f;
-          }
-          char* to = c;
-#pragma unroll
-          for (int p = 0; p < RS / RPP; ++p, to += step) {
-            const int row = p * RPP + lane / LPR, done = i * 32 + s * RS + p * RPP;
-            if (done >= rows || j * 32 >= cols) continue;
-            char* at = to + j * 32 * ESZ;
+        for (int p = 0; p < NP; ++p, to += step) {
+          if constexpr (!MASKED) {
             if constexpr (ROUNDED) {
-              const char* from = stage + row * (CH * 16) + (((lane % LPR) ^ (row & (CH - 1))) * 16);
-              if (j * 32 + 8 <= cols) {
-                *reinterpret_cast<u16x8_any*>(at) = *reinterpret_cast<const u16x8*>(from);
-              } else {
-#pragma unroll 1
-                for (int e = 0; e < cols - j * 32; ++e)
-                  reinterpret_cast<unsigned short*>(at)[e] = reinterpret_cast<const unsigned short*>(from)[e];
+              *reinterpret_cast<u16x8_any*>(to) = v[p].u;
+            } else if constexpr (WIDE) {
+              if (add) {
+                v[p].lo += plo[p];
+                v[p].hi += phi[p];
               }
+              reinterpret_cast<f32x4_any*>(to)[0] = v[p].lo;
+              reinterpret_cast<f32x4_any*>(to)[1] = v[p].hi;
             } else {
-              const char* f0 = stage + row * 128 + (((2 * (lane % LPR)) ^ (row & 7)) * 16);
-              const char* f1 = stage + row * 128 + (((2 * (lane % LPR) + 1) ^ (row & 7)) * 16);
-              if (j * 32 + 8 <= cols) {
-                f32x4 lo = *reinterpret_cast<const f32x4*>(f0), hi = *reinterpret_cast<const f32x4*>(f1);
-                if constexpr (WIDE) {
-                  f32x4_any* d = reinterpret_cast<f32x4_any*>(at);
-                  if (g.accumulate) {
-                    lo += d[0];
-                    hi += d[1];
-                  }
-                  d[0] = lo;
-                  d[1] = hi;
-                } else {
-                  u16x8_any* d = reinterpret_cast<u16x8_any*>(at);
-                  const u16x8 u = *d;
-                  const bool bf = g.c_dtype == MUON_DTYPE_BF16;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    lo[e] += bf ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
-                    hi[e] += bf ? bf16_bits_to_f32(u[4 + e]) : f16_bits_to_f32(u[4 + e]);
-                  }
-                  const u16x4 x = bf ? round4<__bf16>(lo[0], lo[1], lo[2], lo[3]) : round4<_Float16>(lo[0], lo[1], lo[2], lo[3]);
-                  const u16x4 y = bf ? round4<__bf16>(hi[0], hi[1], hi[2], hi[3]) : round4<_Float16>(hi[0], hi[1], hi[2], hi[3]);
-                  *d = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+              add_16(v[p], pu[p]);
+              *reinterpret_cast<u16x8_any*>(to) = v[p].u;
+            }
+          } else if (ROW + p * RPP < rows && J * 32 < cols) {
+            if (J * 32 + 8 <= cols) {
+              if constexpr (WIDE) {
+                f32x4_any* d = reinterpret_cast<f32x4_any*>(to);
+                if (add) {
+                  v[p].lo += d[0];
+                  v[p].hi += d[1];
                 }
+                d[0] = v[p].lo;
+                d[1] = v[p].hi;
               } else {
+                if constexpr (!ROUNDED) add_16(v[p], *reinterpret_cast<const u16x8_any*>(to));
+                *reinterpret_cast<u16x8_any*>(to) = v[p].u;
+              }
+            } else {   // the matrix's last columns, one by one out of LDS
+              const int row = p * RPP + lane / LPR;
 #pragma unroll 1
-                for (int e = 0; e < cols - j * 32; ++e) {
-                  float x = reinterpret_cast<const float*>(e < 4 ? f0 : f1)[e & 3];
-                  if (g.accumulate) x += load_c(at, g.c_dtype, e);
-                  store_c(at, g.c_dtype, e, x);
+              for (int e = 0; e < cols - J * 32; ++e) {
+                if constexpr (ROUNDED) {
+                  reinterpret_cast<unsigned short*>(to)[e] = reinterpret_cast<const unsigned short*>(
+                      stage + row * (CH * 16) + (((lane % LPR) ^ (row & (CH - 1))) * 16))[e];
+                } else {
+                  float x = reinterpret_cast<const float*>(
+                      stage + row * 128 + (((2 * (lane % LPR) + e / 4) ^ (row & 7)) * 16))[e & 3];
+                  if (add) x += load_c(to, g.c_dtype, e);
+                  store_c(to, g.c_dtype, e, x);
                 }
               }
             }
           }
-          __builtin_amdgcn_wave_barrier();
-          __builtin_amdgcn_sched_barrier(0);
         }
-        c += step * (RS / RPP);
-        asm volatile("" : "+v"(c));   // one row's address at a time: computed ahead they fill the registers
-      }
-    }
+        if constexpr (MASKED && K + 1 < WB * NS * NJ) {
+          __builtin_amdgcn_wave_barrier();
+          stage_write(Int<K + 1>{});
+        }
+        if constexpr (K % NJ == NJ - 1) {
+          c += step * NP;
+          asm volatile("" : "+v"(c));   // one row's address at a time: computed ahead they fill the registers
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    if (whole) steps(Int<0>{});
+    else steps(Int<1>{});
   };
 
   int index = blockIdx.x;
@@ -627,6 +693,7 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   publish();
   read_scales(0, slot, cur.kb0);
   read(0, buf0);
+  clear();
   for (;;) {
     index += gridDim.x;
     const bool more = index < total;
@@ -686,6 +753,7 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
     store(cur);
     if (!more) return;
     cur = nxt;
+    clear();
   }
 }
 
