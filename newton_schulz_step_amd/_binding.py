@@ -546,22 +546,47 @@ def profile_end() -> Dict[str, Tuple[int, float]]:
 
 # ----------------------------------------------------------------------------- 8-bit operands and experts
 
+_FP8_TYPES = None
+
+
 def _fp8_types():
-    torch = _torch()
-    return {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+    global _FP8_TYPES
+    if _FP8_TYPES is None:
+        torch = _torch()
+        _FP8_TYPES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+    return _FP8_TYPES
+
+
+def _same_device(first, *others):
+    """The GPU that `first` and the others (None skipped) live on."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to libmuonstep must be on a GPU")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors passed to libmuonstep must share one GPU, got {dev} and {t.device}")
+    return dev
+
+
+def _flat(t) -> Optional[int]:
+    """Pointer of a contiguous tensor whose device is checked elsewhere (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmuonstep must be contiguous")
+    return t.data_ptr()
 
 
 def _last_dense(t, name):
     """(pointer, row pitch, batch stride) of a 2-D or 3-D tensor whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU")
-    if t.dim() not in (2, 3):
-        raise ValueError(f"{name} must be a matrix or a batch of matrices")
     shape, stride = t.shape, t.stride()
+    n = len(shape)
+    if n != 2 and n != 3:
+        raise ValueError(f"{name} must be a matrix or a batch of matrices")
     if shape[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     ld = stride[-2] if shape[-2] > 1 else shape[-1]
-    bs = stride[0] if t.dim() == 3 and shape[0] > 1 else 0
+    bs = stride[0] if n == 3 and shape[0] > 1 else 0
     return t.data_ptr(), ld, bs
 
 
@@ -570,30 +595,32 @@ class _on:
     allocates belong to that stream. A raw stream handle has no torch allocator,
     so it takes calls whose outputs are given (`fresh` then refuses)."""
 
+    __slots__ = ("dev", "raw", "handle", "_ctx", "_stream")
+
     def __init__(self, dev, stream):
         torch = _torch()
-        self.dev, self.raw = dev, stream is not None and not isinstance(stream, torch.cuda.Stream)
-        self._ctx = torch.cuda.stream(stream) if stream is not None and not self.raw else torch.cuda.device(dev)
-        self._same = stream is None and torch.cuda.current_device() == dev.index
-        if stream is not None and not self.raw and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self._stream = stream
+        self.dev, self.raw, self._ctx, self._stream = dev, False, None, stream
+        if stream is None:
+            if torch.cuda.current_device() != dev.index:
+                self._ctx = torch.cuda.device(dev)
+        elif isinstance(stream, torch.cuda.Stream):
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            self._ctx = torch.cuda.stream(stream)
+        else:
+            self.raw, self._ctx = True, torch.cuda.device(dev)
 
     def __enter__(self):
-        torch = _torch()
-        if not self._same:
+        if self._ctx is not None:
             self._ctx.__enter__()
-            if self.raw:
-                self.handle = int(self._stream)
-                return self
-        self.handle = torch.cuda.current_stream(self.dev).cuda_stream
+        self.handle = int(self._stream) if self.raw else _torch()._C._cuda_getCurrentRawStream(self.dev.index)
         return self
 
     def __exit__(self, *exc):
-        if not self._same:
+        if self._ctx is not None:
             self._ctx.__exit__(*exc)
 
-    def fresh(self, *shape, dtype):
+    def fresh(self, shape, dtype):
         if self.raw:
             raise ValueError("with a raw stream handle the outputs must be given")
         return _torch().empty(shape, dtype=dtype, device=self.dev)
@@ -637,8 +664,16 @@ class Fp8:
 
     def _c(self) -> Fp8Operand:
         d = self.data
-        return Fp8Operand(_ptr(d), _ptr(self.scale), d.shape[0] if d.dim() == 3 else 1, d.shape[-2], self.cols,
+        shape = d.shape
+        return Fp8Operand(_flat(d), _flat(self.scale), shape[0] if len(shape) == 3 else 1, shape[-2], self.cols,
                           _fp8_types()[d.dtype], 0)
+
+    @classmethod
+    def _of(cls, data, scale, cols):
+        """Parts that are known to fit."""
+        self = cls.__new__(cls)
+        self.data, self.scale, self.cols = data, scale, cols
+        return self
 
 
 def fp8_empty(rows: int, cols: int, fmt: str = "e4m3", device="cuda", batch: Optional[int] = None) -> Fp8:
@@ -651,7 +686,7 @@ def fp8_empty(rows: int, cols: int, fmt: str = "e4m3", device="cuda", batch: Opt
     dt = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
     data = torch.empty(lead + (rows, pitch), dtype=dt, device=device)
     scale = torch.empty(lead + (rows, -(-(pitch // FP8_BLOCK) // 4) * 4), dtype=torch.float8_e8m0fnu, device=device)
-    return Fp8(data, scale, cols)
+    return Fp8._of(data, scale, cols)
 
 
 def fp8_quantize(x, fmt: str = "e4m3", blocks: bool = False, transposed="no", row_index=None, row_div: int = 1,
@@ -677,7 +712,7 @@ def fp8_quantize(x, fmt: str = "e4m3", blocks: bool = False, transposed="no", ro
     batch = x.shape[0] if x.dim() == 3 else None
     cols = x.shape[-1]
     rows = x.shape[-2] if row_index is None else row_index.numel()
-    dev = _device(x, row_index, row_weight, *(t for o in (out, out_t) if o is not None for t in (o.data, o.scale)))
+    dev = _same_device(x, row_index, row_weight, *(t for o in (out, out_t) if o is not None for t in (o.data, o.scale)))
     with _on(dev, stream) as on:
         def make(r, c):
             if on.raw:
@@ -689,7 +724,7 @@ def fp8_quantize(x, fmt: str = "e4m3", blocks: bool = False, transposed="no", ro
             if o is not None and o.format != fmt:
                 raise ValueError(f"outputs are {o.format}, the call asks for {fmt}")
         src = Fp8Source(ptr, bs, ld, 1 if batch is None else batch, x.shape[-2], cols, _dtype_code(x), row_div,
-                        _ptr(row_index), rows, _ptr(row_weight), 0 if row_weight is None else row_weight.numel())
+                        _flat(row_index), rows, _flat(row_weight), 0 if row_weight is None else row_weight.numel())
         _check(load().muon_fp8_quantize(ctypes.byref(src), int(bool(blocks)),
                                         None if q is None else ctypes.byref(q._c()),
                                         None if qt is None else ctypes.byref(qt._c()), on.handle))
@@ -702,7 +737,7 @@ def _result(out, shape, on, out_dtype, accumulate):
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = on.fresh(*shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+        out = on.fresh(shape, torch.bfloat16 if out_dtype is None else out_dtype)
     elif tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
     elif out_dtype is not None and out.dtype != out_dtype:
@@ -732,7 +767,7 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=None, accumulate: bool = Fals
         if a.data.dim() != b.data.dim():
             raise ValueError("a and b must both be single matrices or both be batches")
         shape = tuple(a.data.shape[:-1]) + (b.rows,)
-    dev = _device(a.data, a.scale, b.data, b.scale, out, offsets)
+    dev = _same_device(a.data, a.scale, b.data, b.scale, out, offsets)
     lib = load()
     with _on(dev, stream) as on:
         ca, cb = a._c(), b._c()
@@ -741,7 +776,7 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=None, accumulate: bool = Fals
                                                   ctypes.byref(need)))
         out, c = _result(out, shape, on, out_dtype, accumulate)
         ws = on.scratch(need.value)
-        _check(lib.muon_fp8_matmul(ctypes.byref(ca), ctypes.byref(cb), _ptr(offsets), ctypes.byref(c), _ptr(ws),
+        _check(lib.muon_fp8_matmul(ctypes.byref(ca), ctypes.byref(cb), _flat(offsets), ctypes.byref(c), _flat(ws),
                                    0 if ws is None else ws.numel(), on.handle))
     return out
 
@@ -754,10 +789,10 @@ def fp8_matmul_grouped_k(a: Fp8, b: Fp8, offsets, out=None, out_dtype=None, accu
     groups = offsets.numel() - 1
     if groups < 0 or a.data.dim() != 2 or b.data.dim() != 2:
         raise ValueError("a grouped contraction takes single matrices and groups + 1 offsets")
-    dev = _device(a.data, a.scale, b.data, b.scale, out, offsets)
+    dev = _same_device(a.data, a.scale, b.data, b.scale, out, offsets)
     with _on(dev, stream) as on:
         out, c = _result(out, (groups, a.rows, b.rows), on, out_dtype, accumulate)
-        _check(load().muon_fp8_matmul_grouped_k(ctypes.byref(a._c()), ctypes.byref(b._c()), _ptr(offsets), groups,
+        _check(load().muon_fp8_matmul_grouped_k(ctypes.byref(a._c()), ctypes.byref(b._c()), _flat(offsets), groups,
                                                 ctypes.byref(c), on.handle))
     return out
 
@@ -784,7 +819,7 @@ def _logits(t):
 
 def _given(t, shape, dtype, on, name):
     if t is None:
-        return on.fresh(*shape, dtype=dtype)
+        return on.fresh(shape, dtype)
     if t.dtype != dtype or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
     return t
@@ -797,13 +832,13 @@ def route(logits, h: RouteHyper, bias=None, ids=None, weights=None, stream=None)
     tokens, experts = logits.shape
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != experts):
         raise ValueError("bias must be float32 with one element per expert")
-    dev = _device(logits, bias, ids, weights)
+    dev = _same_device(logits, bias, ids, weights)
     with _on(dev, stream) as on:
         k = max(h.top_k, 0)
         ids = _given(ids, (tokens, k), torch.int32, on, "ids")
         weights = _given(weights, (tokens, k), torch.float32, on, "weights")
-        _check(load().muon_route(ptr, _dtype_code(logits), tokens, experts, ld, _ptr(bias), ctypes.byref(h), _ptr(ids),
-                                 _ptr(weights), on.handle))
+        _check(load().muon_route(ptr, _dtype_code(logits), tokens, experts, ld, _flat(bias), ctypes.byref(h), _flat(ids),
+                                 _flat(weights), on.handle))
     return ids, weights
 
 
@@ -816,11 +851,11 @@ def route_backward(dweights, logits, ids, h: RouteHyper, dlogits=None, stream=No
         raise ValueError(f"dweights must be float32 of shape {(tokens, h.top_k)}")
     if ids.dtype != torch.int32 or tuple(ids.shape) != (tokens, h.top_k):
         raise ValueError(f"ids must be int32 of shape {(tokens, h.top_k)}")
-    dev = _device(dweights, logits, ids, dlogits)
+    dev = _same_device(dweights, logits, ids, dlogits)
     with _on(dev, stream) as on:
         dlogits = _given(dlogits, (tokens, experts), logits.dtype, on, "dlogits")
         dptr, ldd, _ = _last_dense(dlogits, "dlogits")
-        _check(load().muon_route_backward(_ptr(dweights), ptr, _dtype_code(logits), tokens, experts, ld, _ptr(ids),
+        _check(load().muon_route_backward(_flat(dweights), ptr, _dtype_code(logits), tokens, experts, ld, _flat(ids),
                                           ctypes.byref(h), dptr, ldd, on.handle))
     return dlogits
 
@@ -832,7 +867,7 @@ def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=Non
     torch = _torch()
     _int32(ids, None, "ids")
     n = ids.numel()
-    dev = _device(ids, offsets, counts, rows, pos)
+    dev = _same_device(ids, offsets, counts, rows, pos)
     lib = load()
     with _on(dev, stream) as on:
         need = ctypes.c_size_t(0)
@@ -840,13 +875,13 @@ def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=Non
         offsets = _given(offsets, (n_experts + 1,), torch.int32, on, "offsets")
         counts = _given(counts, (n_experts,), torch.int32, on, "counts")
         if rows is None:
-            rows = on.fresh(max(n + n_experts * (align - 1), 0), dtype=torch.int32)
+            rows = on.fresh((max(n + n_experts * (align - 1), 0),), torch.int32)
         else:
             _int32(rows, None, "rows")
         pos = _given(pos, ids.shape, torch.int32, on, "pos")
         ws = on.scratch(need.value)
-        _check(lib.muon_expert_order(_ptr(ids), n, n_experts, align, _ptr(offsets), _ptr(counts), _ptr(rows),
-                                     rows.numel(), _ptr(pos), _ptr(ws), 0 if ws is None else ws.numel(), on.handle))
+        _check(lib.muon_expert_order(_flat(ids), n, n_experts, align, _flat(offsets), _flat(counts), _flat(rows),
+                                     rows.numel(), _flat(pos), _flat(ws), 0 if ws is None else ws.numel(), on.handle))
     return offsets, counts, rows, pos
 
 
@@ -866,11 +901,11 @@ def combine(o, pos, weights, out=None, stream=None):
     _slots(o, pos, weights)
     optr, ldo, _ = _last_dense(o, "o")
     tokens, k = pos.shape
-    dev = _device(o, pos, weights, out)
+    dev = _same_device(o, pos, weights, out)
     with _on(dev, stream) as on:
         out = _given(out, (tokens, o.shape[1]), o.dtype, on, "out")
         yptr, ldy, _ = _last_dense(out, "out")
-        _check(load().muon_combine(optr, _dtype_code(o), o.shape[0], o.shape[1], ldo, _ptr(pos), _ptr(weights), tokens,
+        _check(load().muon_combine(optr, _dtype_code(o), o.shape[0], o.shape[1], ldo, _flat(pos), _flat(weights), tokens,
                                    k, yptr, ldy, on.handle))
     return out
 
@@ -885,11 +920,11 @@ def combine_backward(dy, o, pos, weights, dweights=None, do=None, stream=None):
     tokens, k = pos.shape
     dyptr, lddy, _ = _last_dense(dy, "dy")
     optr, ldo, _ = _last_dense(o, "o")
-    dev = _device(dy, o, pos, weights, dweights, do)
+    dev = _same_device(dy, o, pos, weights, dweights, do)
     with _on(dev, stream) as on:
         dweights = _given(dweights, (tokens, k), torch.float32, on, "dweights")
-        do = on.fresh(*o.shape, dtype=o.dtype).zero_() if do is None else _given(do, o.shape, o.dtype, on, "do")
+        do = on.fresh(o.shape, o.dtype).zero_() if do is None else _given(do, o.shape, o.dtype, on, "do")
         doptr, lddo, _ = _last_dense(do, "do")
         _check(load().muon_combine_backward(dyptr, _dtype_code(dy), tokens, o.shape[1], lddy, optr, o.shape[0], ldo,
-                                            _ptr(pos), _ptr(weights), k, _ptr(dweights), doptr, lddo, on.handle))
+                                            _flat(pos), _flat(weights), k, _flat(dweights), doptr, lddo, on.handle))
     return dweights, do
