@@ -236,7 +236,7 @@ int muon_fp8_matmul_workspace_size(const muon_fp8_t* a, const muon_fp8_t* b, int
     const int st = check_matmul(a, b, grouped != 0);
     if (st != MUON_OK) return st;
     const Fp8Plan p = plan_fp8_gemm(a->rows, b->rows, fp8_data_pitch(a->cols) / MUON_FP8_BLOCK,
-                                    grouped ? FP8_GROUP_ROWS : FP8_DENSE, b->batch, true);
+                                    grouped ? FP8_GROUP_ROWS : FP8_DENSE, b->batch, false);
     *bytes_out = p.splits > 1 ? static_cast<size_t>(p.splits) * b->batch * a->rows * b->rows * 4 : 0;
     return MUON_OK;
   });
@@ -260,7 +260,7 @@ int muon_fp8_matmul(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* gro
     Fp8Gemm g = gemm_of(a, b, c, group_offsets);
     g.mode = grouped ? FP8_GROUP_ROWS : FP8_DENSE;
     g.batch = static_cast<int32_t>(b->batch);
-    const Fp8Plan p = plan_fp8_gemm(g.M, g.N, g.kb, g.mode, g.batch, workspace != nullptr);
+    const Fp8Plan p = plan_fp8_gemm(g.M, g.N, g.kb, g.mode, g.batch, g.c_dtype == MUON_DTYPE_F32);
     g.splits = p.splits;
     if (p.splits > 1) {
       const size_t need = static_cast<size_t>(p.splits) * g.batch * g.M * g.N * 4;
@@ -298,7 +298,7 @@ int muon_fp8_matmul_grouped_k(const muon_fp8_t* a, const muon_fp8_t* b, const in
     Fp8Gemm g = gemm_of(a, b, c, group_offsets);
     g.mode = FP8_GROUP_K;
     g.batch = n_groups;
-    const Fp8Plan p = plan_fp8_gemm(g.M, g.N, g.kb, g.mode, g.batch, false);
+    const Fp8Plan p = plan_fp8_gemm(g.M, g.N, g.kb, g.mode, g.batch, g.c_dtype == MUON_DTYPE_F32);
     return run_gemm(a, b, g, p, static_cast<hipStream_t>(stream));
   });
 }

@@ -54,7 +54,7 @@ struct Fp8Plan {
   int32_t kind;                  // kernel, by the rule in plan_fp8_gemm
   int32_t splits;
 };
-Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t kb, int32_t mode, int64_t batch, bool may_split);
+Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t kb, int32_t mode, int64_t batch, bool wide);
 hipError_t launch_fp8_gemm(int fmt_a, int fmt_b, const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s);
 hipError_t launch_fp8_reduce(const Fp8Gemm& g, hipStream_t s);
 

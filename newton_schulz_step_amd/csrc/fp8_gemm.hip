@@ -21,6 +21,7 @@
 // values have at most 4 significant bits), and multiplied by the bf16 instructions,
 // whose sums keep 24 bits: 2e-7 of the norm, at half the rate.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.hpp"
@@ -139,52 +140,51 @@ __device__ __forceinline__ bf16x8 to_bf16x8(int lo, int hi, float s) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: 16 x 16 outputs per workgroup, the contraction split over its eight waves
-// four blocks (one register of scales) at a time, joined in LDS in a fixed order. The
-// weights are read once from memory straight into the instruction's registers; with
-// four blocks in flight per wave that keeps the memory system busy, which is all that
+// Few rows: 16 MT rows x 16 columns of outputs per workgroup, the contraction split over
+// its eight waves four blocks (one word of scales) at a time, joined in LDS in a fixed
+// order. The weights are read once from memory straight into the instruction's registers;
+// with four blocks in flight per wave that keeps the memory system busy, which is all that
 // bounds a product of a few tokens. Rows beyond the matrix repeat its last row (their
-// results are not stored).
+// results are not stored). One token, 11008 x 4096: 11 us (4.1 TB/s).
 constexpr int kFewWaves = 8;
 
 template <int FA, int FB, bool WIDE, int U>
-__device__ __forceinline__ void few_step(const i32x4 (&a0)[4], const i32x4 (&a1)[4], const i32x4 (&b0)[4],
-                                         const i32x4 (&b1)[4], int sa, int sb, f32x4& acc) {
+__device__ __forceinline__ void few_step(const i32x4& a0, const i32x4& a1, const i32x4& b0, const i32x4& b1, int sa,
+                                         int sb, f32x4& acc) {
   // B's rows are the instruction's rows: register e of lane l is column 4 (l / 16) + e
   // of the tile, row l % 16
   if constexpr (WIDE) {
     const float fsa = scale_value(sa, U), fsb = scale_value(sb, U);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(b0[U][2 * h], b0[U][2 * h + 1], fsb),
-                                                    to_bf16x8<FA>(a0[U][2 * h], a0[U][2 * h + 1], fsa), acc, 0, 0, 0);
-    }
+    for (int h = 0; h < 2; ++h)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(b0[2 * h], b0[2 * h + 1], fsb),
+                                                    to_bf16x8<FA>(a0[2 * h], a0[2 * h + 1], fsa), acc, 0, 0, 0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(b1[U][2 * h], b1[U][2 * h + 1], fsb),
-                                                    to_bf16x8<FA>(a1[U][2 * h], a1[U][2 * h + 1], fsa), acc, 0, 0, 0);
-    }
+    for (int h = 0; h < 2; ++h)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(b1[2 * h], b1[2 * h + 1], fsb),
+                                                    to_bf16x8<FA>(a1[2 * h], a1[2 * h + 1], fsa), acc, 0, 0, 0);
   } else {
-    const i32x8 fa = __builtin_shufflevector(a0[U], a1[U], 0, 1, 2, 3, 4, 5, 6, 7);
-    const i32x8 fb = __builtin_shufflevector(b0[U], b1[U], 0, 1, 2, 3, 4, 5, 6, 7);
+    const i32x8 fa = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+    const i32x8 fb = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc, FB, FA, U, sb, U, sa);
   }
 }
 
-template <int FA, int FB, bool WIDE>
+template <int FA, int FB, bool WIDE, int MT>
 __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g, int mtiles, int ntiles) {
-  __shared__ float part[kFewWaves][16][17];
+  constexpr int TM = 16 * MT;
+  __shared__ float part[kFewWaves][TM][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int per = mtiles * ntiles;
   const int z = blockIdx.x / per;
   const int rest = blockIdx.x - z * per;
   const int nt = rest / mtiles, mt = rest - nt * mtiles;
   // rows [m0, mend) of A (a tile of them), matrix `mat` of B and C, blocks [kb0, kb1)
-  struct { int m0, mend, mat, amat, bmat, kb0, kb1; } w = {mt * 16, static_cast<int>(g.M), z, z, z, 0, g.kb};
+  struct { int m0, mend, mat, amat, bmat, kb0, kb1; } w = {mt * TM, static_cast<int>(g.M), z, z, z, 0, g.kb};
   if (g.mode == FP8_GROUP_ROWS) {
     Groups groups;
-    groups.fetch(g.offsets, g.batch, static_cast<int>(g.M), 16, 0);
-    if (!find_group(g.offsets, g.batch, static_cast<int>(g.M), 16, groups, mt, w.mat, w.m0, w.mend)) return;
+    groups.fetch(g.offsets, g.batch, static_cast<int>(g.M), TM, 0);
+    if (!find_group(g.offsets, g.batch, static_cast<int>(g.M), TM, groups, mt, w.mat, w.m0, w.mend)) return;
     w.amat = 0;
     w.bmat = w.mat;
   } else if (g.mode == FP8_GROUP_K) {
@@ -193,43 +193,62 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
   }
   const int r = lane & 15, p = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(nt) * 16;
-  const int64_t ra = min(w.m0 + r, w.mend - 1), rb = min(n0 + r, g.N - 1);
-  const uint8_t* pa = g.a + w.amat * g.a_batch + ra * g.pitch + p * 16;
+  const int64_t rb = min(n0 + r, g.N - 1);
   const uint8_t* pb = g.b + w.bmat * g.b_batch + rb * g.pitch + p * 16;
-  const uint8_t* psa = g.sa + w.amat * g.sa_batch + ra * g.s_pitch;
   const uint8_t* psb = g.sb + w.bmat * g.sb_batch + rb * g.s_pitch;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint8_t* pa[MT];
+  const uint8_t* psa[MT];
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t ra = min(w.m0 + i * 16 + r, w.mend - 1);
+    pa[i] = g.a + w.amat * g.a_batch + ra * g.pitch + p * 16;
+    psa[i] = g.sa + w.amat * g.sa_batch + ra * g.s_pitch;
+    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
   for (int q = w.kb0 / 4 + wave; q * 4 < w.kb1; q += kFewWaves) {
-    const int sa = *reinterpret_cast<const int*>(psa + q * 4);
     const int sb = *reinterpret_cast<const int*>(psb + q * 4);
-    i32x4 a0[4], a1[4], b0[4], b1[4];
+    // blocks outside [kb0, kb1) load the first one of the range and are not used
+    int64_t at[4];
+    bool in[4];
+    i32x4 b0[4], b1[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      // blocks outside [kb0, kb1) load the first one of the range and are not used
-      const int kb = q * 4 + u >= w.kb0 && q * 4 + u < w.kb1 ? q * 4 + u : w.kb0;
-      b0[u] = *reinterpret_cast<const i32x4*>(pb + static_cast<int64_t>(kb) * 128);
-      b1[u] = *reinterpret_cast<const i32x4*>(pb + static_cast<int64_t>(kb) * 128 + 64);
-      a0[u] = *reinterpret_cast<const i32x4*>(pa + static_cast<int64_t>(kb) * 128);
-      a1[u] = *reinterpret_cast<const i32x4*>(pa + static_cast<int64_t>(kb) * 128 + 64);
+      in[u] = q * 4 + u >= w.kb0 && q * 4 + u < w.kb1;
+      at[u] = static_cast<int64_t>(in[u] ? q * 4 + u : w.kb0) * 128;
+      b0[u] = *reinterpret_cast<const i32x4*>(pb + at[u]);
+      b1[u] = *reinterpret_cast<const i32x4*>(pb + at[u] + 64);
     }
-    if (q * 4 >= w.kb0 && q * 4 < w.kb1) few_step<FA, FB, WIDE, 0>(a0, a1, b0, b1, sa, sb, acc);
-    if (q * 4 + 1 >= w.kb0 && q * 4 + 1 < w.kb1) few_step<FA, FB, WIDE, 1>(a0, a1, b0, b1, sa, sb, acc);
-    if (q * 4 + 2 >= w.kb0 && q * 4 + 2 < w.kb1) few_step<FA, FB, WIDE, 2>(a0, a1, b0, b1, sa, sb, acc);
-    if (q * 4 + 3 >= w.kb0 && q * 4 + 3 < w.kb1) few_step<FA, FB, WIDE, 3>(a0, a1, b0, b1, sa, sb, acc);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int sa = *reinterpret_cast<const int*>(psa[i] + q * 4);
+      i32x4 a0[4], a1[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        a0[u] = *reinterpret_cast<const i32x4*>(pa[i] + at[u]);
+        a1[u] = *reinterpret_cast<const i32x4*>(pa[i] + at[u] + 64);
+      }
+      if (in[0]) few_step<FA, FB, WIDE, 0>(a0[0], a1[0], b0[0], b1[0], sa, sb, acc[i]);
+      if (in[1]) few_step<FA, FB, WIDE, 1>(a0[1], a1[1], b0[1], b1[1], sa, sb, acc[i]);
+      if (in[2]) few_step<FA, FB, WIDE, 2>(a0[2], a1[2], b0[2], b1[2], sa, sb, acc[i]);
+      if (in[3]) few_step<FA, FB, WIDE, 3>(a0[3], a1[3], b0[3], b1[3], sa, sb, acc[i]);
+    }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) part[wave][r][p * 4 + e] = acc[e];
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave][i * 16 + r][p * 4 + e] = acc[i][e];
   __syncthreads();
-  if (threadIdx.x < 256) {
-    const int i = threadIdx.x >> 4, j = threadIdx.x & 15;
+  for (int k = threadIdx.x; k < TM * 16; k += 64 * kFewWaves) {
+    const int i = k >> 4, j = k & 15;
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kFewWaves; ++k) v += part[k][i][j];
+    for (int x = 0; x < kFewWaves; ++x) v += part[x][i][j];
     const int64_t m = w.m0 + i, n = n0 + j;
     if (m < w.mend && n < g.N) {
-      const int64_t at = (g.mode == FP8_GROUP_ROWS ? 0 : w.mat * g.c_batch) + m * g.ldc + n;
-      if (g.accumulate) v += load_c(g.c, g.c_dtype, at);
-      store_c(g.c, g.c_dtype, at, v);
+      const int64_t c = (g.mode == FP8_GROUP_ROWS ? 0 : w.mat * g.c_batch) + m * g.ldc + n;
+      if (g.accumulate) v += load_c(g.c, g.c_dtype, c);
+      store_c(g.c, g.c_dtype, c, v);
     }
   }
 }
@@ -763,14 +782,42 @@ __global__ __launch_bounds__(256, TILE == 256 ? 1 : 2) void fp8_tile_kernel(Fp8G
 }
 
 // Which kernel a product takes.
-enum { FP8_FEW_ROWS = 0, FP8_TILE_128 = 1, FP8_TILE_256 = 2 };
+enum { FP8_FEW_16 = 0, FP8_FEW_32 = 1, FP8_FEW_64 = 2, FP8_TILE_128 = 3, FP8_TILE_256 = 4 };
 
-Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t, int32_t mode, int64_t batch, bool) {
-  const int64_t mats = mode == FP8_GROUP_ROWS ? 1 : batch;
-  auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t) * mats; };
-  if (M <= 32 || N <= 16) return {FP8_FEW_ROWS, 1};
-  if (tiles(256) >= 128) return {FP8_TILE_256, 1};
-  return {FP8_TILE_128, 1};
+static int tile_rows(int kind) {
+  const int rows[] = {16, 32, 64, 128, 256};
+  return rows[kind];
+}
+
+// The kernel with the least estimated time: rounds of 256 workgroups times what a round
+// costs, some us and some per block of the contraction (measured, 8-bit and fp32 results;
+// 128-tiles run two workgroups per CU, counted as two rounds). It weighs reading B again
+// for every 16 to 64 rows against a wide tile's empty rows and idle CUs. For instance
+// (us, few rows 16 / 32 / 64, tiles 128 / 256; bf16, K = 4096):
+//   1 x 11008: 11 / 13 / 16 / 23 / 39       64 x 4096: 20 / 15 / 13 / 16 / 39
+//   128 x 11008: 90 / 68 / 62 / 24 / 42     2048 x 4096: - / - / - / 36 / 47
+//   8192 x 11008: - / - / - / 416 / 306
+// Of groups only the total of their rows is known here; half a tile is added for each.
+Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t kb, int32_t mode, int64_t batch, bool wide) {
+  struct Cost { double start, round, block; };
+  static const Cost cost[2][5] = {
+      {{2.5, 0.3, 0.13}, {2.7, 0.3, 0.20}, {3.2, 0.3, 0.32}, {3.5, 2.0, 0.48}, {4.0, 5.0, 1.40}},
+      {{2.6, 0.4, 0.13}, {3.0, 0.4, 0.22}, {3.8, 0.4, 0.36}, {3.5, 4.0, 1.05}, {4.0, 9.0, 3.20}}};
+  const double blocks = mode == FP8_GROUP_K ? static_cast<double>(kb) / static_cast<double>(batch) : static_cast<double>(kb);
+  int best = 0;
+  double least = 0.0;
+  for (int kind = FP8_FEW_16; kind <= FP8_TILE_256; ++kind) {
+    const int64_t tm = tile_rows(kind), tn = kind < FP8_TILE_128 ? 16 : tm;
+    const int64_t rows = mode == FP8_GROUP_ROWS ? (2 * M / tm + batch + 1) / 2 : (M + tm - 1) / tm * batch;
+    const Cost& c = cost[wide][kind];
+    const double rounds = std::ceil(static_cast<double>(rows * ((N + tn - 1) / tn)) / 256.0);
+    const double us = c.start + rounds * (c.round + c.block * blocks);
+    if (kind == FP8_FEW_16 || us < least) {
+      best = kind;
+      least = us;
+    }
+  }
+  return {best, 1};
 }
 
 template <int FA, int FB, int OUT>
@@ -783,8 +830,8 @@ static void launch_tiles(const Fp8Plan& p, const Fp8Gemm& g, int64_t total, int 
 
 template <int FA, int FB>
 static hipError_t launch(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
-  const int tm = p.kind == FP8_FEW_ROWS ? 16 : p.kind == FP8_TILE_128 ? 128 : 256;
-  const int64_t nt = (g.N + tm - 1) / tm;
+  const int tm = tile_rows(p.kind), tn = p.kind < FP8_TILE_128 ? 16 : tm;
+  const int64_t nt = (g.N + tn - 1) / tn;
   int64_t mt = (g.M + tm - 1) / tm, z = g.batch;
   if (g.mode == FP8_GROUP_ROWS) {   // every group may end in a part of a tile
     mt = std::min<int64_t>(g.M, g.M / tm + g.batch);
@@ -795,10 +842,20 @@ static hipError_t launch(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
   if (total > 0x7fffffff) return hipErrorInvalidValue;
   const int m = static_cast<int>(mt), n = static_cast<int>(nt);
   const bool wide = g.c_dtype == MUON_DTYPE_F32;
-  if (p.kind == FP8_FEW_ROWS) {
+  if (p.kind < FP8_TILE_128) {
     const dim3 grid(static_cast<unsigned>(total)), block(64 * kFewWaves);
-    if (wide) hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, true>), grid, block, 0, s, g, m, n);
-    else hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, false>), grid, block, 0, s, g, m, n);
+#define MUON_FEW(W, MT) hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, W, MT>), grid, block, 0, s, g, m, n)
+    if (p.kind == FP8_FEW_16) {
+      if (wide) MUON_FEW(true, 1);
+      else MUON_FEW(false, 1);
+    } else if (p.kind == FP8_FEW_32) {
+      if (wide) MUON_FEW(true, 2);
+      else MUON_FEW(false, 2);
+    } else {
+      if (wide) MUON_FEW(true, 4);
+      else MUON_FEW(false, 4);
+    }
+#undef MUON_FEW
   } else if (wide) {
     launch_tiles<FA, FB, OUT_F32>(p, g, total, m, n, s);
   } else if (g.accumulate) {

@@ -12,10 +12,54 @@ template <int DT> __device__ __forceinline__ void store1(void* p, int64_t i, flo
   else static_cast<_Float16*>(p)[i] = static_cast<_Float16>(v);
 }
 
-__device__ __forceinline__ double wave_max_d(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-  return v;
+// ---------------------------------------------------------------------------
+// Reductions over a wave with row shifts and broadcasts (no LDS); the result in all lanes.
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t shifted(uint32_t v, uint32_t other) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(other), static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+
+template <typename F>
+__device__ __forceinline__ uint32_t wave_fold(uint32_t v, uint32_t identity, F&& f) {
+  v = f(v, shifted<0x111, 0xf>(v, identity));   // lanes 1, 2, 4, 8 before, within 16
+  v = f(v, shifted<0x112, 0xf>(v, identity));
+  v = f(v, shifted<0x114, 0xf>(v, identity));
+  v = f(v, shifted<0x118, 0xf>(v, identity));
+  v = f(v, shifted<0x142, 0xa>(v, identity));   // last lane of the 16 before
+  v = f(v, shifted<0x143, 0xc>(v, identity));   // last lane of the first 32
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
+  return wave_fold(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ float wave_max_f(float v) {   // ignores NaN
+  return __uint_as_float(wave_fold(__float_as_uint(v), __float_as_uint(-__builtin_huge_valf()), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_shifted(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t o = static_cast<uint64_t>(shifted<CTRL, ROWS>(static_cast<uint32_t>(b >> 32), 0u)) << 32 |
+                     shifted<CTRL, ROWS>(static_cast<uint32_t>(b), 0u);
+  return v + __builtin_bit_cast(double, o);
+}
+__device__ __forceinline__ double lane_double(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_add(double v) {
+  v = add_shifted<0x111, 0xf>(v);
+  v = add_shifted<0x112, 0xf>(v);
+  v = add_shifted<0x114, 0xf>(v);
+  v = add_shifted<0x118, 0xf>(v);
+  v = add_shifted<0x142, 0xa>(v);
+  v = add_shifted<0x143, 0xc>(v);
+  return lane_double(v, 63);
 }
 
 // ---------------------------------------------------------------------------
@@ -23,23 +67,55 @@ __device__ __forceinline__ double wave_max_d(double v) {
 //
 // Scores and keys are held in 64 bits: which experts a token gets is then the same
 // wherever it is computed in 64 bits, while 32-bit exponentials of different libraries
-// would order near neighbours differently.
+// would order near neighbours differently. What bounds it is the number of steps, not
+// memory: choosing takes top_k rounds of one maximum over the wave. Keys are mapped to
+// ordered 64-bit integers and the maximum is taken of their upper halves; only lanes that
+// tie there compare the lower ones. 16384 tokens, 64 experts, 8 groups, 6 of 64: 15 us
+// (43 us with 64-bit butterflies through LDS).
 
 constexpr double kNone = -__builtin_huge_val();      // not available
 constexpr double kLowest = -1.7976931348623157e308;  // a NaN key: below every number
+
+// Ordered key: larger numbers have larger keys, 0 stands for "not available".
+struct Key {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Key ordered(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t o = b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
+  return v == kNone ? Key{0u, 0u} : Key{static_cast<uint32_t>(o >> 32), static_cast<uint32_t>(o)};
+}
+
+// The lanes' best (largest key, ties to the lowest 64 reg + lane): its lane, -1 for none.
+// `reg` is the register the lane's own best sits in.
+__device__ __forceinline__ int wave_best(const Key& k, int reg) {
+  const uint32_t hi = wave_max_u(k.hi);
+  if (hi == 0u) return -1;
+  unsigned long long who = __ballot(k.hi == hi);
+  if ((who & (who - 1)) != 0) {
+    const uint32_t lo = wave_max_u(k.hi == hi ? k.lo : 0u);
+    who = __ballot(k.hi == hi && k.lo == lo);
+    if ((who & (who - 1)) != 0) {
+      const bool in = k.hi == hi && k.lo == lo;
+      const uint32_t first = ~wave_max_u(in ? ~static_cast<uint32_t>(reg) : 0u);
+      who = __ballot(in && static_cast<uint32_t>(reg) == first);
+    }
+  }
+  return __builtin_ctzll(who);
+}
 
 // One softmax or sigmoid score per register; -inf logits score 0, a row of them too.
 template <int V>
 __device__ __forceinline__ void row_scores(const float (&l)[V], int score, double (&s)[V]) {
   if (score == MUON_ROUTE_SOFTMAX) {
-    double m = kNone;
+    float most = -__builtin_huge_valf();
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      m = fmax(m, static_cast<double>(l[i]));   // ignores NaN
+      most = fmaxf(most, l[i]);   // ignores NaN
       nan = nan || l[i] != l[i];
     }
-    m = wave_max_d(m);
+    const double m = static_cast<double>(wave_max_f(most));
     nan = __any(nan);
     double sum = 0.0;
 #pragma unroll
@@ -47,26 +123,13 @@ __device__ __forceinline__ void row_scores(const float (&l)[V], int score, doubl
       s[i] = l[i] == -__builtin_huge_valf() ? 0.0 : exp(static_cast<double>(l[i]) - m);
       sum += s[i];
     }
-    sum = wave_sum_d(sum);
+    sum = wave_add(sum);
     if (nan) sum = __builtin_nan("");
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = l[i] == -__builtin_huge_valf() ? 0.0 : s[i] / sum;
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
-  }
-}
-
-// The lane-wise best (key, index) of the wave: largest key, ties to the lower index.
-__device__ __forceinline__ void wave_best(double& k, int& i) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const double ko = __shfl_xor(k, o, 64);
-    const int io = __shfl_xor(i, o, 64);
-    if (ko > k || (ko == k && io < i)) {
-      k = ko;
-      i = io;
-    }
   }
 }
 
@@ -93,6 +156,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     if (key[i] != key[i]) key[i] = kLowest;
     if (e >= E || l[i] == -__builtin_huge_valf()) key[i] = kNone;
   }
+  unsigned long long kept = ~0ull;   // groups
+  const int per = E / a.n_groups;
   if (a.n_groups > 1) {
     double* mine = keys + wave * E;
 #pragma unroll
@@ -101,64 +166,63 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     // lane g scores group g
-    const int per = E / a.n_groups;
     double gk = kNone;
     if (lane < a.n_groups) {
       double t1 = kNone, t2 = kNone;
+#pragma unroll 4
       for (int j = 0; j < per; ++j) {
         const double k = mine[lane * per + j];
-        if (k > t1) {
-          t2 = t1;
-          t1 = k;
-        } else if (k > t2) {
-          t2 = k;
-        }
+        t2 = fmax(t2, fmin(t1, k));
+        t1 = fmax(t1, k);
       }
       gk = t1;
       if (a.group_top > 1 && t2 > kNone) gk = t1 <= kLowest ? t1 : (t2 <= kLowest ? kLowest : t1 + t2);
     }
-    unsigned long long kept = 0;
+    Key k = ordered(gk);
+    kept = 0;
     for (int j = 0; j < a.top_groups; ++j) {
-      double k = gk;
-      int g = lane;
-      wave_best(k, g);
-      if (k == kNone) break;
+      const int g = wave_best(k, 0);
+      if (g < 0) break;
       kept |= 1ull << g;
-      if (lane == g) gk = kNone;
+      if (lane == g) k = Key{0u, 0u};
     }
+  }
+  Key o[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+  for (int i = 0; i < V; ++i) {
+    o[i] = ordered(key[i]);
+    if (a.n_groups > 1) {
       const int e = i * 64 + lane;
-      if (e < E && !((kept >> (e / per)) & 1)) key[i] = kNone;
+      if (e < E && !((kept >> (e / per)) & 1)) o[i] = Key{0u, 0u};
     }
   }
   int my_id = -1;
   double my_s = 0.0;
   for (int j = 0; j < a.top_k; ++j) {
-    double k = kNone;
-    int e = lane;
-    double sc = 0.0;
+    Key k = o[0];
+    int reg = 0;
+    double sc = s[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] > k) {
-        k = key[i];
-        e = i * 64 + lane;
+    for (int i = 1; i < V; ++i)
+      if (o[i].hi > k.hi || (o[i].hi == k.hi && o[i].lo > k.lo)) {
+        k = o[i];
+        reg = i;
         sc = s[i];
       }
-    const int own = e;
-    wave_best(k, e);
-    if (k == kNone) break;
-    sc = __shfl(sc, e & 63, 64);
+    const int who = wave_best(k, reg);
+    if (who < 0) break;
+    const int at = V > 1 ? __builtin_amdgcn_readlane(reg, who) : 0;
+    const double chosen = lane_double(sc, who);
     if (lane == j) {
-      my_id = e;
-      my_s = sc;
+      my_id = at * 64 + who;
+      my_s = chosen;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (own == e && i * 64 + lane == e) key[i] = kNone;
+      if (lane == who && i == at) o[i] = Key{0u, 0u};
   }
   double f = static_cast<double>(a.scale);
-  if (a.renormalize) f /= wave_sum_d(my_s) + 1e-20;
+  if (a.renormalize) f /= wave_add(my_s) + 1e-20;
   if (lane < a.top_k) {
     a.ids[token * a.top_k + lane] = my_id;
     a.weights[token * a.top_k + lane] = my_id < 0 ? 0.0f : static_cast<float>(my_s * f);
@@ -168,8 +232,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 // The gradient: with T = sum of the chosen s + 1e-20 and w_j = scale s_j / T,
 //   ds_j = (scale dw_j - sum_i dw_i w_i) / T     (scale dw_j without renormalisation)
 //   sigmoid: dl_j = ds_j s_j (1 - s_j);  softmax: dl_i = s_i (ds_i - sum_j ds_j s_j).
-// The chosen slots' values are scattered to their experts' registers by a search over
-// the slots (at most 32), one broadcast each.
+// The chosen slots' values reach their experts' registers slot by slot, broadcast to the
+// wave (at most 32).
 template <int DT, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -182,48 +246,53 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
     const int e = i * 64 + lane;
     l[i] = e < E ? load1<DT>(a.logits, token * a.ld + e) : -__builtin_huge_valf();
   }
-  double s[V], ds[V];
-  row_scores<V>(l, a.score, s);
   int id = -1;
-  double dw = 0.0;
+  float dw = 0.0f;
   if (lane < a.top_k) {
     id = a.ids[token * a.top_k + lane];
     if (id < 0 || id >= E) id = -1;
-    else dw = static_cast<double>(a.dweights[token * a.top_k + lane]);
+    else dw = a.dweights[token * a.top_k + lane];
   }
+  double s[V], ds[V];
+  row_scores<V>(l, a.score, s);
   bool hit[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     ds[i] = 0.0;
     hit[i] = false;
   }
-  double total = 0.0, dot = 0.0;
   for (int j = 0; j < a.top_k; ++j) {
-    const int e = __shfl(id, j, 64);
-    const double d = __shfl(dw, j, 64);
+    const int e = __builtin_amdgcn_readlane(id, j);
+    const float d = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(dw), j));
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (e == i * 64 + lane) {
-        ds[i] = d;
+        ds[i] = static_cast<double>(d);
         hit[i] = true;
       }
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (hit[i]) {
-      total += s[i];
-      dot += ds[i] * s[i];
-    }
-  total = wave_sum_d(total) + 1e-20;
-  dot = wave_sum_d(dot);
   const double f = static_cast<double>(a.scale);
-  double sum = 0.0;
+  if (a.renormalize) {
+    double total = 0.0, dot = 0.0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (hit[i]) ds[i] = a.renormalize ? f * (ds[i] - dot / total) / total : f * ds[i];
-    sum += hit[i] ? ds[i] * s[i] : 0.0;
+    for (int i = 0; i < V; ++i) {
+      total += hit[i] ? s[i] : 0.0;
+      dot += hit[i] ? ds[i] * s[i] : 0.0;
+    }
+    total = wave_add(total) + 1e-20;
+    dot = wave_add(dot) / total;
+#pragma unroll
+    for (int i = 0; i < V; ++i) ds[i] = hit[i] ? f * (ds[i] - dot) / total : 0.0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) ds[i] *= f;
   }
-  if (a.score == MUON_ROUTE_SOFTMAX) sum = wave_sum_d(sum);
+  double sum = 0.0;
+  if (a.score == MUON_ROUTE_SOFTMAX) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += hit[i] ? ds[i] * s[i] : 0.0;
+    sum = wave_add(sum);
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = i * 64 + lane;
@@ -305,6 +374,8 @@ __global__ __launch_bounds__(kOrderThreads) void order_hist_kernel(OrderArgs a) 
 
 __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a) {
   __shared__ int total[MUON_ROUTE_MAX_EXPERTS];              // slots of each expert
+  __shared__ int earlier[MUON_ROUTE_MAX_EXPERTS];            // those in earlier blocks
+  __shared__ int pad[MUON_ROUTE_MAX_EXPERTS];                // its first padding row
   __shared__ int next[kOrderWaves][MUON_ROUTE_MAX_EXPERTS];  // next row of each expert, per wave
   __shared__ int scan[kOrderWaves];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -321,24 +392,36 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
     if (e >= 0) atomicAdd(&next[wave][e], 1);
   }
   __syncthreads();
-  // totals, slots before this block and before each wave
-  for (int e = t; e < E; e += kOrderThreads) {
-    int all = 0, before = 0;
-    if (a.blocks > 1) {
-      for (int b = 0; b < a.blocks; ++b) {
-        const int c = a.hist[static_cast<int64_t>(b) * E + e];
-        if (b < static_cast<int>(blockIdx.x)) before += c;
-        all += c;
+  // totals, slots before this block and before each wave; the blocks' counts are summed by
+  // all threads together
+  if (a.blocks > 1) {
+    for (int e = t; e < E; e += kOrderThreads) total[e] = earlier[e] = 0;
+    __syncthreads();
+    const int parts = max(1, kOrderThreads / E);
+    for (int e0 = 0; e0 < E; e0 += kOrderThreads) {
+      const int e = e0 + (E < kOrderThreads ? t % E : t), part = E < kOrderThreads ? t / E : 0;
+      if (e < E && part < parts) {
+        int all = 0, before = 0;
+#pragma unroll 4
+        for (int b = part; b < a.blocks; b += parts) {
+          const int c = a.hist[static_cast<int64_t>(b) * E + e];
+          before += b < static_cast<int>(blockIdx.x) ? c : 0;
+          all += c;
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&earlier[e], before);
       }
-    } else {
-      for (int w = 0; w < kOrderWaves; ++w) all += next[w][e];
     }
-    total[e] = all;
+    __syncthreads();
+  }
+  for (int e = t; e < E; e += kOrderThreads) {
+    int before = a.blocks > 1 ? earlier[e] : 0;
     for (int w = 0; w < kOrderWaves; ++w) {
       const int c = next[w][e];
       next[w][e] = before;
       before += c;
     }
+    if (a.blocks == 1) total[e] = before;
   }
   __syncthreads();
   // padded offsets: exclusive scan over the experts, kOrderThreads at a time
@@ -366,14 +449,17 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs a)
         a.offsets[e] = static_cast<int>(first);
         a.counts[e] = total[e];
       }
-      // the expert's padding rows
-      if (e % a.blocks == static_cast<int>(blockIdx.x))
-        for (int r = total[e]; r < n; ++r) a.rows[first + r] = -1;
+      pad[e] = static_cast<int>(first) + total[e];
     }
     base += sum;
     __syncthreads();
   }
   if (blockIdx.x == 0 && t == 0) a.offsets[E] = static_cast<int>(base);
+  // padding rows, a wave per expert; rows behind the last expert
+  for (int e = static_cast<int>(blockIdx.x) * kOrderWaves + wave; e < E; e += a.blocks * kOrderWaves) {
+    const int n = (a.align - total[e] % a.align) % a.align;
+    for (int r = lane; r < n; r += 64) a.rows[pad[e] + r] = -1;
+  }
   for (int64_t r = base + static_cast<int64_t>(blockIdx.x) * kOrderThreads + t; r < a.capacity;
        r += static_cast<int64_t>(a.blocks) * kOrderThreads)
     a.rows[r] = -1;
