@@ -159,7 +159,6 @@ int muon_fp8_quantize(const muon_fp8_source_t* src, int32_t blocks, const muon_f
     if (rt * ct * B > 0x7fffffff) return fail(MUON_ERR_BAD_SHAPE, "the matrix has too many 128 x 128 tiles for a launch");
     a.row_tiles = static_cast<int32_t>(rt);
     a.col_tiles = static_cast<int32_t>(ct);
-    a.vec = !misaligned(src->data, 16) && (src->ld * esz) % 16 == 0 && (B == 1 || (src->batch_stride * esz) % 16 == 0);
     if (out != nullptr) {
       a.q = out->data;
       a.s = out->scale;
@@ -217,8 +216,6 @@ static Fp8Gemm gemm_of(const muon_fp8_t* a, const muon_fp8_t* b, const muon_fp8_
   g.ldc = c->ld;
   g.c_dtype = c->dtype;
   g.accumulate = c->accumulate != 0;
-  const int esz = element_size(c->dtype);
-  g.c_vec = !misaligned(c->data, 16) && (c->ld * esz) % 16 == 0 && (c->batch_stride * esz) % 16 == 0;
   g.splits = 1;
   return g;
 }
@@ -492,8 +489,6 @@ static int combine_common(int32_t dtype, int64_t o_rows, int64_t cols, const int
   return MUON_OK;
 }
 
-static bool vectors(const void* p, int64_t ld, int esz) { return !misaligned(p, 16) && (ld * esz) % 16 == 0; }
-
 int muon_combine(const void* o, int32_t dtype, int64_t o_rows, int64_t cols, int64_t ld_o, const int32_t* pos,
                  const float* weights, int64_t tokens, int32_t top_k, void* y, int64_t ld_y, void* stream) {
   return guarded([&]() -> int {
@@ -508,12 +503,10 @@ int muon_combine(const void* o, int32_t dtype, int64_t o_rows, int64_t cols, int
                             {span_of(o, strided_bytes(dtype, 1, o_rows, cols, ld_o, 0), "o"), span_of(pos, n * 4, "pos"),
                              span_of(weights, n * 4, "weights")})) != MUON_OK)
       return st;
-    const int esz = element_size(dtype);
     a.o = o;
     a.ld_o = ld_o;
     a.y = y;
     a.ld_y = ld_y;
-    a.vec = vectors(o, ld_o, esz) && vectors(y, ld_y, esz);
     hipStream_t s = static_cast<hipStream_t>(stream);
     MUON_LAUNCH("combine", s, launch_combine(dtype, a, s));
     return MUON_OK;
@@ -544,7 +537,6 @@ int muon_combine_backward(const void* dy, int32_t dtype, int64_t tokens, int64_t
     }
     if (tokens == 0) return MUON_OK;
     if ((st = check_outputs(outs, ins)) != MUON_OK) return st;
-    const int esz = element_size(dtype);
     a.dy = dy;
     a.ld_dy = ld_dy;
     a.o = o;
@@ -552,8 +544,6 @@ int muon_combine_backward(const void* dy, int32_t dtype, int64_t tokens, int64_t
     a.dweights = dweights;
     a.d_o = d_o;
     a.ld_do = ld_do;
-    a.vec = vectors(dy, ld_dy, esz) && (dweights == nullptr || vectors(o, ld_o, esz)) &&
-            (d_o == nullptr || vectors(d_o, ld_do, esz));
     hipStream_t s = static_cast<hipStream_t>(stream);
     MUON_LAUNCH("combine_backward", s, launch_combine_backward(dtype, a, s));
     return MUON_OK;

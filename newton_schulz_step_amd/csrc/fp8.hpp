@@ -22,7 +22,6 @@ struct QuantArgs {
   int64_t n_weights;
   int64_t rows, cols;           // of the quantised matrix
   int32_t row_tiles, col_tiles, total_tiles;
-  int32_t vec;                  // 16-byte loads allowed (base, pitch and batch stride aligned)
   uint8_t* q;                   // rows x qp, scales rows x qs (NULL: not wanted)
   uint8_t* s;
   uint8_t* qt;                  // cols x tp, scales cols x ts (NULL: not wanted)
@@ -46,7 +45,6 @@ struct Fp8Gemm {
   void* c;
   int64_t c_batch, ldc;          // elements
   int32_t c_dtype, accumulate;
-  int32_t c_vec;                 // rows of 16-byte aligned groups of 8 results
   float* partial;                // splits x batch x M x N sums, where splits > 1
   int32_t splits;
 };
@@ -102,7 +100,6 @@ struct CombineArgs {
   const float* weights;
   int64_t tokens;
   int32_t top_k;
-  int32_t vec;          // 16-byte accesses allowed
   void* y;              // forward
   int64_t ld_y;
   const void* dy;       // backward
