@@ -452,16 +452,12 @@ typedef struct {
  * With the forward product Y = X W^T of W (N x K): the input gradient is the
  * product of dY and W's transposed operand, the weight gradient that of the
  * transposed operands of dY and X.
- * workspace (device, 16-byte aligned, muon_fp8_matmul_workspace_size() bytes):
- * partial sums when the contraction is split over workgroups, which a product
- * of few tiles needs to fill the GPU; NULL with 0 bytes never splits. The
- * result does not depend on timing, but its last bits do on the split.
+ * The sizes choose among kernels whose sums run in different orders; for given
+ * sizes the result is the same in every call.
  * Errors: MUON_ERR_NULL, BAD_SHAPE, UNSUPPORTED, ALIGN (operands and result
  * must be aligned to their element, data to 16 bytes), OVERLAP. */
 int muon_fp8_matmul(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* group_offsets,
-                    const muon_fp8_result_t* c, void* workspace, size_t workspace_bytes, void* stream);
-int muon_fp8_matmul_workspace_size(const muon_fp8_t* a, const muon_fp8_t* b, int32_t grouped,
-                                   size_t* bytes_out);
+                    const muon_fp8_result_t* c, void* stream);
 
 /* Grouped contractions (the experts' weight gradients): matrix g of C, M x N,
  * (+)= sum over k in [offsets[g], offsets[g + 1]) of A[i][k] B[j][k], for

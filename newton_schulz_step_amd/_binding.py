@@ -34,7 +34,7 @@ EXPORTED = (
     "muon_step_window", "adamw_step", "muon_pack", "muon_unpack", "muon_last_error", "muon_release_plans",
     "muon_profile_begin", "muon_profile_end", "muon_version", "muon_ns_flops",
     "muon_plan_owners", "muon_comm_elements", "muon_step_noalloc",
-    "muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_workspace_size", "muon_fp8_matmul_grouped_k",
+    "muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_grouped_k",
     "muon_default_route_hyper", "muon_route", "muon_route_backward", "muon_expert_order",
     "muon_expert_order_workspace_size", "muon_combine", "muon_combine_backward",
 )
@@ -169,8 +169,7 @@ def load() -> ctypes.CDLL:
         po, ps, pr = ctypes.POINTER(Fp8Operand), ctypes.POINTER(Fp8Source), ctypes.POINTER(Fp8Result)
         ph = ctypes.POINTER(RouteHyper)
         lib.muon_fp8_quantize.argtypes = [ps, i32, po, po, vp]
-        lib.muon_fp8_matmul.argtypes = [po, po, vp, pr, vp, sz, vp]
-        lib.muon_fp8_matmul_workspace_size.argtypes = [po, po, i32, ctypes.POINTER(sz)]
+        lib.muon_fp8_matmul.argtypes = [po, po, vp, pr, vp]
         lib.muon_fp8_matmul_grouped_k.argtypes = [po, po, vp, i32, pr, vp]
         lib.muon_default_route_hyper.argtypes = [ph]
         lib.muon_default_route_hyper.restype = None
@@ -180,8 +179,8 @@ def load() -> ctypes.CDLL:
         lib.muon_expert_order_workspace_size.argtypes = [i64, i32, ctypes.POINTER(sz)]
         lib.muon_combine.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp]
         lib.muon_combine_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp]
-        for name in ("muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_workspace_size",
-                     "muon_fp8_matmul_grouped_k", "muon_route", "muon_route_backward", "muon_expert_order",
+        for name in ("muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_grouped_k",
+                     "muon_route", "muon_route_backward", "muon_expert_order",
                      "muon_expert_order_workspace_size", "muon_combine", "muon_combine_backward"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("muon_workspace_size", "muon_step", "muon_step_noalloc", "muon_step_window", "muon_plan_owners",
@@ -768,16 +767,10 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=None, accumulate: bool = Fals
             raise ValueError("a and b must both be single matrices or both be batches")
         shape = tuple(a.data.shape[:-1]) + (b.rows,)
     dev = _same_device(a.data, a.scale, b.data, b.scale, out, offsets)
-    lib = load()
     with _on(dev, stream) as on:
-        ca, cb = a._c(), b._c()
-        need = ctypes.c_size_t(0)
-        _check(lib.muon_fp8_matmul_workspace_size(ctypes.byref(ca), ctypes.byref(cb), int(offsets is not None),
-                                                  ctypes.byref(need)))
         out, c = _result(out, shape, on, out_dtype, accumulate)
-        ws = on.scratch(need.value)
-        _check(lib.muon_fp8_matmul(ctypes.byref(ca), ctypes.byref(cb), _flat(offsets), ctypes.byref(c), _flat(ws),
-                                   0 if ws is None else ws.numel(), on.handle))
+        _check(load().muon_fp8_matmul(ctypes.byref(a._c()), ctypes.byref(b._c()), _flat(offsets), ctypes.byref(c),
+                                      on.handle))
     return out
 
 

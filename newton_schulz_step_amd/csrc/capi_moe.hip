@@ -216,31 +216,17 @@ static Fp8Gemm gemm_of(const muon_fp8_t* a, const muon_fp8_t* b, const muon_fp8_
   g.ldc = c->ld;
   g.c_dtype = c->dtype;
   g.accumulate = c->accumulate != 0;
-  g.splits = 1;
   return g;
 }
 
-static int run_gemm(const muon_fp8_t* a, const muon_fp8_t* b, Fp8Gemm& g, const Fp8Plan& p, hipStream_t s) {
-  MUON_LAUNCH(g.mode == FP8_DENSE ? "fp8_gemm" : g.mode == FP8_GROUP_ROWS ? "fp8_gemm_grouped" : "fp8_gemm_grouped_k", s,
-              launch_fp8_gemm(a->format, b->format, p, g, s));
-  if (g.splits > 1) MUON_LAUNCH("fp8_reduce", s, launch_fp8_reduce(g, s));
+static int run_gemm(const muon_fp8_t* a, const muon_fp8_t* b, const Fp8Gemm& g, hipStream_t s) {
+  const Fp8Plan p = plan_fp8_gemm(g.M, g.N, g.kb, g.mode, g.batch, g.c_dtype == MUON_DTYPE_F32);
+  MUON_LAUNCH(fp8_gemm_kind(p), s, launch_fp8_gemm(a->format, b->format, p, g, s));
   return MUON_OK;
 }
 
-int muon_fp8_matmul_workspace_size(const muon_fp8_t* a, const muon_fp8_t* b, int32_t grouped, size_t* bytes_out) {
-  return guarded([&]() -> int {
-    if (bytes_out == nullptr) return fail(MUON_ERR_NULL, "bytes_out is NULL");
-    const int st = check_matmul(a, b, grouped != 0);
-    if (st != MUON_OK) return st;
-    const Fp8Plan p = plan_fp8_gemm(a->rows, b->rows, fp8_data_pitch(a->cols) / MUON_FP8_BLOCK,
-                                    grouped ? FP8_GROUP_ROWS : FP8_DENSE, b->batch, false);
-    *bytes_out = p.splits > 1 ? static_cast<size_t>(p.splits) * b->batch * a->rows * b->rows * 4 : 0;
-    return MUON_OK;
-  });
-}
-
 int muon_fp8_matmul(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* group_offsets, const muon_fp8_result_t* c,
-                    void* workspace, size_t workspace_bytes, void* stream) {
+                    void* stream) {
   return guarded([&]() -> int {
     const bool grouped = group_offsets != nullptr;
     int st = check_matmul(a, b, grouped);
@@ -257,18 +243,8 @@ int muon_fp8_matmul(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* gro
     Fp8Gemm g = gemm_of(a, b, c, group_offsets);
     g.mode = grouped ? FP8_GROUP_ROWS : FP8_DENSE;
     g.batch = static_cast<int32_t>(b->batch);
-    const Fp8Plan p = plan_fp8_gemm(g.M, g.N, g.kb, g.mode, g.batch, g.c_dtype == MUON_DTYPE_F32);
-    g.splits = p.splits;
-    if (p.splits > 1) {
-      const size_t need = static_cast<size_t>(p.splits) * g.batch * g.M * g.N * 4;
-      if (workspace_bytes < need)
-        return fail(MUON_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
-      if (misaligned(workspace, 16)) return fail(MUON_ERR_ALIGN, "workspace is not 16-byte aligned");
-      g.partial = static_cast<float*>(workspace);
-      outs.push_back(span_of(workspace, static_cast<int64_t>(need), "workspace"));
-    }
     if ((st = check_outputs(outs, ins)) != MUON_OK) return st;
-    return run_gemm(a, b, g, p, static_cast<hipStream_t>(stream));
+    return run_gemm(a, b, g, static_cast<hipStream_t>(stream));
   });
 }
 
@@ -295,8 +271,7 @@ int muon_fp8_matmul_grouped_k(const muon_fp8_t* a, const muon_fp8_t* b, const in
     Fp8Gemm g = gemm_of(a, b, c, group_offsets);
     g.mode = FP8_GROUP_K;
     g.batch = n_groups;
-    const Fp8Plan p = plan_fp8_gemm(g.M, g.N, g.kb, g.mode, g.batch, g.c_dtype == MUON_DTYPE_F32);
-    return run_gemm(a, b, g, p, static_cast<hipStream_t>(stream));
+    return run_gemm(a, b, g, static_cast<hipStream_t>(stream));
   });
 }
 

@@ -45,16 +45,13 @@ struct Fp8Gemm {
   void* c;
   int64_t c_batch, ldc;          // elements
   int32_t c_dtype, accumulate;
-  float* partial;                // splits x batch x M x N sums, where splits > 1
-  int32_t splits;
 };
 struct Fp8Plan {
-  int32_t kind;                  // kernel, by the rule in plan_fp8_gemm
-  int32_t splits;
+  int32_t kind;   // which kernel, see plan_fp8_gemm
 };
 Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t kb, int32_t mode, int64_t batch, bool wide);
 hipError_t launch_fp8_gemm(int fmt_a, int fmt_b, const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s);
-hipError_t launch_fp8_reduce(const Fp8Gemm& g, hipStream_t s);
+const char* fp8_gemm_kind(const Fp8Plan& p);   // its name in the launch statistics
 
 struct RouteArgs {
   const void* logits;

@@ -612,94 +612,96 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
               ((g.mode == FP8_GROUP_ROWS ? 0 : t.mat * g.c_batch) + (t.m0 + wm * HALF + lane / LPR) * g.ldc + t.n0 +
                wn * HALF + col) * ESZ;
     const int64_t step = RPP * g.ldc * ESZ;   // bytes from pass to pass
-    const bool whole = t.mend - t.m0 >= TILE && g.N - t.n0 >= TILE;
+    const int wrows = t.mend - (t.m0 + wm * HALF), wcols = static_cast<int>(min<int64_t>(HALF, g.N - (t.n0 + wn * HALF)));
+    if (wrows <= 0 || wcols <= 0) return;
+    const bool whole = wrows >= HALF && wcols >= HALF;   // of this wave's part
     const bool add = OUT == OUT_ADD_16 || (WIDE && g.accumulate);
     stage_write(Int<0>{});
-    auto steps = [&](auto masked) {
-      constexpr bool MASKED = decltype(masked)::value != 0;
-      each_step<WB * NS * NJ>([&](auto number) {
-        constexpr int K = decltype(number)::value, J = K % NJ * NB, ROW = K / (NS * NJ) * 32 + K / NJ % NS * RS;
-        Taken v[NP];
-        // whole tiles: what is added comes while LDS is read
-        [[maybe_unused]] f32x4 plo[NP], phi[NP];
-        [[maybe_unused]] u16x8 pu[NP];
-        if constexpr (!MASKED && !ROUNDED) {
-          if (add) {
-            const char* from = c + J * 32 * ESZ;
+    each_step<WB * NS * NJ>([&](auto number) {
+      constexpr int K = decltype(number)::value, J = K % NJ * NB, ROW = K / (NS * NJ) * 32 + K / NJ % NS * RS;
+      Taken v[NP];
+      // what is added comes while LDS is read
+      [[maybe_unused]] f32x4 plo[NP], phi[NP];
+      [[maybe_unused]] u16x8 pu[NP];
+      if constexpr (!ROUNDED) {
+        if (whole && add) {
+          const char* from = c + J * 32 * ESZ;
 #pragma unroll
-            for (int p = 0; p < NP; ++p, from += step) {
-              if constexpr (WIDE) {
-                plo[p] = reinterpret_cast<const f32x4_any*>(from)[0];
-                phi[p] = reinterpret_cast<const f32x4_any*>(from)[1];
-              } else {
-                pu[p] = *reinterpret_cast<const u16x8_any*>(from);
-              }
+          for (int p = 0; p < NP; ++p, from += step) {
+            if constexpr (WIDE) {
+              plo[p] = reinterpret_cast<const f32x4_any*>(from)[0];
+              phi[p] = reinterpret_cast<const f32x4_any*>(from)[1];
+            } else {
+              pu[p] = *reinterpret_cast<const u16x8_any*>(from);
             }
           }
         }
-        stage_read(v);
-        if constexpr (!MASKED && K + 1 < WB * NS * NJ) stage_write(Int<K + 1>{});
+      }
+      stage_read(v);
+      if (!whole) {
         char* to = c + J * 32 * ESZ;
 #pragma unroll
         for (int p = 0; p < NP; ++p, to += step) {
-          if constexpr (!MASKED) {
-            if constexpr (ROUNDED) {
-              *reinterpret_cast<u16x8_any*>(to) = v[p].u;
-            } else if constexpr (WIDE) {
+          if (ROW + p * RPP >= rows || J * 32 >= cols) continue;
+          if (J * 32 + 8 <= cols) {
+            if constexpr (WIDE) {
+              f32x4_any* d = reinterpret_cast<f32x4_any*>(to);
               if (add) {
-                v[p].lo += plo[p];
-                v[p].hi += phi[p];
+                v[p].lo += d[0];
+                v[p].hi += d[1];
               }
-              reinterpret_cast<f32x4_any*>(to)[0] = v[p].lo;
-              reinterpret_cast<f32x4_any*>(to)[1] = v[p].hi;
+              d[0] = v[p].lo;
+              d[1] = v[p].hi;
             } else {
-              add_16(v[p], pu[p]);
+              if constexpr (!ROUNDED) add_16(v[p], *reinterpret_cast<const u16x8_any*>(to));
               *reinterpret_cast<u16x8_any*>(to) = v[p].u;
             }
-          } else if (ROW + p * RPP < rows && J * 32 < cols) {
-            if (J * 32 + 8 <= cols) {
-              if constexpr (WIDE) {
-                f32x4_any* d = reinterpret_cast<f32x4_any*>(to);
-                if (add) {
-                  v[p].lo += d[0];
-                  v[p].hi += d[1];
-                }
-                d[0] = v[p].lo;
-                d[1] = v[p].hi;
-              } else {
-                if constexpr (!ROUNDED) add_16(v[p], *reinterpret_cast<const u16x8_any*>(to));
-                *reinterpret_cast<u16x8_any*>(to) = v[p].u;
-              }
-            } else {   // the matrix's last columns, one by one out of LDS
-              const int row = p * RPP + lane / LPR;
+          } else {   // the matrix's last columns, one by one out of LDS
+            const int row = p * RPP + lane / LPR;
 #pragma unroll 1
-              for (int e = 0; e < cols - J * 32; ++e) {
-                if constexpr (ROUNDED) {
-                  reinterpret_cast<unsigned short*>(to)[e] = reinterpret_cast<const unsigned short*>(
-                      stage + row * (CH * 16) + (((lane % LPR) ^ (row & (CH - 1))) * 16))[e];
-                } else {
-                  float x = reinterpret_cast<const float*>(
-                      stage + row * 128 + (((2 * (lane % LPR) + e / 4) ^ (row & 7)) * 16))[e & 3];
-                  if (add) x += load_c(to, g.c_dtype, e);
-                  store_c(to, g.c_dtype, e, x);
-                }
+            for (int e = 0; e < cols - J * 32; ++e) {
+              if constexpr (ROUNDED) {
+                reinterpret_cast<unsigned short*>(to)[e] = reinterpret_cast<const unsigned short*>(
+                    stage + row * (CH * 16) + (((lane % LPR) ^ (row & (CH - 1))) * 16))[e];
+              } else {
+                float x = reinterpret_cast<const float*>(
+                    stage + row * 128 + (((2 * (lane % LPR) + e / 4) ^ (row & 7)) * 16))[e & 3];
+                if (add) x += load_c(to, g.c_dtype, e);
+                store_c(to, g.c_dtype, e, x);
               }
             }
           }
         }
-        if constexpr (MASKED && K + 1 < WB * NS * NJ) {
-          __builtin_amdgcn_wave_barrier();
-          stage_write(Int<K + 1>{});
+        __builtin_amdgcn_wave_barrier();
+      }
+      if constexpr (K + 1 < WB * NS * NJ) stage_write(Int<K + 1>{});
+      if (whole) {
+        // 16-bit results leave as whole lines that are not read here again: past the cache
+        // they leave room for operands (experts' weight gradients 251 -> 210 us). fp32 ones
+        // leave as half lines, which the cache has to join (past it 8192 x 8192 x 512 took
+        // 176 instead of 97 us).
+        char* to = c + J * 32 * ESZ;
+#pragma unroll
+        for (int p = 0; p < NP; ++p, to += step) {
+          if constexpr (WIDE) {
+            if (add) {
+              v[p].lo += plo[p];
+              v[p].hi += phi[p];
+            }
+            reinterpret_cast<f32x4_any*>(to)[0] = v[p].lo;
+            reinterpret_cast<f32x4_any*>(to)[1] = v[p].hi;
+          } else {
+            if constexpr (!ROUNDED) add_16(v[p], pu[p]);
+            __builtin_nontemporal_store(v[p].u, reinterpret_cast<u16x8_any*>(to));
+          }
         }
-        if constexpr (K % NJ == NJ - 1) {
-          c += step * NP;
-          asm volatile("" : "+v"(c));   // one row's address at a time: computed ahead they fill the registers
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
-    };
-    if (whole) steps(Int<0>{});
-    else steps(Int<1>{});
+      }
+      if constexpr (K % NJ == NJ - 1) {
+        c += step * NP;
+        asm volatile("" : "+v"(c));   // one row's address at a time: computed ahead they fill the registers
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
 
   int index = blockIdx.x;
@@ -817,7 +819,7 @@ Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t kb, int32_t mode, int64_t ba
       least = us;
     }
   }
-  return {best, 1};
+  return {best};
 }
 
 template <int FA, int FB, int OUT>
@@ -868,11 +870,13 @@ static hipError_t launch(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+const char* fp8_gemm_kind(const Fp8Plan& p) {
+  return p.kind < FP8_TILE_128 ? "fp8_gemm_few_rows" : p.kind == FP8_TILE_128 ? "fp8_gemm_128" : "fp8_gemm_256";
+}
+
 hipError_t launch_fp8_gemm(int fmt_a, int fmt_b, const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
   if (fmt_a == MUON_FP8_E4M3) return fmt_b == MUON_FP8_E4M3 ? launch<0, 0>(p, g, s) : launch<0, 1>(p, g, s);
   return fmt_b == MUON_FP8_E4M3 ? launch<1, 0>(p, g, s) : launch<1, 1>(p, g, s);
 }
-
-hipError_t launch_fp8_reduce(const Fp8Gemm&, hipStream_t) { return hipSuccess; }
 
 }  // namespace muon

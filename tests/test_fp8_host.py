@@ -82,11 +82,11 @@ def test_quantize_refusals(lib):
     assert quantize(lib, source(cols=0), operand(1, cols=0)) == nss.OK
 
 
-def matmul(lib, a, b, off=None, ws=None, wsb=0, c=True, **kw):
+def matmul(lib, a, b, off=None, c=True, **kw):
     f = dict(data=at(8), batch_stride=0, ld=b.rows if b else 1, dtype=1, accumulate=0)
     f.update(kw)
     r = B.Fp8Result(f["data"], f["batch_stride"], f["ld"], f["dtype"], f["accumulate"])
-    return lib.muon_fp8_matmul(ref(a), ref(b), off, ref(r) if c else None, ws, wsb, None)
+    return lib.muon_fp8_matmul(ref(a), ref(b), off, ref(r) if c else None, None)
 
 
 def test_matmul_refusals(lib):
@@ -135,22 +135,6 @@ def test_matmul_grouped_k_refusals(lib):
     assert run(a, b, dtype=7) == nss.ERR_UNSUPPORTED
     assert run(a, b, off=at(8)) == nss.ERR_OVERLAP
     assert run(a, b, n=0) == nss.OK
-
-
-def test_matmul_workspace(lib):
-    out = ctypes.c_size_t(0)
-    a, b = operand(1, 40, 300), operand(2, 50, 300)
-    assert lib.muon_fp8_matmul_workspace_size(ref(a), ref(b), 0, None) == nss.ERR_NULL
-    assert lib.muon_fp8_matmul_workspace_size(ref(a), ref(operand(2, 50, 299)), 0, ctypes.byref(out)) == nss.ERR_BAD_SHAPE
-    assert lib.muon_fp8_matmul_workspace_size(ref(a), ref(b), 0, ctypes.byref(out)) == nss.OK
-    # a product with a workspace too small for its split is refused
-    for m, n, k in ((256, 256, 1 << 16), (1, 16, 1 << 16), (512, 2048, 8192)):
-        a, b = operand(1, m, k), operand(2, n, k)
-        assert lib.muon_fp8_matmul_workspace_size(ref(a), ref(b), 0, ctypes.byref(out)) == nss.OK
-        if out.value:
-            assert matmul(lib, a, b, ws=at(9), wsb=out.value - 1) == nss.ERR_WORKSPACE
-            assert matmul(lib, a, b, ws=at(9) + 4, wsb=out.value) == nss.ERR_ALIGN
-            assert matmul(lib, a, b, ws=at(8), wsb=out.value) == nss.ERR_OVERLAP
 
 
 def route(lib, h, tokens=10, experts=16, logits=at(0), ids=at(1), w=at(2), bias=None, dtype=0, ld=None):

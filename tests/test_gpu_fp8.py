@@ -411,35 +411,53 @@ def test_product_gradients_by_differences(lib):
         assert abs((hi - lo) - dw[n, k]) <= (T + 16) * 2.0 ** -23 * mag + 1e-9 * (abs(hi) + abs(lo))
 
 
-# products large enough for the widest tiles: many small matrices, ragged groups and
-# contractions, in every mode, both kinds of result
+# products large enough for the widest tiles: many matrices, ragged groups and
+# contractions, in every mode, both kinds of result; the launch statistics say which
+# kernel ran
+
+def kinds(lib, call):
+    lib.profile_begin()
+    call()
+    return set(lib.profile_end())
+
+
+def test_every_kernel_is_reached(lib):
+    import torch
+    for (m, n, k), want in (((1, 512, 512), "fp8_gemm_few_rows"), ((64, 512, 512), "fp8_gemm_few_rows"),
+                            ((1024, 1024, 4096), "fp8_gemm_128"), ((4096, 4096, 256), "fp8_gemm_256")):
+        a = lib.fp8_quantize(torch.zeros(m, k, device="cuda"))
+        b = lib.fp8_quantize(torch.zeros(n, k, device="cuda"))
+        for dtype in (torch.float32, torch.bfloat16):
+            assert kinds(lib, lambda: lib.fp8_matmul(a, b, out_dtype=dtype)) == {want}
+
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("M,N,K", [(300, 260, 300), (256, 512, 128), (257, 511, 1)])
+@pytest.mark.parametrize("M,N,K", [(500, 490, 300), (512, 512, 128), (257, 511, 1), (300, 260, 2100)])
 def test_many_wide_tiles_batch(lib, M, N, K, dtype):
     import torch
     rng = np.random.default_rng([M, N])
-    B = 40
+    B = 64
     a, va = operand(lib, rng, M, K, "e4m3", B)
     b, vb = operand(lib, rng, N, K, "e5m2", B)
     buf = torch.full((B, M + 1, N + 3), 7.0, dtype=dt(torch, dtype), device="cuda")
     out = buf[:, :M, 3:]
     for acc in (False, True):
         base = host(out) if acc else None
-        lib.fp8_matmul(a, b, out=out, accumulate=acc)
+        ran = kinds(lib, lambda: lib.fp8_matmul(a, b, out=out, accumulate=acc))
+        assert M < 500 or ran == {"fp8_gemm_256"}
         torch.cuda.synchronize()
         got = host(out)
-        for i in range(0, B, 3):
+        for i in range(0, B, 13):
             check_product(got[i], va[i], vb[i], dtype, None if base is None else base[i])
     assert torch.all(buf[:, M] == 7.0) and torch.all(buf[:, :, :3] == 7.0)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
-def test_many_wide_tiles_grouped_rows(lib, dtype):
+@pytest.mark.parametrize("counts", [[0, 700, 1, 0, 255, 257, 256, 0, 40, 590, 0] + [512] * 8, [300] * 20 + [0] * 50 + [128] * 10])
+def test_many_wide_tiles_grouped_rows(lib, dtype, counts):
     import torch
     rng = np.random.default_rng(21)
-    counts = [0, 700, 1, 0, 255, 257, 256, 0, 40, 590, 0]
-    N, K = 3700, 136
+    N, K = 2600, 136
     G, off = len(counts), np.concatenate([[0], np.cumsum(counts)])
     M = int(off[-1]) + 500
     a, va = operand(lib, rng, M, K, "e4m3")
@@ -454,21 +472,74 @@ def test_many_wide_tiles_grouped_rows(lib, dtype):
     got = host(out)
     for g in range(G):
         lo, hi = off[g], off[g + 1]
-        for n in range(0, N, 740):      # a part of the columns at a time
-            check_product(got[lo:hi, n:n + 200], va[lo:hi], vb[g][n:n + 200], dtype)
+        for n in range(0, N, 500):      # a part of the columns at a time
+            check_product(got[lo:hi, n:n + 100], va[lo:hi], vb[g][n:n + 100], dtype)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_wide_tiles_grouped_contraction(lib, dtype):
+    # contractions that start and end anywhere in the 16-block parts of the scales
     import torch
     rng = np.random.default_rng(22)
-    blocks = [0, 1, 3, 0, 2, 5, 1, 4] * 6
+    blocks = ([0, 1, 3, 0, 2, 5, 1, 4, 17, 1, 15, 16, 0, 33] * 5)[:64]
     off = 128 * np.concatenate([[0], np.cumsum(blocks)])
-    M, N, K = 260, 300, int(off[-1]) + 1
+    M, N, K = 512, 480, int(off[-1]) + 1
     a, va = operand(lib, rng, M, K, "e5m2")
     b, vb = operand(lib, rng, N, K, "e4m3")
-    out = lib.fp8_matmul_grouped_k(a, b, torch.from_numpy(off.astype(np.int32)).cuda(), out_dtype=dt(torch, dtype))
+    offsets = torch.from_numpy(off.astype(np.int32)).cuda()
+    out = torch.empty(len(blocks), M, N, dtype=dt(torch, dtype), device="cuda")
+    assert kinds(lib, lambda: lib.fp8_matmul_grouped_k(a, b, offsets, out=out)) == {"fp8_gemm_256"}
     torch.cuda.synchronize()
     got = host(out)
     for g in range(len(blocks)):
-        check_product(got[g], va[:, off[g]:off[g + 1]], vb[:, off[g]:off[g + 1]], dtype)
+        sl = slice(off[g], off[g + 1])
+        check_product(got[g][::7], va[::7, sl], vb[:, sl], dtype)
+
+
+def test_groups_without_columns_ignore_their_neighbours(lib):
+    # an empty group gives zeros even where the columns around it hold NaN, and a group of
+    # an odd number of blocks does not take in the next group's
+    import torch
+    rng = np.random.default_rng(23)
+    x = rng.standard_normal((512, 128 * 9)).astype(np.float32)
+    x[:, 128 * 3:128 * 6] = np.nan
+    a = lib.fp8_quantize(torch.from_numpy(x).cuda(), "e5m2")
+    b, vb = operand(lib, rng, 512, 128 * 9, "e4m3")
+    off = [0, 3, 3, 6, 6, 9] + [9] * 60
+    for part in (slice(0, 512), slice(0, 40)):
+        aa = lib.Fp8(a.data[part].contiguous(), a.scale[part].contiguous(), a.cols)
+        got = host(lib.fp8_matmul_grouped_k(aa, b, (128 * torch.tensor(off, dtype=torch.int32)).cuda(),
+                                            out_dtype=torch.float32))
+        va = values(aa)
+        for g, (lo, hi) in enumerate(zip(off, off[1:])):
+            if lo == 3 and hi == 6:
+                assert np.all(np.isnan(got[g]))
+            elif lo == hi:
+                assert np.all(got[g] == 0)
+            else:
+                check_product(got[g], va[:, 128 * lo:128 * hi], vb[:, 128 * lo:128 * hi], "f32")
+
+
+def test_long_contraction_and_far_rows(lib):
+    # more blocks than the parts of the scales hold twice, rows whose bytes lie beyond 2^32
+    import torch
+    rng = np.random.default_rng(24)
+    K = 128 * 70 + 5
+    a, va = operand(lib, rng, 300, K, "e4m3")
+    b, vb = operand(lib, rng, 200, K, "e4m3")
+    for dtype in ("f32", "bf16"):
+        c = lib.fp8_matmul(a, b, out_dtype=dt(torch, dtype))
+        check_product(host(c), va, vb, dtype)
+    rows, K = (1 << 32) // 4096 + 300, 4096
+    big = lib.fp8_empty(rows, K)
+    big.data.view(torch.uint8).zero_()
+    big.scale.view(torch.uint8).fill_(127)
+    tail, vt = operand(lib, rng, 260, K, "e4m3")
+    big.data[-260:] = tail.data
+    big.scale[-260:] = tail.scale
+    w, vw = operand(lib, rng, 48, K, "e4m3")
+    c = lib.fp8_matmul(big, w)
+    assert torch.all(c[:-260] == 0)
+    check_product(host(c[-260:]), vt, vw, "bf16")
+    c = lib.fp8_matmul(w, big)
+    check_product(host(c[:, -260:]), vw, vt, "bf16")
