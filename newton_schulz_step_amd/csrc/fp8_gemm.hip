@@ -94,14 +94,15 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups,
   return true;
 }
 
-// Blocks [kb0, kb1) of group z of a grouped contraction (scalar loads: z is uniform).
+// Blocks [kb0, kb1) of group z of a grouped contraction (scalar loads: z is uniform), [0, 0)
+// of one without columns: its first block may lie behind the operand's last.
 __device__ __forceinline__ void group_blocks(const Fp8Gemm& g, int z, int& kb0, int& kb1) {
   const auto* off = (const __attribute__((address_space(4))) int32_t*)(g.offsets);
   const int limit = g.kb * 128;
   const int lo = min(max(off[z], 0), limit);
   const int hi = min(max(off[z + 1], lo), limit);
-  kb0 = lo / 128;
-  kb1 = hi > lo ? (hi + 127) / 128 : kb0;
+  kb0 = hi > lo ? lo / 128 : 0;
+  kb1 = hi > lo ? (hi + 127) / 128 : 0;
 }
 
 __device__ __forceinline__ float load_c(const void* c, int dtype, int64_t i) {

@@ -543,3 +543,19 @@ def test_long_contraction_and_far_rows(lib):
     check_product(host(c[-260:]), vt, vw, "bf16")
     c = lib.fp8_matmul(w, big)
     check_product(host(c[:, -260:]), vw, vt, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(3, 40), (40, 40), (512, 512)])
+def test_last_groups_without_columns(lib, M, N, dtype):
+    # they begin behind the operand's last block: nothing there is read, also where the
+    # last block is not the last of four
+    import torch
+    rng = np.random.default_rng([M, 25])
+    a, va = operand(lib, rng, M, 128 * 5, "e4m3")
+    b, vb = operand(lib, rng, N, 128 * 5, "e4m3")
+    off = [0, 5] + [5] * 62
+    out = torch.full((len(off) - 1, M, N), 7.0, dtype=dt(torch, dtype), device="cuda")
+    lib.fp8_matmul_grouped_k(a, b, (128 * torch.tensor(off, dtype=torch.int32)).cuda(), out=out)
+    check_product(host(out[0]), va, vb, dtype)
+    assert torch.all(out[1:] == 0)
