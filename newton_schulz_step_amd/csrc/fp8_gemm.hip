@@ -412,7 +412,8 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
 #define MUON_RSRC(p, n) __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, n, 0x00027000)
 #define MUON_GLDS(rsrc, lds, size, voff, soff)                                                              \
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(lds), size, voff, soff, 0, 0)
-  // slice `s` of a tile (zeros behind its last one)
+  // slice `s` of a tile (zeros behind its last one: no bytes and no offset, since the
+  // bounds are what the offset leaves of the bytes)
   auto load_slice = [&](char* to, const uint8_t* a, const uint8_t* b, int na, int nb, int kb0, int kb1, int s) {
     const bool there = kb0 + s < kb1;
     const auto ra = MUON_RSRC(a, there ? na : 0), rb = MUON_RSRC(b, there ? nb : 0);
@@ -721,7 +722,7 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
     const bool more = index < total;
     Tile nxt = cur;
     if (more) nxt = tile_at(index);
-    else nxt.na = nxt.nb = 0;   // fetched as zeros, never used
+    else nxt.na = nxt.nb = nxt.kb0 = nxt.kb1 = 0;   // fetched as zeros, never used
     const int n = slices_of(cur);
     int t = 0, kb = cur.kb0;
     bool fetched = false;   // the next tile's first scales

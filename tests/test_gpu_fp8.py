@@ -559,3 +559,19 @@ def test_last_groups_without_columns(lib, M, N, dtype):
     lib.fp8_matmul_grouped_k(a, b, (128 * torch.tensor(off, dtype=torch.int32)).cuda(), out=out)
     check_product(host(out[0]), va, vb, dtype)
     assert torch.all(out[1:] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(129, 130), (257, 300)])
+def test_last_tile_fetches_nothing_more(lib, M, N, dtype):
+    # the last tiles' contraction begins in the middle of the operands (beyond the first 16
+    # blocks too); behind them a workgroup fetches nothing
+    import torch
+    rng = np.random.default_rng([M, 26])
+    off = [0, 1, 19, 20, 37]
+    a, va = operand(lib, rng, M, 128 * 37, "e4m3")
+    b, vb = operand(lib, rng, N, 128 * 37, "e5m2")
+    got = host(lib.fp8_matmul_grouped_k(a, b, (128 * torch.tensor(off, dtype=torch.int32)).cuda(),
+                                        out_dtype=dt(torch, dtype)))
+    for g, (lo, hi) in enumerate(zip(off, off[1:])):
+        check_product(got[g], va[:, 128 * lo:128 * hi], vb[:, 128 * lo:128 * hi], dtype)
