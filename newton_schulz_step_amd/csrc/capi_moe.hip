@@ -159,6 +159,7 @@ int muon_fp8_quantize(const muon_fp8_source_t* src, int32_t blocks, const muon_f
     if (rt * ct * B > 0x7fffffff) return fail(MUON_ERR_BAD_SHAPE, "the matrix has too many 128 x 128 tiles for a launch");
     a.row_tiles = static_cast<int32_t>(rt);
     a.col_tiles = static_cast<int32_t>(ct);
+    a.total_tiles = static_cast<int32_t>(rt * ct * B);
     if (out != nullptr) {
       a.q = out->data;
       a.s = out->scale;
@@ -172,7 +173,7 @@ int muon_fp8_quantize(const muon_fp8_source_t* src, int32_t blocks, const muon_f
       a.ts = fp8_scale_pitch(R);
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
-    MUON_LAUNCH("fp8_quantize", s, launch_fp8_quantize(src->dtype, format, blocks != 0, a, B, s));
+    MUON_LAUNCH("fp8_quantize", s, launch_fp8_quantize(src->dtype, format, blocks != 0, a, s));
     return MUON_OK;
   });
 }

@@ -118,9 +118,11 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs a) {
   __shared__ float cmax[4][128];
   __shared__ __align__(16) unsigned char tile[128 * 128];
   const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
-  const int b = blockIdx.x;
-  const int64_t batch = b / (a.row_tiles * a.col_tiles);
-  const int rest = b - static_cast<int>(batch) * (a.row_tiles * a.col_tiles);
+  const uint32_t b = flat_block();
+  if (b >= static_cast<uint32_t>(a.total_tiles)) return;
+  const uint32_t per = static_cast<uint32_t>(a.row_tiles * a.col_tiles);
+  const int64_t batch = b / per;
+  const int rest = static_cast<int>(b % per);
   const int rt = rest / a.col_tiles, ct = rest - rt * a.col_tiles;
   const int64_t r0 = static_cast<int64_t>(rt) * 128 + rg * 8;
   const int64_t c0 = static_cast<int64_t>(ct) * 128 + cg * 8;
@@ -241,11 +243,9 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs a) {
   }
 }
 
-hipError_t launch_fp8_quantize(int x_dtype, int format, bool blocks, const QuantArgs& a, int64_t batch, hipStream_t s) {
-  const int64_t total = batch * a.row_tiles * a.col_tiles;
-  if (total <= 0) return hipSuccess;
-  if (total > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(total));
+hipError_t launch_fp8_quantize(int x_dtype, int format, bool blocks, const QuantArgs& a, hipStream_t s) {
+  if (a.total_tiles <= 0) return hipSuccess;
+  const dim3 grid = flat_grid(a.total_tiles);
   const bool weighted = a.row_weight != nullptr;
 #define MUON_QB(XT, FMT, B)                                                                                    \
   do {                                                                                                         \

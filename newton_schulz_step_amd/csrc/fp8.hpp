@@ -6,6 +6,16 @@
 
 namespace muon {
 
+// Grids of up to 2^31 workgroups. A grid dimension takes less than 2^32 threads, so beyond
+// 2^20 workgroups the number is split over two dimensions; the last ones may lie behind the
+// count, and kernels leave those alone.
+constexpr int kGridBits = 20;
+inline dim3 flat_grid(int64_t blocks) {
+  const int64_t x = blocks < (int64_t(1) << kGridBits) ? blocks : int64_t(1) << kGridBits;
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>((blocks + x - 1) / x));
+}
+__device__ __forceinline__ uint32_t flat_block() { return (blockIdx.y << kGridBits) + blockIdx.x; }
+
 inline int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 // Row pitches of a quantised operand with `cols` columns (bytes).
@@ -28,7 +38,7 @@ struct QuantArgs {
   uint8_t* st;
   int64_t qp, qs, tp, ts;
 };
-hipError_t launch_fp8_quantize(int x_dtype, int format, bool blocks, const QuantArgs& a, int64_t batch, hipStream_t s);
+hipError_t launch_fp8_quantize(int x_dtype, int format, bool blocks, const QuantArgs& a, hipStream_t s);
 
 // C (+)= A B^T of quantised operands. Batches and groups: see the C ABI.
 enum { FP8_DENSE = 0, FP8_GROUP_ROWS = 1, FP8_GROUP_K = 2 };

@@ -176,9 +176,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
   constexpr int TM = 16 * MT;
   __shared__ float part[kFewWaves][TM][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int per = mtiles * ntiles;
-  const int z = blockIdx.x / per;
-  const int rest = blockIdx.x - z * per;
+  const uint32_t per = static_cast<uint32_t>(mtiles * ntiles), block = flat_block();
+  const int z = static_cast<int>(block / per);
+  if (z >= (g.mode == FP8_GROUP_ROWS ? 1 : g.batch)) return;
+  const int rest = static_cast<int>(block - z * per);
   const int nt = rest / mtiles, mt = rest - nt * mtiles;
   // rows [m0, mend) of A (a tile of them), matrix `mat` of B and C, blocks [kb0, kb1)
   struct { int m0, mend, mat, amat, bmat, kb0, kb1; } w = {mt * TM, static_cast<int>(g.M), z, z, z, 0, g.kb};
@@ -847,7 +848,7 @@ static hipError_t launch(const Fp8Plan& p, const Fp8Gemm& g, hipStream_t s) {
   const int m = static_cast<int>(mt), n = static_cast<int>(nt);
   const bool wide = g.c_dtype == MUON_DTYPE_F32;
   if (p.kind < FP8_TILE_128) {
-    const dim3 grid(static_cast<unsigned>(total)), block(64 * kFewWaves);
+    const dim3 grid = flat_grid(total), block(64 * kFewWaves);
 #define MUON_FEW(W, MT) hipLaunchKernelGGL((fp8_few_rows_kernel<FA, FB, W, MT>), grid, block, 0, s, g, m, n)
     if (p.kind == FP8_FEW_16) {
       if (wide) MUON_FEW(true, 1);

@@ -137,7 +137,7 @@ template <int DT, int V>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   extern __shared__ double keys[];   // 4 x experts, where there are groups
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const int64_t token = static_cast<int64_t>(flat_block()) * 4 + wave;
   if (token >= a.tokens) return;     // no barrier below: a wave is by itself
   const int E = a.experts;
   float l[V];
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 template <int DT, int V>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const int64_t token = static_cast<int64_t>(flat_block()) * 4 + wave;
   if (token >= a.tokens) return;
   const int E = a.experts;
   float l[V];
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
 
 template <int DT>
 static hipError_t route_dt(const RouteArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.tokens + 3) / 4));
+  const dim3 grid = flat_grid((a.tokens + 3) / 4);
   const size_t lds = a.n_groups > 1 ? 4 * sizeof(double) * a.experts : 0;
   if (a.experts <= 64) hipLaunchKernelGGL((route_kernel<DT, 1>), grid, dim3(256), lds, s, a);
   else if (a.experts <= 128) hipLaunchKernelGGL((route_kernel<DT, 2>), grid, dim3(256), lds, s, a);
@@ -323,7 +323,7 @@ hipError_t launch_route(int dtype, const RouteArgs& a, hipStream_t s) {
 
 template <int DT>
 static hipError_t route_backward_dt(const RouteBackArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.tokens + 3) / 4));
+  const dim3 grid = flat_grid((a.tokens + 3) / 4);
   if (a.experts <= 64) hipLaunchKernelGGL((route_backward_kernel<DT, 1>), grid, dim3(256), 0, s, a);
   else if (a.experts <= 128) hipLaunchKernelGGL((route_backward_kernel<DT, 2>), grid, dim3(256), 0, s, a);
   else if (a.experts <= 256) hipLaunchKernelGGL((route_backward_kernel<DT, 4>), grid, dim3(256), 0, s, a);
@@ -550,7 +550,8 @@ constexpr int kCombineRows = 4;
 
 template <int DT>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
-  const int64_t t = blockIdx.x;
+  const int64_t t = flat_block();
+  if (t >= a.tokens) return;
   const int32_t* pos = a.pos + t * a.top_k;
   const float* w = a.weights + t * a.top_k;
   for (int64_t c = threadIdx.x * 8; c < a.cols; c += 256 * 8) {
@@ -583,7 +584,8 @@ constexpr int kBackRows = 1;   // rows in flight: 2 and 4 were 4% and 19% slower
 template <int DT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineArgs a) {
   __shared__ float red[2][4][kBackRows];
-  const int64_t t = blockIdx.x;
+  const int64_t t = flat_block();
+  if (t >= a.tokens) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int j0 = 0, turn = 0; j0 < a.top_k; j0 += kBackRows, turn ^= 1) {
     int r[kBackRows];
@@ -643,12 +645,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineArgs a) {
 
 hipError_t launch_combine(int dtype, const CombineArgs& a, hipStream_t s) {
   if (a.tokens <= 0 || a.cols <= 0) return hipSuccess;
-  MUON_BY_DTYPE(combine_kernel, dim3(static_cast<unsigned>(a.tokens)), a);
+  MUON_BY_DTYPE(combine_kernel, flat_grid(a.tokens), a);
   return hipGetLastError();
 }
 hipError_t launch_combine_backward(int dtype, const CombineArgs& a, hipStream_t s) {
   if (a.tokens <= 0) return hipSuccess;
-  MUON_BY_DTYPE(combine_backward_kernel, dim3(static_cast<unsigned>(a.tokens)), a);
+  MUON_BY_DTYPE(combine_backward_kernel, flat_grid(a.tokens), a);
   return hipGetLastError();
 }
 
