@@ -575,3 +575,23 @@ def test_last_tile_fetches_nothing_more(lib, M, N, dtype):
                                         out_dtype=dt(torch, dtype)))
     for g, (lo, hi) in enumerate(zip(off, off[1:])):
         check_product(got[g], va[:, 128 * lo:128 * hi], vb[:, 128 * lo:128 * hi], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(512, 512), (300, 260)])
+def test_many_groups_of_very_different_length(lib, M, N, dtype):
+    # several rounds of tiles and more than 64 groups: they are taken in another order
+    import torch
+    rng = np.random.default_rng([M, 27])
+    blocks = rng.integers(0, 5, 150)
+    blocks[rng.random(150) < 0.1] = 11
+    blocks[64:80] = 0
+    off = np.concatenate([[0], np.cumsum(blocks)])
+    a, va = operand(lib, rng, M, 128 * int(off[-1]), "e5m2")
+    b, vb = operand(lib, rng, N, 128 * int(off[-1]), "e4m3")
+    out = torch.full((150, M, N), 7.0, dtype=dt(torch, dtype), device="cuda")
+    lib.fp8_matmul_grouped_k(a, b, (128 * torch.from_numpy(off.astype(np.int32))).cuda(), out=out)
+    out = out[:, ::37].cpu()
+    for g, (lo, hi) in enumerate(zip(off, off[1:])):
+        sl = slice(128 * lo, 128 * hi)
+        check_product(host(out[g]), va[::37, sl], vb[:, sl], dtype)
