@@ -8,6 +8,7 @@ if the library is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Dict, Iterable, List, Optional, Sequence, Tuple
@@ -853,28 +854,41 @@ def route_backward(dweights, logits, ids, h: RouteHyper, dlogits=None, stream=No
     return dlogits
 
 
+@functools.lru_cache(maxsize=256)
+def _order_workspace(n: int, n_experts: int) -> int:
+    need = ctypes.c_size_t(0)
+    _check(load().muon_expert_order_workspace_size(n, n_experts, ctypes.byref(need)))
+    return need.value
+
+
 def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=None, rows=None, pos=None, stream=None):
     """Order of routed slots by expert (muon_expert_order): (offsets [experts + 1],
     counts [experts], rows [capacity], pos like ids), all int32. The capacity
-    that any routing fits is ids.numel() + n_experts * (align - 1)."""
+    that any routing fits is ids.numel() + n_experts * (align - 1). Where none of
+    offsets, counts and rows is given they are views of one new tensor."""
     torch = _torch()
     _int32(ids, None, "ids")
     n = ids.numel()
     dev = _same_device(ids, offsets, counts, rows, pos)
-    lib = load()
     with _on(dev, stream) as on:
-        need = ctypes.c_size_t(0)
-        _check(lib.muon_expert_order_workspace_size(n, n_experts, ctypes.byref(need)))
-        offsets = _given(offsets, (n_experts + 1,), torch.int32, on, "offsets")
-        counts = _given(counts, (n_experts,), torch.int32, on, "counts")
-        if rows is None:
-            rows = on.fresh((max(n + n_experts * (align - 1), 0),), torch.int32)
+        need = _order_workspace(n, n_experts)
+        capacity = max(n + n_experts * (align - 1), 0)
+        if offsets is None and counts is None and rows is None:
+            # one allocation: three cost as much time as the launch
+            parts = (n_experts + 1, n_experts, capacity)
+            offsets, counts, rows = on.fresh((sum(parts),), torch.int32).split_with_sizes(parts)
         else:
-            _int32(rows, None, "rows")
+            offsets = _given(offsets, (n_experts + 1,), torch.int32, on, "offsets")
+            counts = _given(counts, (n_experts,), torch.int32, on, "counts")
+            if rows is None:
+                rows = on.fresh((capacity,), torch.int32)
+            else:
+                _int32(rows, None, "rows")
         pos = _given(pos, ids.shape, torch.int32, on, "pos")
-        ws = on.scratch(need.value)
-        _check(lib.muon_expert_order(_flat(ids), n, n_experts, align, _flat(offsets), _flat(counts), _flat(rows),
-                                     rows.numel(), _flat(pos), _flat(ws), 0 if ws is None else ws.numel(), on.handle))
+        ws = on.scratch(need)
+        _check(load().muon_expert_order(_flat(ids), n, n_experts, align, _flat(offsets), _flat(counts), _flat(rows),
+                                        rows.numel(), _flat(pos), _flat(ws), 0 if ws is None else ws.numel(),
+                                        on.handle))
     return offsets, counts, rows, pos
 
 

@@ -266,3 +266,16 @@ def test_combine_views(lib):
         lib.combine(buf[:, lo:hi], pos, w, out=y[:, 5:5 + hi - lo])
         assert torch.equal(y[:, 5:5 + hi - lo], lib.combine(buf[:, lo:hi].contiguous(), pos, w))
         assert torch.all(y[:, :5] == 7) and torch.all(y[:, 5 + hi - lo:] == 7)
+
+
+@pytest.mark.parametrize("n,E,align", [(0, 3, 128), (96, 64, 16), (5000, 40, 128)])
+def test_expert_order_allocates_its_results(lib, n, E, align):
+    import torch
+    ids = np.random.default_rng([n, 31]).integers(-1, E, n).astype(np.int32)
+    want = R.expert_order(ids, E, align, n + E * (align - 1))
+    got = lib.expert_order(dev(ids), E, align=align)
+    later = lib.expert_order(dev(ids[::-1].copy()), E, align=align)   # results of their own
+    assert [t.is_contiguous() and t.dtype == torch.int32 for t in got] == [True] * 4
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    assert not {t.data_ptr() for t in got if t.numel()} & {t.data_ptr() for t in later if t.numel()}
