@@ -34,7 +34,8 @@ def route(logits, top_k, score="softmax", bias=None, n_groups=1, top_groups=1, g
             best = []
             for g in range(n_groups):
                 k = sorted((k for k in key[g * per:(g + 1) * per] if k > -np.inf), reverse=True)[:group_top]
-                best.append((-sum(k) if k else np.inf, g))
+                # two NaN keys together stay the lowest number (their sum would be -inf, no key)
+                best.append((-max(LOWEST, k[0] if k[0] == LOWEST else sum(k)) if k else np.inf, g))
             kept = [g for v, g in sorted(best)[:top_groups] if v < np.inf]
             key = np.where(np.isin(np.arange(E) // per, kept), key, -np.inf)
         order = sorted((-k, e) for e, k in enumerate(key) if k > -np.inf)[:top_k]

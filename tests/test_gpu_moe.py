@@ -279,3 +279,31 @@ def test_expert_order_allocates_its_results(lib, n, E, align):
     for g, w in zip(got, want):
         assert np.array_equal(g.cpu().numpy(), w)
     assert not {t.data_ptr() for t in got if t.numel()} & {t.data_ptr() for t in later if t.numel()}
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups,K", [(64, 1, 1, 6), (64, 32, 7, 6), (64, 64, 9, 6), (33, 33, 4, 4),
+                                                   (33, 1, 1, 32), (32, 8, 2, 5), (63, 21, 3, 5)])
+def test_route_rows_do_not_meet_their_neighbours(lib, E, groups, top_groups, K, score):
+    # neighbouring rows share a wave: rows of ties, of no expert, of few experts and of NaN
+    # next to ordinary ones, in every pairing
+    rng = np.random.default_rng([E, groups])
+    kinds = [(a, b) for a in range(5) for b in range(5)]
+    l = rng.standard_normal((2 * len(kinds) + 1, E)).astype(np.float32)
+    for i, kind in enumerate(k for pair in kinds for k in pair):
+        if kind == 1:
+            l[i] = 0.5                                   # ties
+        elif kind == 2:
+            l[i] = -np.inf                               # no expert
+        elif kind == 3:
+            l[i, rng.permutation(E)[: E - 3]] = -np.inf  # three experts
+        elif kind == 4:
+            l[i, rng.integers(E)] = np.nan
+    h = lib.route_hyper(score=score, top_k=K, n_groups=groups, top_groups=top_groups)
+    ids, w = lib.route(dev(l), h)
+    want_ids, want_w = R.route(l.astype(np.float64), score=score, top_k=K, n_groups=groups, top_groups=top_groups)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    got = host(w)
+    assert np.array_equal(np.isnan(got), np.isnan(want_w))
+    ok = ~np.isnan(want_w)
+    assert np.all(np.abs(got - want_w)[ok] <= (2.0 ** -24 * want_w + 1e-12)[ok])
