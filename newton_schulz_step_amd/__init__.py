@@ -15,8 +15,9 @@ from ._binding import (  # noqa: F401
     step_noalloc, step_window, table, unpack, version, windows, workspace, workspace_size)
 from ._binding import NOALLOC_WORKSPACE_BYTES  # noqa: F401
 from ._binding import (  # noqa: F401
-    FP8_BLOCK, FP8_FORMATS, ROUTE_SCORES, Fp8, RouteHyper, combine, combine_backward, expert_order, fp8_empty,
-    fp8_matmul, fp8_matmul_grouped_k, fp8_quantize, route, route_backward, route_hyper)
+    FP8_BLOCK, FP8_FORMATS, ROUTE_SCORES, Fp8, RouteHyper, combine, combine_backward, expert_order,
+    expert_order_workspace_size, fp8_empty, fp8_matmul, fp8_matmul_grouped_k, fp8_quantize, route, route_backward,
+    route_hyper)
 from ._binding import (  # noqa: F401
     ERR_ALIGN, ERR_BAD_HYPER, ERR_BAD_METHOD, ERR_BAD_SHAPE, ERR_HIP, ERR_NULL, ERR_OVERLAP,
     ERR_RANGE, ERR_UNSUPPORTED, ERR_WORKSPACE, OK)

@@ -625,15 +625,16 @@ class _on:
             raise ValueError("with a raw stream handle the outputs must be given")
         return _torch().empty(shape, dtype=dtype, device=self.dev)
 
-    def scratch(self, nbytes):
-        """Workspace of a call: cached per (device, stream); under graph capture one of
-        its own, from the graph's memory, so that no two graphs share it."""
+    def scratch(self, nbytes, ws=None):
+        """Workspace of a call: the caller's, or one of its own. Calls of two launches pass
+        data through it, and other threads' calls may come between them on the same stream;
+        under graph capture it is from the graph's memory, so that no two graphs share it."""
+        if ws is not None or nbytes == 0:
+            return ws
+        if self.raw:
+            raise ValueError("with a raw stream handle the workspace must be given")
         torch = _torch()
-        if nbytes == 0:
-            return None
-        if not self.raw and torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
-        return workspace(nbytes, self.dev, self._stream)
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
 
 
 class Fp8:
@@ -855,23 +856,29 @@ def route_backward(dweights, logits, ids, h: RouteHyper, dlogits=None, stream=No
 
 
 @functools.lru_cache(maxsize=256)
-def _order_workspace(n: int, n_experts: int) -> int:
+def expert_order_workspace_size(n: int, n_experts: int) -> int:
+    """Bytes of workspace that ordering n slots takes (muon_expert_order_workspace_size);
+    0 for few slots."""
     need = ctypes.c_size_t(0)
     _check(load().muon_expert_order_workspace_size(n, n_experts, ctypes.byref(need)))
     return need.value
 
 
-def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=None, rows=None, pos=None, stream=None):
+def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=None, rows=None, pos=None, stream=None,
+                 ws=None):
     """Order of routed slots by expert (muon_expert_order): (offsets [experts + 1],
     counts [experts], rows [capacity], pos like ids), all int32. The capacity
     that any routing fits is ids.numel() + n_experts * (align - 1). Where none of
-    offsets, counts and rows is given they are views of one new tensor."""
+    offsets, counts and rows is given they are views of one new tensor. ws: a
+    workspace of expert_order_workspace_size bytes that no other call uses until this
+    one is done; without it the call allocates its own on its stream (with a raw
+    stream handle it has to be given where the size is not 0)."""
     torch = _torch()
     _int32(ids, None, "ids")
     n = ids.numel()
-    dev = _same_device(ids, offsets, counts, rows, pos)
+    dev = _same_device(ids, offsets, counts, rows, pos, ws)
     with _on(dev, stream) as on:
-        need = _order_workspace(n, n_experts)
+        need = expert_order_workspace_size(n, n_experts)
         capacity = max(n + n_experts * (align - 1), 0)
         if offsets is None and counts is None and rows is None:
             # one allocation: three cost as much time as the launch
@@ -885,10 +892,10 @@ def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=Non
             else:
                 _int32(rows, None, "rows")
         pos = _given(pos, ids.shape, torch.int32, on, "pos")
-        ws = on.scratch(need)
+        ws = on.scratch(need, ws)
         _check(load().muon_expert_order(_flat(ids), n, n_experts, align, _flat(offsets), _flat(counts), _flat(rows),
-                                        rows.numel(), _flat(pos), _flat(ws), 0 if ws is None else ws.numel(),
-                                        on.handle))
+                                        rows.numel(), _flat(pos), _flat(ws),
+                                        0 if ws is None else ws.numel() * ws.element_size(), on.handle))
     return offsets, counts, rows, pos
 
 
