@@ -448,7 +448,8 @@ typedef struct {
  *   group_offsets (device int32[b.batch + 1], ascending, a.batch == 1): rows
  *   [offsets[g], offsets[g + 1]) of A meet matrix g of B and give the same rows
  *   of C. Rows outside every group are not written. Offsets are clamped to
- *   [0, M] and to the previous one.
+ *   [0, M], and one that is less than an earlier one counts as the largest
+ *   before it, so that no row belongs to two groups.
  * With the forward product Y = X W^T of W (N x K): the input gradient is the
  * product of dY and W's transposed operand, the weight gradient that of the
  * transposed operands of dY and X.
@@ -464,8 +465,9 @@ int muon_fp8_matmul(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* gro
  * n_groups groups (device int32[n_groups + 1], ascending). a: M x K, b: N x K,
  * batch 1. Offsets must be multiples of 128, as muon_expert_order gives them
  * with align 128 (a group's sum runs over whole blocks, from offset / 128
- * rounded down to the next offset / 128 rounded up), and are clamped to
- * [0, K] and to the previous one. A group without columns gives zeros (with
+ * rounded down to the next offset / 128 rounded up). They are clamped to
+ * [0, K], and one that is less than an earlier one counts as the largest
+ * before it. A group without columns gives zeros (with
  * accumulate: leaves its matrix). */
 int muon_fp8_matmul_grouped_k(const muon_fp8_t* a, const muon_fp8_t* b, const int32_t* group_offsets,
                               int32_t n_groups, const muon_fp8_result_t* c, void* stream);

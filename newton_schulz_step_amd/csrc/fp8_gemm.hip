@@ -34,7 +34,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------------------
 // Groups of rows. Every wave finds a tile's group by itself: 64 groups at a time, a prefix
-// sum of their tile counts. The first 64 groups stay in registers.
+// sum of their tile counts. The first 64 groups stay in registers. Where an offset falls, the
+// largest one before it takes its place, so that no two groups own a row: a prefix maximum,
+// made only then (ascending offsets are found by one vote).
 
 __device__ __forceinline__ int wave_inclusive_sum(int v) {
   const int lane = threadIdx.x & 63;
@@ -50,28 +52,43 @@ struct Groups {
   int lo, hi, incl;   // of group `lane` of the 64: rows, tiles of it and the ones before it
   int first;          // the first of the 64
 
-  __device__ __forceinline__ void fetch(const int32_t* offsets, int n_groups, int limit, int tile_rows, int g0) {
-    const int g = g0 + (threadIdx.x & 63);
-    lo = hi = 0;
+  // `before`: where the groups before g0 end
+  __device__ __forceinline__ void fetch(const int32_t* offsets, int n_groups, int limit, int tile_rows, int g0,
+                                        int before) {
+    const int lane = threadIdx.x & 63, g = g0 + lane;
+    lo = hi = before;
     if (g < n_groups) {
       lo = min(max(offsets[g], 0), limit);
-      hi = min(max(offsets[g + 1], lo), limit);
+      hi = min(max(offsets[g + 1], 0), limit);
+    }
+    if (__ballot(lo < before || hi < lo) != 0) {
+      lo = max(lo, before);
+      hi = max(lo, hi);
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(hi, o, 64);
+        if (lane >= o) hi = max(hi, up);
+      }
+      const int up = __shfl_up(hi, 1, 64);
+      if (lane > 0) lo = up;
     }
     incl = wave_inclusive_sum((hi - lo + tile_rows - 1) / tile_rows);
     first = g0;
   }
+  __device__ __forceinline__ int end() const { return __builtin_amdgcn_readlane(hi, 63); }   // of all 64
   __device__ __forceinline__ int tiles() const { return __builtin_amdgcn_readlane(incl, 63); }
 };
 
 // Row tiles of all groups.
 __device__ __forceinline__ int count_group_tiles(const int32_t* offsets, int n_groups, int limit, int tile_rows,
                                                  Groups& cache) {
-  cache.fetch(offsets, n_groups, limit, tile_rows, 0);
-  int n = cache.tiles();
+  cache.fetch(offsets, n_groups, limit, tile_rows, 0, 0);
+  int n = cache.tiles(), before = cache.end();
   for (int g0 = 64; g0 < n_groups; g0 += 64) {
     Groups more;
-    more.fetch(offsets, n_groups, limit, tile_rows, g0);
+    more.fetch(offsets, n_groups, limit, tile_rows, g0, before);
     n += more.tiles();
+    before = more.end();
   }
   return n;
 }
@@ -83,7 +100,7 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups,
   while (tile >= g.tiles()) {
     tile -= g.tiles();
     if (g.first + 64 >= n_groups) return false;
-    g.fetch(offsets, n_groups, limit, tile_rows, g.first + 64);
+    g.fetch(offsets, n_groups, limit, tile_rows, g.first + 64, g.end());
   }
   const int l = __builtin_ctzll(__ballot(g.incl > tile));
   const int lo = __builtin_amdgcn_readlane(g.lo, l), hi = __builtin_amdgcn_readlane(g.hi, l);
@@ -94,12 +111,22 @@ __device__ __forceinline__ bool find_group(const int32_t* offsets, int n_groups,
   return true;
 }
 
+// Whether no offset of a grouped contraction falls.
+__device__ __forceinline__ bool offsets_ascend(const Fp8Gemm& g) {
+  bool falls = false;
+  for (int z = threadIdx.x & 63; z < g.batch; z += 64) falls = falls || g.offsets[z + 1] < g.offsets[z];
+  return __ballot(falls) == 0;
+}
+
 // Blocks [kb0, kb1) of group z of a grouped contraction (scalar loads: z is uniform), [0, 0)
 // of one without columns: its first block may lie behind the operand's last.
-__device__ __forceinline__ void group_blocks(const Fp8Gemm& g, int z, int& kb0, int& kb1) {
+__device__ __forceinline__ void group_blocks(const Fp8Gemm& g, int z, bool ascend, int& kb0, int& kb1) {
   const auto* off = (const __attribute__((address_space(4))) int32_t*)(g.offsets);
   const int limit = g.kb * 128;
-  const int lo = min(max(off[z], 0), limit);
+  int most = off[z];   // of the offsets up to it
+  if (!ascend)
+    for (int i = 0; i < z; ++i) most = max(most, off[i]);
+  const int lo = min(max(most, 0), limit);
   const int hi = min(max(off[z + 1], lo), limit);
   kb0 = hi > lo ? lo / 128 : 0;
   kb1 = hi > lo ? (hi + 127) / 128 : 0;
@@ -107,7 +134,8 @@ __device__ __forceinline__ void group_blocks(const Fp8Gemm& g, int z, int& kb0, 
 
 // 64 groups of a contraction from the one with most blocks to the one with least: lane r
 // holds the r-th. A lane counts the longer groups (those as long, before it) and sends its
-// number to that lane; lanes without a group are the shortest ones.
+// number to that lane; lanes without a group are the shortest ones. (An order only: where
+// offsets fall, the lengths here are not the groups' own.)
 __device__ __forceinline__ int longest_first(const Fp8Gemm& g, int first) {
   const int lane = threadIdx.x & 63, limit = g.kb * 128, z = first + lane;
   int blocks = -1;
@@ -205,13 +233,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
   struct { int m0, mend, mat, amat, bmat, kb0, kb1; } w = {mt * TM, static_cast<int>(g.M), z, z, z, 0, g.kb};
   if (g.mode == FP8_GROUP_ROWS) {
     Groups groups;
-    groups.fetch(g.offsets, g.batch, static_cast<int>(g.M), TM, 0);
+    groups.fetch(g.offsets, g.batch, static_cast<int>(g.M), TM, 0, 0);
     if (!find_group(g.offsets, g.batch, static_cast<int>(g.M), TM, groups, mt, w.mat, w.m0, w.mend)) return;
     w.amat = 0;
     w.bmat = w.mat;
   } else if (g.mode == FP8_GROUP_K) {
     w.amat = w.bmat = 0;
-    group_blocks(g, z, w.kb0, w.kb1);
+    group_blocks(g, z, offsets_ascend(g), w.kb0, w.kb1);
   }
   const int r = lane & 15, p = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(nt) * 16;
@@ -381,6 +409,7 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   // longest first, and every second round runs backwards: 1.05 to 1.13 times.
   constexpr int ROUND = TILE == 256 ? 256 : 512;
   const bool by_length = g.mode == FP8_GROUP_K && total > ROUND;
+  const bool ascend = g.mode == FP8_GROUP_K && offsets_ascend(g);
   int sorted = 0, sorted_first = -1;   // the 64 groups from sorted_first on
   auto tile_at = [&](int index) {
     const int chunk = index / ROUND, inside = index % ROUND;
@@ -412,7 +441,7 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
     if (g.mode == FP8_GROUP_ROWS)
       find_group(g.offsets, g.batch, static_cast<int>(g.M), TILE, groups, mt, t.mat, t.m0, t.mend);
     else if (g.mode == FP8_GROUP_K)
-      group_blocks(g, z, t.kb0, t.kb1);
+      group_blocks(g, z, ascend, t.kb0, t.kb1);
     t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
     t.mend = __builtin_amdgcn_readfirstlane(t.mend);
     t.mat = __builtin_amdgcn_readfirstlane(t.mat);
