@@ -362,7 +362,8 @@ double muon_comm_elements(int64_t p_m, int32_t n_ranks, int32_t zero_stage, int3
  * cols by the products below. Row r's columns [128 b, 128 b + 128) are one
  * block with one scale 2^e: element = value8 * 2^e, the value in e4m3 (no
  * infinities, largest 448) or e5m2 (largest finite 57344), e stored as the
- * byte e + 127. A power of two loses nothing to the scale itself, and the
+ * byte e + 127 (0 .. 254; 255 makes the block NaN, and is never written by
+ * muon_fp8_quantize). A power of two loses nothing to the scale itself, and the
  * matrix instruction applies it exactly while it multiplies.
  *   data   batch x rows x P bytes, P = cols rounded up to a multiple of 128;
  *          columns [cols, P) hold zeros. 16-byte aligned.
@@ -443,7 +444,9 @@ typedef struct {
  * fp32 and rounded once. a: M x K, b: N x K (same K). A BF16 or F16 result is
  * formed by the 8-bit matrix instructions, which cut each product to 13 bits
  * below the largest of its eight neighbours along k (about 1.3e-5 of the
- * result's norm); an F32 result from exact products, at half their rate.
+ * result's norm); an F32 result from exact products, at half their rate
+ *   (a part of C with results that are not finite, or beyond 2^94, is made
+ *   twice, up to ten times slower).
  *   group_offsets NULL: a.batch == b.batch, one product per matrix.
  *   group_offsets (device int32[b.batch + 1], ascending, a.batch == 1): rows
  *   [offsets[g], offsets[g + 1]) of A meet matrix g of B and give the same rows

@@ -19,7 +19,11 @@
 // which a 16-bit result (2e-4 for fp16, 2e-3 for bf16) does not show. For a 32-bit
 // result the operands are converted to bf16 in registers, scale included (exact: 8-bit
 // values have at most 4 significant bits), and multiplied by the bf16 instructions,
-// whose sums keep 24 bits: 2e-7 of the norm, at half the rate.
+// whose sums keep 24 bits: 2e-7 of the norm, at half the rate. bf16 has fp32's range, which
+// values times scales can leave. So scales are raised by 2^17, which takes in the smallest
+// ones, and where a result is not finite then (large ones beyond about 2^95, or NaN and
+// infinities in the data) its sums are made once more: scales cut to what bf16 takes, each
+// block's sum multiplied by what was cut off. Ordinary data never comes there.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -169,10 +173,27 @@ __device__ __forceinline__ void store_c(void* c, int dtype, int64_t i, float v) 
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ float scale_value(int word, int byte) {
-  const uint32_t b = (static_cast<uint32_t>(word) >> (8 * byte)) & 255u;
-  return __uint_as_float(b != 0 ? b << 23 : 0x400000u);   // byte 0 is 2^-127
+// The scale bytes whose 8-bit values are normal bf16 numbers, from the smallest (2^-9 for
+// e4m3, 2^-16 for e5m2) to the largest (448, 57344).
+template <int F> struct ScaleRange {
+  static constexpr int LOW = F == MUON_FP8_E4M3 ? 10 : 17, HIGH = F == MUON_FP8_E4M3 ? 246 : 239;
+};
+template <int F>
+__device__ __forceinline__ int near_scale(int byte) { return min(max(byte, ScaleRange<F>::LOW), ScaleRange<F>::HIGH); }
+// What near_scale cut off, as a factor; byte 255 stands for a NaN.
+template <int F>
+__device__ __forceinline__ float rest_scale(int byte) {
+  return byte == 255 ? __builtin_nanf("") : __uint_as_float(static_cast<uint32_t>(byte - near_scale<F>(byte) + 127) << 23);
 }
+
+__device__ __forceinline__ float scale_value(int byte) { return __uint_as_float(static_cast<uint32_t>(byte) << 23); }
+
+// 2^17 times the scale: every value of the smallest scales is a normal number then. Scales
+// too large for that become a NaN, their values or the sum infinite, so that a finite sum
+// of such products, 2^34 times the wanted one, is right.
+constexpr int kRaise = ScaleRange<MUON_FP8_E5M2>::LOW;
+constexpr float kLower = 1.0f / (1ull << (2 * kRaise));
+__device__ __forceinline__ float raised_scale(int byte) { return scale_value(min(byte + kRaise, 255)); }
 
 template <int F, bool HI>
 __device__ __forceinline__ bf16x2 to_bf16(int w, float s) {
@@ -197,13 +218,17 @@ __device__ __forceinline__ bf16x8 to_bf16x8(int lo, int hi, float s) {
 // still in the last-level cache, 13 us from memory.
 constexpr int kFewWaves = 8;
 
-template <int FA, int FB, bool WIDE, int U>
+template <int FA, int FB, bool WIDE, bool FAR, int U>
 __device__ __forceinline__ void few_step(const i32x4& a0, const i32x4& a1, const i32x4& b0, const i32x4& b1, int sa,
                                          int sb, f32x4& acc) {
   // B's rows are the instruction's rows: register e of lane l is column 4 (l / 16) + e
   // of the tile, row l % 16
   if constexpr (WIDE) {
-    const float fsa = scale_value(sa, U), fsb = scale_value(sb, U);
+    const int ba = (static_cast<uint32_t>(sa) >> (8 * U)) & 255, bb = (static_cast<uint32_t>(sb) >> (8 * U)) & 255;
+    const float fsa = FAR ? scale_value(near_scale<FA>(ba)) : raised_scale(ba);
+    const float fsb = FAR ? scale_value(near_scale<FB>(bb)) : raised_scale(bb);
+    const f32x4 sum = acc;
+    if constexpr (FAR) acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(b0[2 * h], b0[2 * h + 1], fsb),
@@ -212,6 +237,12 @@ __device__ __forceinline__ void few_step(const i32x4& a0, const i32x4& a1, const
     for (int h = 0; h < 2; ++h)
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8<FB>(b1[2 * h], b1[2 * h + 1], fsb),
                                                     to_bf16x8<FA>(a1[2 * h], a1[2 * h + 1], fsa), acc, 0, 0, 0);
+    if constexpr (FAR) {
+      const float ra = rest_scale<FA>(ba);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[e] = sum[e] + acc[e] * (ra * rest_scale<FB>(__shfl(bb, ((threadIdx.x >> 4) & 3) * 4 + e, 64)));
+    }
   } else {
     const i32x8 fa = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
     const i32x8 fb = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -256,32 +287,51 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Gemm g,
     psa[i] = g.sa + w.amat * g.sa_batch + ra * g.s_pitch;
     acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  for (int q = w.kb0 / 4 + wave; q * 4 < w.kb1; q += kFewWaves) {
-    const int sb = *reinterpret_cast<const int*>(psb + q * 4);
-    // blocks outside [kb0, kb1) load the first one of the range and are not used
-    int64_t at[4];
-    bool in[4];
-    i32x4 b0[4], b1[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      in[u] = q * 4 + u >= w.kb0 && q * 4 + u < w.kb1;
-      at[u] = static_cast<int64_t>(in[u] ? q * 4 + u : w.kb0) * 128;
-      b0[u] = *reinterpret_cast<const i32x4*>(pb + at[u]);
-      b1[u] = *reinterpret_cast<const i32x4*>(pb + at[u] + 64);
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int sa = *reinterpret_cast<const int*>(psa[i] + q * 4);
-      i32x4 a0[4], a1[4];
+  auto contract = [&](auto far) {
+    constexpr bool FAR = decltype(far)::value;
+    for (int q = w.kb0 / 4 + wave; q * 4 < w.kb1; q += kFewWaves) {
+      const int sb = *reinterpret_cast<const int*>(psb + q * 4);
+      // blocks outside [kb0, kb1) load the first one of the range and are not used
+      int64_t at[4];
+      bool in[4];
+      i32x4 b0[4], b1[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        a0[u] = *reinterpret_cast<const i32x4*>(pa[i] + at[u]);
-        a1[u] = *reinterpret_cast<const i32x4*>(pa[i] + at[u] + 64);
+        in[u] = q * 4 + u >= w.kb0 && q * 4 + u < w.kb1;
+        at[u] = static_cast<int64_t>(in[u] ? q * 4 + u : w.kb0) * 128;
+        b0[u] = *reinterpret_cast<const i32x4*>(pb + at[u]);
+        b1[u] = *reinterpret_cast<const i32x4*>(pb + at[u] + 64);
       }
-      if (in[0]) few_step<FA, FB, WIDE, 0>(a0[0], a1[0], b0[0], b1[0], sa, sb, acc[i]);
-      if (in[1]) few_step<FA, FB, WIDE, 1>(a0[1], a1[1], b0[1], b1[1], sa, sb, acc[i]);
-      if (in[2]) few_step<FA, FB, WIDE, 2>(a0[2], a1[2], b0[2], b1[2], sa, sb, acc[i]);
-      if (in[3]) few_step<FA, FB, WIDE, 3>(a0[3], a1[3], b0[3], b1[3], sa, sb, acc[i]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int sa = *reinterpret_cast<const int*>(psa[i] + q * 4);
+        i32x4 a0[4], a1[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          a0[u] = *reinterpret_cast<const i32x4*>(pa[i] + at[u]);
+          a1[u] = *reinterpret_cast<const i32x4*>(pa[i] + at[u] + 64);
+        }
+        if (in[0]) few_step<FA, FB, WIDE, FAR, 0>(a0[0], a1[0], b0[0], b1[0], sa, sb, acc[i]);
+        if (in[1]) few_step<FA, FB, WIDE, FAR, 1>(a0[1], a1[1], b0[1], b1[1], sa, sb, acc[i]);
+        if (in[2]) few_step<FA, FB, WIDE, FAR, 2>(a0[2], a1[2], b0[2], b1[2], sa, sb, acc[i]);
+        if (in[3]) few_step<FA, FB, WIDE, FAR, 3>(a0[3], a1[3], b0[3], b1[3], sa, sb, acc[i]);
+      }
+    }
+  };
+  contract(std::false_type{});
+  if constexpr (WIDE) {
+    float test = 0.0f;   // a NaN if a sum is not finite
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        test += acc[i][e] * 0.0f;
+        acc[i][e] *= kLower;
+      }
+    if (__ballot(test != 0.0f) != 0) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      contract(std::true_type{});
     }
   }
 #pragma unroll
@@ -454,9 +504,9 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
   // slices of a tile, counted in pairs
   auto slices_of = [](const Tile& t) { return max(2, (t.kb1 - t.kb0 + 1) & ~1); };
 
-  // per-lane offsets: operand rows (both operands have the same), scale rows (64 per load:
-  // of a 256-tile each wave fetches 64 rows of both operands, of a 128-tile waves 0 and 1
-  // rows of A, 2 and 3 of B)
+  // per-lane offsets of operand rows (both operands have the same). Scale rows come 64 per
+  // load: of a 256-tile each wave fetches 64 rows of both operands, of a 128-tile waves 0 and
+  // 1 rows of A, 2 and 3 of B.
   int vo[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
@@ -552,7 +602,7 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
     if constexpr (WIDE) {
       float fs[2 * WB];
 #pragma unroll
-      for (int i = 0; i < 2 * WB; ++i) fs[i] = scale_value(sc[U][i], 0);
+      for (int i = 0; i < 2 * WB; ++i) fs[i] = raised_scale(sc[U][i]);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         bf16x8 xa[WB], xb[WB];
@@ -634,8 +684,9 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
             *reinterpret_cast<u16x4*>(stage + r * (CH * 16) + (((b * 4 + q) ^ (r & (CH - 1))) * 16) + h * 8) =
                 round4<T>(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
           } else {
+            constexpr float f = WIDE ? kLower : 1.0f;
             *reinterpret_cast<f32x4*>(stage + (r % RS) * 128 + (((2 * q + h) ^ (r & 7)) * 16)) =
-                f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                f32x4{x[4 * q] * f, x[4 * q + 1] * f, x[4 * q + 2] * f, x[4 * q + 3] * f};
           }
         }
     }
@@ -771,6 +822,71 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
     });
   };
 
+  // WIDE: whether a result of the wave's part of a tile, or one beyond its edges, is not finite
+  auto is_far = [&]() {
+    float test = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WB; ++i)
+#pragma unroll
+      for (int j = 0; j < WB; ++j) {
+        if constexpr (TILE == 256) asm volatile("" : "+a"(acc[i][j]));   // they stay in accumulation registers
+#pragma unroll
+        for (int e = 0; e < 16; ++e) test += acc[i][j][e] * 0.0f;
+        if constexpr (TILE == 256) asm volatile("" : "+a"(acc[i][j]), "+v"(test));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    return __ballot(test != 0.0f) != 0;
+  };
+  // Such a part is made once more, one block at a time straight from memory: each slice's sum
+  // with the scales that fit, times what they were cut by, is added in fp32 (5632 x 2048 x
+  // 16383 of NaN: 2.4 ms instead of 0.32).
+  auto store_far = [&](const Tile& t) {
+    const uint8_t* da = g.a + (g.mode == FP8_DENSE ? t.mat * g.a_batch : 0) + h * 32;
+    const uint8_t* db = g.b + (g.mode == FP8_GROUP_K ? 0 : t.mat * g.b_batch) + h * 32;
+    const uint8_t* sa = g.sa + (g.mode == FP8_DENSE ? t.mat * g.sa_batch : 0);
+    const uint8_t* sb = g.sb + (g.mode == FP8_GROUP_K ? 0 : t.mat * g.sb_batch);
+#pragma unroll 1
+    for (int block = 0; block < WB * WB; ++block) {
+      const int m = t.m0 + wm * HALF + block / WB * 32, n = t.n0 + wn * HALF + block % WB * 32;
+      if (m >= t.mend || n >= g.N) continue;
+      const int64_t ra = min(m + r, t.mend - 1), rb = min<int64_t>(n + r, g.N - 1);
+      f32x16 total;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) total[e] = 0.0f;
+#pragma unroll 1
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const int ba = sa[ra * g.s_pitch + kb], bb = sb[rb * g.s_pitch + kb];
+        const float fsa = scale_value(near_scale<FA>(ba)), fsb = scale_value(near_scale<FB>(bb));
+        f32x16 sum;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e] = 0.0f;
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) {   // 16 of the lane's 64 bytes
+          const int at = kb * 128 + (p >> 1) * 64 + (p & 1) * 16;
+          const i32x4 xa = *reinterpret_cast<const i32x4*>(da + ra * g.pitch + at);
+          const i32x4 xb = *reinterpret_cast<const i32x4*>(db + rb * g.pitch + at);
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(to_bf16x8<FB>(xb[2 * s], xb[2 * s + 1], fsb),
+                                                          to_bf16x8<FA>(xa[2 * s], xa[2 * s + 1], fsa), sum, 0, 0, 0);
+        }
+        const float rest = rest_scale<FA>(ba);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          total[e] += sum[e] * (rest * rest_scale<FB>(__shfl(bb, (e >> 2) * 8 + h * 4 + (e & 3), 64)));
+          if ((e & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t col = n + (e >> 2) * 8 + h * 4 + (e & 3);
+        if (m + r >= t.mend || col >= g.N) continue;
+        const int64_t at = (g.mode == FP8_GROUP_ROWS ? 0 : t.mat * g.c_batch) + (m + r) * g.ldc + col;
+        store_c(g.c, g.c_dtype, at, total[e] + (g.accumulate ? load_c(g.c, g.c_dtype, at) : 0.0f));
+      }
+    }
+  };
+
   int index = blockIdx.x;
   if (index >= total) return;
   Tile cur = tile_at(index);
@@ -838,7 +954,8 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
     }
     // no load may be on its way into LDS when the workgroup ends
     if (!more) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    store(cur);
+    if (WIDE && __builtin_expect(is_far(), 0)) store_far(cur);
+    else store(cur);
     if (!more) return;
     cur = nxt;
     clear();
