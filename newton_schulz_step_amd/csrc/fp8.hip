@@ -190,6 +190,10 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs a) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = value(i, e);
+        if (WEIGHTED && ncol < 8) {   // columns behind the last one stay zeros, also for a weight that is not finite
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = e < ncol ? v[e] : 0.0f;
+        }
         *reinterpret_cast<u32x2*>(q + r * a.qp + c0) = pack8<FMT>(v, inverse_scale(byte));
         if (cg == 0) s[r * a.qs + ct] = static_cast<uint8_t>(byte);
         if (ct == a.col_tiles - 1 && cg > 0 && ct + cg < a.qs) s[r * a.qs + ct + cg] = 127;   // padding
