@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 from typing import Dict, Iterable, List, Optional, Sequence, Tuple
@@ -557,6 +558,14 @@ def _fp8_types():
     return _FP8_TYPES
 
 
+def _i32(v, name) -> int:
+    """v as the C ABI's 32-bit integer; ctypes alone would drop the upper bits."""
+    v = operator.index(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} must be a 32-bit integer, got {v}")
+    return v
+
+
 def _same_device(first, *others):
     """The GPU that `first` and the others (None skipped) live on."""
     dev = first.device
@@ -706,6 +715,7 @@ def fp8_quantize(x, fmt: str = "e4m3", blocks: bool = False, transposed="no", ro
         raise ValueError(f"format must be one of {sorted(FP8_FORMATS)}, got {fmt!r}")
     if (out is not None and transposed == "only") or (out_t is not None and transposed == "no"):
         raise ValueError("an output was given that `transposed` does not ask for")
+    row_div = _i32(row_div, "row_div")
     for t, dt, name in ((row_index, torch.int32, "row_index"), (row_weight, torch.float32, "row_weight")):
         if t is not None and t.dtype != dt:
             raise TypeError(f"{name} must be {dt}")
@@ -802,7 +812,7 @@ def route_hyper(**kw) -> RouteHyper:
             v = ROUTE_SCORES.get(v, -1)
         if not hasattr(h, k) or k == "reserved":
             raise TypeError(f"unknown router hyperparameter {k!r}")
-        setattr(h, k, v)
+        setattr(h, k, v if k == "scale" else _i32(v, k))
     return h
 
 
@@ -860,7 +870,7 @@ def expert_order_workspace_size(n: int, n_experts: int) -> int:
     """Bytes of workspace that ordering n slots takes (muon_expert_order_workspace_size);
     0 for few slots."""
     need = ctypes.c_size_t(0)
-    _check(load().muon_expert_order_workspace_size(n, n_experts, ctypes.byref(need)))
+    _check(load().muon_expert_order_workspace_size(n, _i32(n_experts, "n_experts"), ctypes.byref(need)))
     return need.value
 
 
@@ -875,7 +885,7 @@ def expert_order(ids, n_experts: int, align: int = 128, offsets=None, counts=Non
     stream handle it has to be given where the size is not 0)."""
     torch = _torch()
     _int32(ids, None, "ids")
-    n = ids.numel()
+    n, n_experts, align = ids.numel(), _i32(n_experts, "n_experts"), _i32(align, "align")
     dev = _same_device(ids, offsets, counts, rows, pos, ws)
     with _on(dev, stream) as on:
         need = expert_order_workspace_size(n, n_experts)
