@@ -794,10 +794,13 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
       }
       if constexpr (K + 1 < WB * NS * NJ) stage_write(Int<K + 1>{});
       if (whole) {
-        // 16-bit results leave as whole lines that are not read here again: past the cache
-        // they leave room for operands (experts' weight gradients 251 -> 210 us). fp32 ones
-        // leave as half lines, which the cache has to join (past it 8192 x 8192 x 512 took
-        // 176 instead of 97 us).
+        // Rounded results are not read here again: past the cache they leave room for operands.
+        // 256-tiles store whole lines (weight gradients of 64 x 1408 x 2048 over 768 columns
+        // each 226 -> 189 us, 8192 x 8192 x 512 67 -> 54), 128-tiles half lines, still the
+        // faster way (2048 x 4096 x 4096 36.7 -> 35.5 us, x 512 12.1 -> 11.8). Sums with 16-bit
+        // results go through the cache, which has their lines already (past it the weight
+        // gradients took 361 instead of 357 us), and so do the half lines of fp32 results, which
+        // it has to join (past it 8192 x 8192 x 512 took 176 instead of 97 us).
         char* to = c + J * 32 * ESZ;
 #pragma unroll
         for (int p = 0; p < NP; ++p, to += step) {
@@ -809,8 +812,12 @@ __device__ __forceinline__ void tile_product(const Fp8Gemm& g, int mtiles, int n
             reinterpret_cast<f32x4_any*>(to)[0] = v[p].lo;
             reinterpret_cast<f32x4_any*>(to)[1] = v[p].hi;
           } else {
-            if constexpr (!ROUNDED) add_16(v[p], pu[p]);
-            __builtin_nontemporal_store(v[p].u, reinterpret_cast<u16x8_any*>(to));
+            if constexpr (ROUNDED) {
+              __builtin_nontemporal_store(v[p].u, reinterpret_cast<u16x8_any*>(to));
+            } else {
+              add_16(v[p], pu[p]);
+              *reinterpret_cast<u16x8_any*>(to) = v[p].u;
+            }
           }
         }
       }
