@@ -136,3 +136,18 @@ def test_groups_of_rows(lib, M, N, K, G, kernel, dtype):
             at = slice(off[g], off[g + 1])
             check_product(got[at], va[at], vb[g][cols], dtype, base[at] if accumulate else None)
         assert np.all(got[:off[0]] == 7.0) and np.all(got[off[-1]:] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(3, 40), (1100, 1000), (8000, 8100)])
+def test_no_terms(lib, M, N, dtype):
+    # a contraction of length zero, on all kernels: zeros, or what is there
+    import torch
+    for a, b, shape, kw in ((lib.fp8_empty(M, 0), lib.fp8_empty(N, 0), (M, N), {}),
+                            (lib.fp8_empty(M, 0), lib.fp8_empty(N, 0, batch=2), (M, N),
+                             dict(offsets=torch.tensor([0, M // 2, M], dtype=torch.int32).cuda()))):
+        out = torch.full(shape, 3.0, dtype=dt(torch, dtype), device="cuda")
+        lib.fp8_matmul(a, b, out=out, accumulate=True, **kw)
+        assert torch.all(out == 3.0)
+        lib.fp8_matmul(a, b, out=out, **kw)
+        assert torch.all(out == 0.0)
