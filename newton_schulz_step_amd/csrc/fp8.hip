@@ -9,9 +9,9 @@
 // One workgroup takes a 128 x 128 tile: it reads the tile once and writes it in both
 // orientations, since a training step needs the rows for one product and the columns
 // for another. What bounds it is HBM: the source once, one byte per element and
-// orientation, 1/128 byte of scales. Both orientations of 8192 x 4096 bf16: 34 us
-// (4.0 TB/s; 43 us with the inputs held as floats); of 64 x
-// 1408 x 2048 fp32 weights: 201 us (5.5 TB/s, a large copy reaches 5.1).
+// orientation, 1/128 byte of scales. Both orientations of 8192 x 4096 bf16: 32.5
+// us (4.1 TB/s; 43 us with the inputs held as floats); of 64 x 1408 x 2048 fp32 weights:
+// 202 us (5.5 TB/s, a large copy reaches 5.1).
 #include "common.hpp"
 #include "fp8.hpp"
 
@@ -109,7 +109,7 @@ __device__ __forceinline__ u32x2 pack8(const float (&v)[8], float inv) {
 
 // Thread t of 256 holds rows 8 (t / 16) .. + 7 and columns 8 (t % 16) .. + 7 of the
 // tile, 64 values in registers. A row's 128 columns lie in 16 neighbouring lanes (four
-// butterfly steps give its amax); a column's 128 rows lie in 16 threads 16 apart (two
+// rotations within them give its amax); a column's 128 rows lie in 16 threads 16 apart (two
 // butterfly steps, then LDS across the four waves). The transposed tile goes through
 // LDS in 8-byte pieces (8 rows of a column), piece g of column c at place
 // g ^ ((c / 8) % 16), so that the 16 columns a wave writes at once fall in 16 places.

@@ -214,8 +214,8 @@ __device__ __forceinline__ bf16x8 to_bf16x8(int lo, int hi, float s) {
 // order. The weights are read once from memory straight into the instruction's registers;
 // with four blocks in flight per wave that keeps the memory system busy, which is all that
 // bounds a product of a few tokens. Rows beyond the matrix repeat its last row (their
-// results are not stored). One token, 11008 x 4096: 11 us (4.1 TB/s) where the weights are
-// still in the last-level cache, 13 us from memory.
+// results are not stored). One token, 11008 x 4096: 12.4 us where the weights are still in
+// the last-level cache, 12.5 to 12.8 from memory (3.6 TB/s).
 constexpr int kFewWaves = 8;
 
 template <int FA, int FB, bool WIDE, bool FAR, int U>
@@ -987,9 +987,10 @@ static int tile_rows(int kind) {
 // 128-tiles run two workgroups per CU, counted as two rounds). It weighs reading B again
 // for every 16 to 64 rows against a wide tile's empty rows and idle CUs. For instance
 // (us, few rows 16 / 32 / 64, tiles 128 / 256; bf16, K = 4096):
-//   1 x 11008: 11 / 13 / 16 / 23 / 39       64 x 4096: 20 / 15 / 13 / 16 / 39
-//   128 x 11008: 90 / 68 / 62 / 24 / 42     2048 x 4096: - / - / - / 36 / 47
-//   8192 x 11008: - / - / - / 416 / 306
+//   1 x 11008: 12 / 15 / 18 / 23 / 39       64 x 4096: 20 / 15 / 13.5 / 16 / 39
+//   128 x 11008: 89 / 68 / 62 / 25 / 39     2048 x 4096: - / - / - / 36 / 45
+//   256 x 4096: 66 / 50 / 43 / 17 / 39      8192 x 11008: - / - / - / 342 / 281
+// fp32 results: 64 x 4096: 20 / 18 / 14 / 33 / 93    8192 x 11008: - / - / - / 648 / 615
 // Of groups only the total of their rows is known here; half a tile is added for each.
 Fp8Plan plan_fp8_gemm(int64_t M, int64_t N, int64_t kb, int32_t mode, int64_t batch, bool wide) {
   struct Cost { double start, round, block; };
