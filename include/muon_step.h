@@ -504,7 +504,9 @@ void muon_default_route_hyper(muon_route_hyper_t* h);
  * pitch ld elements. bias: device float32[experts] or NULL, added for the
  * choice only. Per token, in 64 bits:
  *   s = softmax(logits) or sigmoid(logits);  key = s + bias;
- *   with n_groups > 1 only the top_groups groups of largest score are kept;
+ *   with n_groups > 1 only the top_groups groups of largest score are kept (the
+ *   sum of a group's group_top largest keys, of as many as are not -inf; a group
+ *   without any is not kept);
  *   the top_k experts of largest key, in that order, ties to the lower index;
  *   weight = scale * s, divided by the sum of the chosen s + 1e-20 with
  *   renormalize.
