@@ -62,7 +62,10 @@
  * ragged row groups of mixture-of-experts layers), the routing of rows to
  * experts, and the weighted sum of the experts' outputs. A weight gradient can
  * be written straight into the packed gradients that muon_step reads, and the
- * 8-bit weights are quantised straight from its packed params.
+ * 8-bit weights are quantised straight from its packed params. Between those
+ * products stand the norm of the residual stream, attention and the embedding,
+ * each with its gradient, and between the gradients and the step their clipping
+ * by the global norm.
  */
 #ifndef MUON_STEP_H
 #define MUON_STEP_H
@@ -564,6 +567,123 @@ int muon_combine_backward(const void* dy, int32_t dtype, int64_t tokens, int64_t
                           const void* o, int64_t o_rows, int64_t ld_o, const int32_t* pos,
                           const float* weights, int32_t top_k, float* dweights, void* d_o,
                           int64_t ld_do, void* stream);
+
+/* ---- Norm, embedding, clipping ------------------------------------------- */
+
+/* Rows of at most MUON_NORM_MAX_COLS columns are normed. */
+#define MUON_NORM_MAX_COLS 16384
+
+/* Rows to norm: rows x cols elements of `dtype`, row pitches in elements. */
+typedef struct {
+  const void* x;          /* device */
+  int64_t ld_x;
+  const void* residual;   /* device, added to x first; NULL: none */
+  int64_t ld_residual;
+  const void* weight;     /* device, cols elements of weight_dtype; NULL: ones */
+  int64_t rows;
+  int64_t cols;           /* 1 .. MUON_NORM_MAX_COLS */
+  int32_t dtype;          /* F32 | BF16 | F16 */
+  int32_t weight_dtype;
+  float eps;              /* >= 0 */
+  int32_t reserved;
+} muon_norm_t;
+
+/* Root-mean-square norm of each row, with sums in fp32:
+ *   s = x + residual, rounded to dtype (x itself without a residual);
+ *   rstd = 1 / sqrt(mean(s^2) + eps);  y = s * rstd * weight, rounded to dtype.
+ *   sum   device, dtype, rows x cols, pitch ld_sum: s, the stream that goes on
+ *         past the layer; NULL: not wanted.
+ *   y     device, dtype, rows x cols, pitch ld_y; NULL: not wanted.
+ *   q     rows x cols, batch 1: y in 8 bits, the bytes that muon_fp8_quantize
+ *         makes of y by rows; NULL: not wanted.
+ *   rstd  device float32[rows], for the gradient; NULL: not wanted.
+ * At least one of them must be wanted. Errors: MUON_ERR_NULL, BAD_SHAPE,
+ * UNSUPPORTED (dtypes, format), ALIGN, OVERLAP, BAD_HYPER (eps). */
+int muon_rms_norm(const muon_norm_t* n, void* sum, int64_t ld_sum, void* y, int64_t ld_y, const muon_fp8_t* q,
+                  float* rstd, void* stream);
+
+/* Its gradient. n->x holds the rows s that were normed (n->residual must be
+ * NULL, eps does not matter), rstd what the forward call gave for them.
+ *   dy       device, dtype, rows x cols: the gradient of y.
+ *   dsum     device, dtype, rows x cols: the gradient that reaches s past the
+ *            norm, added to dx; NULL: none.
+ *   dx       device, dtype, rows x cols: the gradient of s, which is that of x
+ *            and that of the residual; NULL: not wanted.
+ *   dweight  device, dweight_dtype[cols]: sum over the rows of dy * s * rstd, in
+ *            fp32 in a fixed order, rounded once; with `accumulate` added to what
+ *            is there. NULL: not wanted.
+ *   workspace  device, muon_rms_norm_backward_workspace_size() bytes, 4-byte
+ *            aligned (needed for dweight only). */
+int muon_rms_norm_backward(const muon_norm_t* n, const float* rstd, const void* dy, int64_t ld_dy, const void* dsum,
+                           int64_t ld_dsum, void* dx, int64_t ld_dx, void* dweight, int32_t dweight_dtype,
+                           int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+int muon_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes_out);
+
+/* Limits: vocab <= MUON_EMBEDDING_MAX_VOCAB, cols <= MUON_FP8_MAX_SIDE,
+ * tokens < 2^31. */
+#define MUON_EMBEDDING_MAX_VOCAB (1 << 30)
+
+/* Rows of a table (device, table_dtype, vocab x cols, row pitch ld) by token. */
+typedef struct {
+  const void* ids;        /* device, int32 (id_bytes 4) or int64 (8) [tokens] */
+  int64_t tokens;
+  int64_t vocab;
+  int64_t cols;
+  int64_t ld;             /* row pitch of the table, in elements */
+  int32_t id_bytes;
+  int32_t table_dtype;
+  float scale;
+  int32_t reserved;
+} muon_embedding_t;
+
+/* y[t] = scale * table[ids[t]], in fp32, rounded to dtype (device, tokens x cols,
+ * pitch ld_y). A token whose id lies outside [0, vocab), such as -1 for padding,
+ * gets a row of zeros. */
+int muon_embedding(const muon_embedding_t* e, const void* table, void* y, int32_t dtype, int64_t ld_y, void* stream);
+
+/* Its gradient: dtable[v] = scale * sum of dy[t] over the tokens with ids[t] = v,
+ * summed in fp32 in an order that the ids alone decide, and rounded once; every
+ * row is written, zeros where no token is. With `accumulate` the sum is added to
+ * what is there, and rows without a token are left alone. dy: device, dtype,
+ * tokens x cols, pitch ld_dy. Ids outside [0, vocab) have no gradient.
+ *   workspace  device, muon_embedding_backward_workspace_size() bytes, 16-byte
+ *              aligned. */
+int muon_embedding_backward(const muon_embedding_t* e, const void* dy, int32_t dtype, int64_t ld_dy, void* dtable,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+int muon_embedding_backward_workspace_size(const muon_embedding_t* e, size_t* bytes_out);
+
+/* One of many tensors: numel elements of `dtype` (F32, BF16, F16), contiguous. */
+typedef struct {
+  void* data;             /* device */
+  int64_t numel;          /* 0 .. MUON_MAX_TABLE_ELEMENTS; all tensors together too */
+  int32_t dtype;
+  int32_t reserved;
+} muon_tensor_t;
+
+/* At most so many tensors in one call. */
+#define MUON_CLIP_MAX_TENSORS (1 << 20)
+
+/* *sumsq (device) = the sum of the squares of all elements of n tensors (host
+ * array of descriptors), in 64 bits throughout, in a fixed order. With
+ * `accumulate` it is added to what is there. Ranks that hold different shards
+ * add up their sums before they clip.
+ *   workspace  device, muon_grad_sumsq_workspace_size() bytes, 8-byte aligned. */
+int muon_grad_sumsq(const muon_tensor_t* grads, int32_t n, int32_t accumulate, double* sumsq, void* workspace,
+                    size_t workspace_bytes, void* stream);
+int muon_grad_sumsq_workspace_size(const muon_tensor_t* grads, int32_t n, size_t* bytes_out);
+
+/* Scale n tensors by the norm that *sumsq (device) stands for:
+ *   norm = sqrt(*sumsq);  factor = min(1, max_norm / (norm + 1e-6)), in 64 bits;
+ *   outs[i] = grads[i] * factor (the factor and the product in fp32), rounded to
+ *   outs[i]'s type.
+ * outs: n tensors of the same numels, of any of the types: NULL or the same
+ * memory and type for scaling in place (not written where the factor is 1), or
+ * others, such as the entries of a packed gradient buffer. norm: device
+ * float32[1] or NULL, receives the norm. A norm that is infinite gives the factor
+ * 0, a NaN one NaN: the results then hold zeros and NaN, and *norm tells.
+ * Errors: as above, BAD_HYPER (max_norm negative or NaN). */
+int muon_grad_clip(const muon_tensor_t* grads, const muon_tensor_t* outs, int32_t n, const double* sumsq,
+                   float max_norm, float* norm, void* stream);
 
 /* Message for the last failing call on this thread ("" if none). Valid until the
  * next call on this thread. */

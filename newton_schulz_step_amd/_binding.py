@@ -12,7 +12,7 @@ import functools
 import operator
 import os
 import threading
-from typing import Dict, Iterable, List, Optional, Sequence, Tuple
+from typing import Dict, Iterable, List, NamedTuple, Optional, Sequence, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmuonstep.so")
@@ -39,6 +39,9 @@ EXPORTED = (
     "muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_grouped_k",
     "muon_default_route_hyper", "muon_route", "muon_route_backward", "muon_expert_order",
     "muon_expert_order_workspace_size", "muon_combine", "muon_combine_backward",
+    "muon_rms_norm", "muon_rms_norm_backward", "muon_rms_norm_backward_workspace_size",
+    "muon_embedding", "muon_embedding_backward", "muon_embedding_backward_workspace_size",
+    "muon_grad_sumsq", "muon_grad_sumsq_workspace_size", "muon_grad_clip",
 )
 NOALLOC_WORKSPACE_BYTES = 64 << 20     # MUON_NOALLOC_WORKSPACE_BYTES
 
@@ -122,6 +125,19 @@ class RouteHyper(ctypes.Structure):
                 ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class NormRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("weight", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class EmbeddingTokens(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("id_bytes", ctypes.c_int32),
+                ("table_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -181,6 +197,20 @@ def load() -> ctypes.CDLL:
         lib.muon_expert_order_workspace_size.argtypes = [i64, i32, ctypes.POINTER(sz)]
         lib.muon_combine.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp]
         lib.muon_combine_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp]
+        pn, pe, psz = ctypes.POINTER(NormRows), ctypes.POINTER(EmbeddingTokens), ctypes.POINTER(sz)
+        lib.muon_rms_norm.argtypes = [pn, vp, i64, vp, i64, po, vp, vp]
+        lib.muon_rms_norm_backward.argtypes = [pn, vp, vp, i64, vp, i64, vp, i64, vp, i32, i32, vp, sz, vp]
+        lib.muon_rms_norm_backward_workspace_size.argtypes = [i64, i64, psz]
+        lib.muon_embedding.argtypes = [pe, vp, vp, i32, i64, vp]
+        lib.muon_embedding_backward.argtypes = [pe, vp, i32, i64, vp, i32, vp, sz, vp]
+        lib.muon_embedding_backward_workspace_size.argtypes = [pe, psz]
+        lib.muon_grad_sumsq.argtypes = [vp, i32, i32, vp, vp, sz, vp]   # the tensors as a c_int64 array
+        lib.muon_grad_sumsq_workspace_size.argtypes = [vp, i32, psz]
+        lib.muon_grad_clip.argtypes = [vp, vp, i32, vp, ctypes.c_float, vp, vp]
+        for name in ("muon_rms_norm", "muon_rms_norm_backward", "muon_rms_norm_backward_workspace_size",
+                     "muon_embedding", "muon_embedding_backward", "muon_embedding_backward_workspace_size",
+                     "muon_grad_sumsq", "muon_grad_sumsq_workspace_size", "muon_grad_clip"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("muon_fp8_quantize", "muon_fp8_matmul", "muon_fp8_matmul_grouped_k",
                      "muon_route", "muon_route_backward", "muon_expert_order",
                      "muon_expert_order_workspace_size", "muon_combine", "muon_combine_backward"):
@@ -952,3 +982,271 @@ def combine_backward(dy, o, pos, weights, dweights=None, do=None, stream=None):
         _check(load().muon_combine_backward(dyptr, _dtype_code(dy), tokens, o.shape[1], lddy, optr, o.shape[0], ldo,
                                             _flat(pos), _flat(weights), k, _flat(dweights), doptr, lddo, on.handle))
     return dweights, do
+
+
+# ----------------------------------------------------------------------------- norm, embedding, clipping
+
+class RmsNorm(NamedTuple):
+    """What rms_norm returns: the normed rows, the rows they were made of (x, or x +
+    residual), the normed rows in 8 bits, and 1 / rms of each row."""
+    y: object
+    sum: object
+    fp8: Optional[Fp8]
+    rstd: object
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, cols]")
+    ptr, ld, _ = _last_dense(t, name)
+    return ptr, ld
+
+
+def _optional(t, shape, dtype, name):
+    """(pointer, row pitch) of an optional matrix of the given shape and type."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
+    return _matrix(t, name)
+
+
+def _norm_rows(x, weight, residual, eps):
+    rows, cols = x.shape
+    if weight is not None and tuple(weight.shape) != (cols,):
+        raise ValueError(f"weight must have {cols} elements in one dimension")
+    rptr, ldr = _optional(residual, x.shape, x.dtype, "residual")
+    xptr, ldx = _matrix(x, "x")
+    return NormRows(xptr, ldx, rptr, ldr, _flat(weight), rows, cols, _dtype_code(x),
+                    0 if weight is None else _dtype_code(weight), eps, 0)
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, fp8: str = "no", fmt: str = "e4m3", out=None,
+             out_sum=None, out_fp8: Optional[Fp8] = None, rstd=None, stream=None) -> RmsNorm:
+    """Root-mean-square norm of x's rows (muon_rms_norm), [rows, cols] with contiguous rows:
+    s = x + residual (rounded to x's type), y = s / rms(s) * weight. Returns RmsNorm(y, sum,
+    fp8, rstd): sum is s (x itself without a residual), rstd float32 [rows]. fp8: "no"
+    gives y alone, "both" also y as the Fp8 operand that fp8_quantize(y, fmt) would make, "only"
+    that without y (None). weight: [cols] of any type, None for ones. out, out_sum,
+    out_fp8, rstd: results to write into."""
+    torch = _torch()
+    if fp8 not in ("no", "only", "both"):
+        raise ValueError('fp8 must be "no", "only" or "both"')
+    if fmt not in FP8_FORMATS:
+        raise ValueError(f"format must be one of {sorted(FP8_FORMATS)}, got {fmt!r}")
+    if (out is not None and fp8 == "only") or (out_fp8 is not None and fp8 == "no") or \
+            (out_sum is not None and residual is None):
+        raise ValueError("an output was given that the call does not make")
+    n = _norm_rows(x, weight, residual, eps)
+    rows, cols = x.shape
+    dev = _same_device(x, weight, residual, out, out_sum, rstd,
+                       *(() if out_fp8 is None else (out_fp8.data, out_fp8.scale)))
+    with _on(dev, stream) as on:
+        y, total, q = None, x, None
+        yptr = sptr = None
+        ldy = lds = 0
+        if fp8 != "only":
+            y = _given(out, (rows, cols), x.dtype, on, "out")
+            yptr, ldy = _matrix(y, "out")
+        if residual is not None:
+            total = _given(out_sum, (rows, cols), x.dtype, on, "out_sum")
+            sptr, lds = _matrix(total, "out_sum")
+        if fp8 != "no":
+            if out_fp8 is None and on.raw:
+                raise ValueError("with a raw stream handle the outputs must be given")
+            q = out_fp8 if out_fp8 is not None else fp8_empty(rows, cols, fmt, dev)
+            if q.format != fmt:
+                raise ValueError(f"out_fp8 is {q.format}, the call asks for {fmt}")
+        rstd = _given(rstd, (rows,), torch.float32, on, "rstd")
+        _check(load().muon_rms_norm(ctypes.byref(n), sptr, lds, yptr, ldy, None if q is None else ctypes.byref(q._c()),
+                                    _flat(rstd), on.handle))
+    return RmsNorm(y, total, q, rstd)
+
+
+@functools.lru_cache(maxsize=256)
+def rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    """Bytes of workspace that the weight's gradient takes (muon_rms_norm_backward_workspace_size)."""
+    need = ctypes.c_size_t(0)
+    _check(load().muon_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(need)))
+    return need.value
+
+
+def rms_norm_backward(dy, sum, weight, rstd, dsum=None, dx=None, dweight=None, accumulate: bool = False, ws=None,
+                      stream=None):
+    """Gradient of rms_norm (muon_rms_norm_backward): (dx, dweight), from the gradient dy of y,
+    the forward call's `sum` and `rstd`, and dsum, the gradient that reaches the sum past the
+    norm (None: none). dx is the gradient of x and of the residual alike. dweight: float32
+    [cols], or the tensor of any type that is given; with accumulate the gradient is added
+    to it. None where weight is None."""
+    torch = _torch()
+    n = _norm_rows(sum, weight, None, 0.0)
+    rows, cols = sum.shape
+    dyptr, lddy = _optional(dy, sum.shape, sum.dtype, "dy")
+    dsptr, ldds = _optional(dsum, sum.shape, sum.dtype, "dsum")
+    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (rows,):
+        raise ValueError(f"rstd must be float32 with {rows} elements")
+    if weight is None and dweight is not None:
+        raise ValueError("dweight was given without a weight")
+    if accumulate and dweight is None:
+        raise ValueError("accumulate needs dweight")
+    dev = _same_device(sum, dy, weight, rstd, dsum, dx, dweight, ws)
+    with _on(dev, stream) as on:
+        dx = _given(dx, (rows, cols), sum.dtype, on, "dx")
+        dxptr, lddx = _matrix(dx, "dx")
+        need = 0
+        if weight is not None:
+            if dweight is None:
+                dweight = on.fresh((cols,), torch.float32)
+            elif tuple(dweight.shape) != (cols,):
+                raise ValueError(f"dweight must have {cols} elements in one dimension")
+            need = rms_norm_backward_workspace_size(rows, cols)
+        ws = on.scratch(need, ws)
+        _check(load().muon_rms_norm_backward(ctypes.byref(n), _flat(rstd), dyptr, lddy, dsptr, ldds, dxptr, lddx,
+                                             _flat(dweight), 0 if dweight is None else _dtype_code(dweight),
+                                             int(bool(accumulate)), _flat(ws),
+                                             0 if ws is None else ws.numel() * ws.element_size(), on.handle))
+    return dx, dweight
+
+
+def _tokens(ids, vocab, cols, ld, table_dtype, scale):
+    torch = _torch()
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64")
+    return EmbeddingTokens(_flat(ids), ids.numel(), vocab, cols, ld, ids.element_size(), table_dtype, scale, 0)
+
+
+def embedding(ids, table, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """Rows of table [vocab, cols] by token, times scale (muon_embedding): ids' shape + [cols].
+    ids: int32 or int64, contiguous; one outside [0, vocab), such as -1, gives zeros. out: a
+    contiguous result to write into, else a new one of out_dtype (the table's type)."""
+    tptr, ld = _matrix(table, "table")
+    shape = tuple(ids.shape) + (table.shape[1],)
+    dev = _same_device(table, ids, out)
+    with _on(dev, stream) as on:
+        if out is None:
+            out = on.fresh(shape, table.dtype if out_dtype is None else out_dtype)
+        elif tuple(out.shape) != shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must have shape {shape}" + ("" if out_dtype is None else f" and type {out_dtype}"))
+        e = _tokens(ids, table.shape[0], table.shape[1], ld, _dtype_code(table), scale)
+        _check(load().muon_embedding(ctypes.byref(e), tptr, _flat(out), _dtype_code(out), table.shape[1], on.handle))
+    return out
+
+
+def embedding_backward_workspace_size(tokens: int, vocab: int, cols: int) -> int:
+    """Bytes of workspace that the embedding's gradient takes (muon_embedding_backward_workspace_size)."""
+    e = EmbeddingTokens(None, tokens, vocab, cols, cols, 4, 0, 1.0, 0)
+    need = ctypes.c_size_t(0)
+    _check(load().muon_embedding_backward_workspace_size(ctypes.byref(e), ctypes.byref(need)))
+    return need.value
+
+
+def embedding_backward(dy, ids, vocab: int, scale: float = 1.0, out=None, out_dtype=None, accumulate: bool = False,
+                       ws=None, stream=None):
+    """Gradient of embedding's table (muon_embedding_backward): [vocab, cols], row v the sum
+    of dy's rows of the tokens v, times scale; every row is written, zeros where no token is.
+    dy: ids' shape + [cols] (rows contiguous), ids as in embedding. out: a matrix to write
+    into, such as a view of a gradient buffer, else a new one of out_dtype (float32). With
+    accumulate the sums are added to out and rows without a token are left alone."""
+    torch = _torch()
+    if dy.dim() != ids.dim() + 1 or tuple(dy.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dy must have the shape of ids and a dimension of columns")
+    cols = dy.shape[-1]
+    if dy.dim() == 2:
+        dyptr, lddy = _matrix(dy, "dy")
+    else:
+        dyptr, lddy = _flat(dy), cols
+    dev = _same_device(dy, ids, out, ws)
+    with _on(dev, stream) as on:
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs out")
+            out = on.fresh((vocab, cols), torch.float32 if out_dtype is None else out_dtype)
+        elif tuple(out.shape) != (vocab, cols) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must have shape {(vocab, cols)}" + ("" if out_dtype is None else f" and type {out_dtype}"))
+        optr, ld = _matrix(out, "out")
+        e = _tokens(ids, vocab, cols, ld, _dtype_code(out), scale)
+        ws = on.scratch(embedding_backward_workspace_size(ids.numel(), vocab, cols), ws)
+        _check(load().muon_embedding_backward(ctypes.byref(e), dyptr, _dtype_code(dy), lddy, optr, int(bool(accumulate)),
+                                              _flat(ws), 0 if ws is None else ws.numel() * ws.element_size(), on.handle))
+    return out
+
+
+_CLIP_CODES = None
+
+
+def _tensor_list(tensors, name):
+    """muon_tensor_t records of contiguous tensors on one GPU, as a c_int64 array of three per
+    tensor, their number, and the GPU's index."""
+    global _CLIP_CODES
+    if _CLIP_CODES is None:
+        torch = _torch()
+        _CLIP_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    codes, flat, dev = _CLIP_CODES, [], None
+    for t in tensors:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        d = t.get_device()
+        if d != dev:
+            if dev is not None or d < 0:
+                raise ValueError(f"{name} must share one GPU")
+            dev = d
+        if t.dtype not in codes:
+            raise TypeError(f"unsupported tensor dtype {t.dtype}")
+        flat += (t.data_ptr(), t.numel(), codes[t.dtype])
+    return (ctypes.c_int64 * max(len(flat), 1))(*flat), len(flat) // 3, dev
+
+
+def _sumsq(arr, n, sumsq, accumulate, ws, on):
+    need = ctypes.c_size_t(0)
+    _check(load().muon_grad_sumsq_workspace_size(arr, n, ctypes.byref(need)))
+    ws = on.scratch(need.value, ws)
+    _check(load().muon_grad_sumsq(arr, n, int(bool(accumulate)), _flat(sumsq), _flat(ws),
+                                  0 if ws is None else ws.numel() * ws.element_size(), on.handle))
+
+
+def grad_sumsq(grads: Sequence, out=None, accumulate: bool = False, ws=None, stream=None):
+    """Sum of the squares of all elements of the tensors (muon_grad_sumsq): float64, no
+    dimensions, in a fixed order. grads: contiguous tensors of one GPU, of any mix of
+    types. accumulate adds to out. Ranks with different shards add up their sums and pass the
+    total to clip_gradients."""
+    torch = _torch()
+    arr, n, index = _tensor_list(grads, "grads")
+    if n == 0:
+        raise ValueError("grad_sumsq needs at least one tensor")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    dev = _same_device(grads[0], out, ws)
+    with _on(dev, stream) as on:
+        out = _given(out, (), torch.float64, on, "out")
+        _sumsq(arr, n, out, accumulate, ws, on)
+    return out
+
+
+def clip_gradients(grads: Sequence, max_norm: float, sumsq=None, out: Optional[Sequence] = None, norm=None, ws=None,
+                   stream=None):
+    """Scale the tensors by min(1, max_norm / (norm + 1e-6)) of their global norm
+    (muon_grad_clip), in place or into `out`: as many tensors of the same sizes, of any
+    types, such as views of the packed gradient buffer. Returns the norm: float32, no
+    dimensions. sumsq: the float64 sum of squares to go by, where it is not that of these
+    tensors alone (other ranks' shards)."""
+    torch = _torch()
+    arr, n, index = _tensor_list(grads, "grads")
+    if n == 0:
+        raise ValueError("clip_gradients needs at least one tensor")
+    outs = arr
+    if out is not None:
+        outs, m, other = _tensor_list(out, "out")
+        if m != n:
+            raise ValueError(f"{m} outputs for {n} tensors")
+        if other != index:
+            raise ValueError("grads and out must share one GPU")
+    dev = _same_device(grads[0], sumsq, norm, ws)
+    with _on(dev, stream) as on:
+        if sumsq is None:
+            sumsq = on.fresh((), torch.float64)
+            _sumsq(arr, n, sumsq, False, ws, on)
+        else:
+            sumsq = _given(sumsq, (), torch.float64, on, "sumsq")
+        norm = _given(norm, (), torch.float32, on, "norm")
+        _check(load().muon_grad_clip(arr, outs, n, _flat(sumsq), max_norm, _flat(norm), on.handle))
+    return norm

@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuonstep.so")
 
 SOURCES = ["capi.hip", "capi_moe.hip", "plan.cpp", "planner.cpp", "gemm.hip", "elementwise.hip", "fp8.hip",
-           "fp8_gemm.hip", "moe.hip"]
+           "fp8_gemm.hip", "moe.hip", "capi_layer.hip", "norm.hip", "embedding.hip", "clip.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

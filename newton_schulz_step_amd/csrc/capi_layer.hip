@@ -1,0 +1,486 @@
+// C ABI of the norm, embedding and clipping operators: argument checks (all before the
+// first launch) and launch arguments.
+#include <math.h>
+
+#include <algorithm>
+#include <string>
+#include <vector>
+
+#include "capi_util.hpp"
+#include "fp8.hpp"
+#include "layer.hpp"
+#include "plan.hpp"
+
+namespace muon {
+
+// A strided input, whose rows may overlap.
+static int check_input(const char* name, const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
+  const std::string n(name);
+  const int esz = element_size(dtype);
+  if (esz == 0) return fail(MUON_ERR_UNSUPPORTED, n + ": dtype must be F32, BF16 or F16");
+  if (rows == 0 || cols == 0) return MUON_OK;
+  if (p == nullptr) return fail(MUON_ERR_NULL, n + " is NULL");
+  if (misaligned(p, esz)) return fail(MUON_ERR_ALIGN, n + " is not aligned to its element");
+  if (rows > 1 && (ld < 0 || ld > kMaxPitch)) return fail(MUON_ERR_BAD_SHAPE, n + ": row pitch outside [0, 2^28]");
+  return MUON_OK;
+}
+
+static Span matrix_span(const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, const char* name) {
+  return span_of(p, strided_bytes(dtype, 1, rows, cols, rows > 1 ? ld : cols, 0), name);
+}
+
+static int check_workspace(const void* ws, size_t bytes, size_t need, uintptr_t align) {
+  if (need > 0 && ws == nullptr) return fail(MUON_ERR_NULL, "workspace is NULL");
+  if (bytes < need) return fail(MUON_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+  if (need > 0 && misaligned(ws, align)) return fail(MUON_ERR_ALIGN, "workspace is not " + std::to_string(align) + "-byte aligned");
+  return MUON_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Norm
+
+static int check_norm_size(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > 0x7fffffffLL) return fail(MUON_ERR_BAD_SHAPE, "rows must lie in [0, 2^31)");
+  if (cols < 1 || cols > MUON_NORM_MAX_COLS) return fail(MUON_ERR_BAD_SHAPE, "cols must lie in [1, MUON_NORM_MAX_COLS]");
+  return MUON_OK;
+}
+
+// What both directions share; the inputs' spans go to `ins`.
+static int norm_common(const muon_norm_t* n, NormArgs& a, std::vector<Span>& ins) {
+  int st;
+  if (n == nullptr) return fail(MUON_ERR_NULL, "the rows' description is NULL");
+  if ((st = check_norm_size(n->rows, n->cols)) != MUON_OK) return st;
+  if (!(n->eps >= 0.0f) || !std::isfinite(n->eps)) return fail(MUON_ERR_BAD_HYPER, "eps must be finite and not negative");
+  if ((st = check_input("x", n->x, n->dtype, n->rows, n->cols, n->ld_x)) != MUON_OK) return st;
+  ins.push_back(matrix_span(n->x, n->dtype, n->rows, n->cols, n->ld_x, "x"));
+  if (n->residual != nullptr) {
+    if ((st = check_input("residual", n->residual, n->dtype, n->rows, n->cols, n->ld_residual)) != MUON_OK) return st;
+    ins.push_back(matrix_span(n->residual, n->dtype, n->rows, n->cols, n->ld_residual, "residual"));
+  }
+  if (n->weight != nullptr) {
+    if ((st = check_input("weight", n->weight, n->weight_dtype, 1, n->cols, n->cols)) != MUON_OK) return st;
+    ins.push_back(matrix_span(n->weight, n->weight_dtype, 1, n->cols, n->cols, "weight"));
+  }
+  a.x = n->x;
+  a.ld_x = n->ld_x;
+  a.residual = n->residual;
+  a.ld_residual = n->ld_residual;
+  a.weight = n->weight;
+  a.weight_dtype = n->weight_dtype;
+  a.rows = n->rows;
+  a.cols = n->cols;
+  a.eps = n->eps;
+  return MUON_OK;
+}
+
+static size_t norm_workspace(int64_t rows, int64_t cols) {
+  return static_cast<size_t>(norm_blocks(rows, cols)) * static_cast<size_t>(cols) * sizeof(float);
+}
+
+// ---------------------------------------------------------------------------
+// Embedding
+
+static int check_embedding(const muon_embedding_t* e) {
+  if (e == nullptr) return fail(MUON_ERR_NULL, "the tokens' description is NULL");
+  if (e->tokens < 0 || e->tokens > 0x7fffffffLL) return fail(MUON_ERR_BAD_SHAPE, "tokens must lie in [0, 2^31)");
+  if (e->vocab < 1 || e->vocab > MUON_EMBEDDING_MAX_VOCAB)
+    return fail(MUON_ERR_BAD_SHAPE, "vocab must lie in [1, MUON_EMBEDDING_MAX_VOCAB]");
+  if (e->cols < 0 || e->cols > MUON_FP8_MAX_SIDE) return fail(MUON_ERR_BAD_SHAPE, "cols must lie in [0, MUON_FP8_MAX_SIDE]");
+  if (e->id_bytes != 4 && e->id_bytes != 8) return fail(MUON_ERR_UNSUPPORTED, "ids must have 4 or 8 bytes");
+  if (element_size(e->table_dtype) == 0) return fail(MUON_ERR_UNSUPPORTED, "table: dtype must be F32, BF16 or F16");
+  if (!std::isfinite(e->scale)) return fail(MUON_ERR_BAD_HYPER, "scale is not finite");
+  return MUON_OK;
+}
+
+static int check_ids(const muon_embedding_t* e) {
+  if (e->tokens > 0 && e->ids == nullptr) return fail(MUON_ERR_NULL, "ids is NULL");
+  if (misaligned(e->ids, e->id_bytes)) return fail(MUON_ERR_ALIGN, "ids is not aligned to its element");
+  return MUON_OK;
+}
+
+static EmbeddingArgs embedding_args(const muon_embedding_t* e) {
+  EmbeddingArgs a{};
+  a.ids = e->ids;
+  a.wide_ids = e->id_bytes == 8;
+  a.tokens = e->tokens;
+  a.vocab = e->vocab;
+  a.cols = e->cols;
+  a.scale = e->scale;
+  a.table_dtype = e->table_dtype;
+  a.ld_table = e->ld;
+  int bits = 0;   // of the keys 0 .. vocab, the last of them for ids that are no rows
+  while (bits < 31 && (e->vocab >> bits) != 0) ++bits;
+  a.passes = (bits + 7) / 8;
+  a.bits = (bits + a.passes - 1) / a.passes;
+  a.blocks = sort_blocks(e->tokens);
+  a.per_block = (e->tokens + a.blocks - 1) / a.blocks;
+  return a;
+}
+
+// Lays the workspace out from `base`; returns its size.
+static size_t embedding_workspace(EmbeddingArgs& a, char* base) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base == nullptr ? nullptr : base + at;
+    at += (bytes + 15) / 16 * 16;
+    return p;
+  };
+  const size_t list = static_cast<size_t>(a.tokens) * 4;
+  for (int i = 0; i < 2; ++i) {
+    a.keys[i] = reinterpret_cast<int32_t*>(take(list));
+    a.slots[i] = reinterpret_cast<int32_t*>(take(list));
+  }
+  a.hist = reinterpret_cast<int32_t*>(take(a.blocks > 1 ? static_cast<size_t>(a.blocks) * kSortBins * 4 : 0));
+  a.touched = reinterpret_cast<uint8_t*>(take(static_cast<size_t>(a.vocab)));
+  const size_t chunks = static_cast<size_t>((a.tokens + kEmbeddingChunk - 1) / kEmbeddingChunk);
+  a.partial = reinterpret_cast<float*>(take(2 * chunks * static_cast<size_t>(a.cols) * 4));
+  return at;
+}
+
+// ---------------------------------------------------------------------------
+// Clipping
+
+// Elements of a workgroup: as many as leave 2048 workgroups or more, 8192 to 65536.
+static int32_t clip_chunk(int64_t elements) {
+  int32_t chunk = 65536;
+  while (chunk > 8192 && elements / chunk < 2048) chunk /= 2;
+  return chunk;
+}
+
+static int check_tensors(const muon_tensor_t* t, int32_t n, const char* name, int64_t& elements) {
+  const std::string s(name);
+  if (n < 0 || n > MUON_CLIP_MAX_TENSORS) return fail(MUON_ERR_BAD_SHAPE, "n must lie in [0, MUON_CLIP_MAX_TENSORS]");
+  if (n > 0 && t == nullptr) return fail(MUON_ERR_NULL, s + " is NULL");
+  elements = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const int esz = element_size(t[i].dtype);
+    if (esz == 0) return fail(MUON_ERR_UNSUPPORTED, s + "[" + std::to_string(i) + "]: dtype must be F32, BF16 or F16");
+    if (t[i].numel < 0 || t[i].numel > MUON_MAX_TABLE_ELEMENTS || (elements += t[i].numel) > MUON_MAX_TABLE_ELEMENTS)
+      return fail(MUON_ERR_BAD_SHAPE, s + ": more than MUON_MAX_TABLE_ELEMENTS elements, or a negative number");
+    if (t[i].numel == 0) continue;
+    if (t[i].data == nullptr) return fail(MUON_ERR_NULL, s + "[" + std::to_string(i) + "] is NULL");
+    if (misaligned(t[i].data, esz))
+      return fail(MUON_ERR_ALIGN, s + "[" + std::to_string(i) + "] is not aligned to its element");
+  }
+  return MUON_OK;
+}
+
+static int64_t clip_blocks(const muon_tensor_t* t, int32_t n, int32_t chunk) {
+  int64_t b = 0;
+  for (int32_t i = 0; i < n; ++i) b += (t[i].numel + chunk - 1) / chunk;
+  return b;
+}
+
+// Calls f with the arguments of one launch after the other: up to kClipTensors tensors each.
+template <typename F>
+static int each_clip_launch(const muon_tensor_t* in, const muon_tensor_t* out, int32_t n, int32_t chunk, F&& f) {
+  ClipArgs a{};
+  a.chunk = chunk;
+  int64_t before = 0;   // workgroups of earlier launches
+  for (int32_t i = 0; i < n;) {
+    int64_t blocks = 0;
+    a.n = 0;
+    for (; i < n && a.n < kClipTensors; ++i) {
+      if (in[i].numel == 0) continue;
+      ClipTensor& t = a.t[a.n++];
+      t.in = in[i].data;
+      t.out = out[i].data;
+      t.n = in[i].numel;
+      t.first = static_cast<int32_t>(blocks);
+      t.in_dtype = static_cast<int16_t>(in[i].dtype);
+      t.out_dtype = static_cast<int16_t>(out[i].dtype);
+      blocks += (in[i].numel + chunk - 1) / chunk;
+    }
+    a.blocks = static_cast<int32_t>(blocks);   // at most 2^36 / 8192 and one per tensor
+    if (a.n == 0) continue;
+    const int st = f(a, before);
+    if (st != MUON_OK) return st;
+    before += blocks;
+  }
+  return MUON_OK;
+}
+
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+int muon_rms_norm(const muon_norm_t* n, void* sum, int64_t ld_sum, void* y, int64_t ld_y, const muon_fp8_t* q,
+                  float* rstd, void* stream) {
+  return guarded([&]() -> int {
+    NormArgs a{};
+    std::vector<Span> ins, outs;
+    int st = norm_common(n, a, ins);
+    if (st != MUON_OK) return st;
+    if (sum == nullptr && y == nullptr && q == nullptr && rstd == nullptr) return fail(MUON_ERR_NULL, "no output is wanted");
+    const int64_t R = n->rows, C = n->cols;
+    if (sum != nullptr) {
+      if ((st = check_strided("sum", sum, n->dtype, 1, R, C, ld_sum, 0)) != MUON_OK) return st;
+      outs.push_back(matrix_span(sum, n->dtype, R, C, ld_sum, "sum"));
+    }
+    if (y != nullptr) {
+      if ((st = check_strided("y", y, n->dtype, 1, R, C, ld_y, 0)) != MUON_OK) return st;
+      outs.push_back(matrix_span(y, n->dtype, R, C, ld_y, "y"));
+    }
+    if (q != nullptr) {
+      if ((st = check_operand(q, "q")) != MUON_OK) return st;
+      if (q->batch != 1 || q->rows != R || q->cols != C) return fail(MUON_ERR_BAD_SHAPE, "q must be rows x cols, batch 1");
+      outs.push_back(span_of(q->data, data_bytes(*q), "q data"));
+      outs.push_back(span_of(q->scale, scale_bytes(*q), "q scale"));
+      a.q = q->data;
+      a.s = q->scale;
+      a.qp = fp8_data_pitch(C);
+      a.qs = fp8_scale_pitch(C);
+      a.format = q->format;
+    }
+    if (rstd != nullptr) {
+      if (misaligned(rstd, 4)) return fail(MUON_ERR_ALIGN, "rstd is not 4-byte aligned");
+      outs.push_back(span_of(rstd, R * 4, "rstd"));
+    }
+    if (R == 0) return MUON_OK;
+    if ((st = check_outputs(outs, ins)) != MUON_OK) return st;
+    a.sum = sum;
+    a.ld_sum = ld_sum;
+    a.y = y;
+    a.ld_y = ld_y;
+    a.rstd = rstd;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    MUON_LAUNCH("rms_norm", s, launch_rms_norm(n->dtype, a, s));
+    return MUON_OK;
+  });
+}
+
+int muon_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (bytes_out == nullptr) return fail(MUON_ERR_NULL, "bytes_out is NULL");
+    const int st = check_norm_size(rows, cols);
+    if (st != MUON_OK) return st;
+    *bytes_out = norm_workspace(rows, cols);
+    return MUON_OK;
+  });
+}
+
+int muon_rms_norm_backward(const muon_norm_t* n, const float* rstd, const void* dy, int64_t ld_dy, const void* dsum,
+                           int64_t ld_dsum, void* dx, int64_t ld_dx, void* dweight, int32_t dweight_dtype,
+                           int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    NormArgs a{};
+    std::vector<Span> ins, outs;
+    int st = norm_common(n, a, ins);
+    if (st != MUON_OK) return st;
+    if (n->residual != nullptr) return fail(MUON_ERR_UNSUPPORTED, "the gradient takes the rows that were normed, without a residual");
+    if (dx == nullptr && dweight == nullptr) return fail(MUON_ERR_NULL, "dx and dweight are both NULL");
+    const int64_t R = n->rows, C = n->cols;
+    if (R > 0 && rstd == nullptr) return fail(MUON_ERR_NULL, "rstd is NULL");
+    if (misaligned(rstd, 4)) return fail(MUON_ERR_ALIGN, "rstd is not 4-byte aligned");
+    if ((st = check_input("dy", dy, n->dtype, R, C, ld_dy)) != MUON_OK) return st;
+    ins.push_back(span_of(rstd, R * 4, "rstd"));
+    ins.push_back(matrix_span(dy, n->dtype, R, C, ld_dy, "dy"));
+    if (dsum != nullptr) {
+      if ((st = check_input("dsum", dsum, n->dtype, R, C, ld_dsum)) != MUON_OK) return st;
+      ins.push_back(matrix_span(dsum, n->dtype, R, C, ld_dsum, "dsum"));
+    }
+    if (dx != nullptr) {
+      if ((st = check_strided("dx", dx, n->dtype, 1, R, C, ld_dx, 0)) != MUON_OK) return st;
+      outs.push_back(matrix_span(dx, n->dtype, R, C, ld_dx, "dx"));
+    }
+    if (dweight != nullptr) {
+      if ((st = check_strided("dweight", dweight, dweight_dtype, 1, 1, C, C, 0)) != MUON_OK) return st;
+      outs.push_back(matrix_span(dweight, dweight_dtype, 1, C, C, "dweight"));
+      const size_t need = norm_workspace(R, C);
+      if ((st = check_workspace(workspace, workspace_bytes, need, 4)) != MUON_OK) return st;
+      outs.push_back(span_of(workspace, static_cast<int64_t>(need), "workspace"));
+      a.partial = static_cast<float*>(workspace);
+    }
+    if ((st = check_outputs(outs, ins)) != MUON_OK) return st;
+    a.rstd_in = rstd;
+    a.dy = dy;
+    a.ld_dy = ld_dy;
+    a.dsum = dsum;
+    a.ld_dsum = ld_dsum;
+    a.dx = dx;
+    a.ld_dx = ld_dx;
+    a.dweight = dweight;
+    a.dweight_dtype = dweight_dtype;
+    a.accumulate = accumulate != 0;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    // without rows the weight's gradient is still zero
+    if (R > 0 || dweight != nullptr) MUON_LAUNCH("rms_norm_backward", s, launch_rms_norm_backward(n->dtype, a, s));
+    if (dweight != nullptr) MUON_LAUNCH("norm_weight", s, launch_norm_weight(a, s));
+    return MUON_OK;
+  });
+}
+
+int muon_embedding(const muon_embedding_t* e, const void* table, void* y, int32_t dtype, int64_t ld_y, void* stream) {
+  return guarded([&]() -> int {
+    int st = check_embedding(e);
+    if (st != MUON_OK) return st;
+    if ((st = check_ids(e)) != MUON_OK) return st;
+    if ((st = check_input("table", table, e->table_dtype, e->vocab, e->cols, e->ld)) != MUON_OK) return st;
+    if ((st = check_strided("y", y, dtype, 1, e->tokens, e->cols, ld_y, 0)) != MUON_OK) return st;
+    if (e->tokens == 0 || e->cols == 0) return MUON_OK;
+    if ((st = check_outputs({matrix_span(y, dtype, e->tokens, e->cols, ld_y, "y")},
+                            {matrix_span(table, e->table_dtype, e->vocab, e->cols, e->ld, "table"),
+                             span_of(e->ids, e->tokens * e->id_bytes, "ids")})) != MUON_OK)
+      return st;
+    if (e->tokens * ((e->cols + 2047) / 2048) > 0x7fffffffLL)
+      return fail(MUON_ERR_BAD_SHAPE, "too many tokens and columns for a launch");
+    EmbeddingArgs a = embedding_args(e);
+    a.table = table;
+    a.y = y;
+    a.ld_y = ld_y;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    MUON_LAUNCH("embedding", s, launch_embedding(dtype, a, s));
+    return MUON_OK;
+  });
+}
+
+int muon_embedding_backward_workspace_size(const muon_embedding_t* e, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (bytes_out == nullptr) return fail(MUON_ERR_NULL, "bytes_out is NULL");
+    const int st = check_embedding(e);
+    if (st != MUON_OK) return st;
+    EmbeddingArgs a = embedding_args(e);
+    *bytes_out = embedding_workspace(a, nullptr);
+    return MUON_OK;
+  });
+}
+
+int muon_embedding_backward(const muon_embedding_t* e, const void* dy, int32_t dtype, int64_t ld_dy, void* dtable,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int st = check_embedding(e);
+    if (st != MUON_OK) return st;
+    if ((st = check_ids(e)) != MUON_OK) return st;
+    if ((st = check_input("dy", dy, dtype, e->tokens, e->cols, ld_dy)) != MUON_OK) return st;
+    if ((st = check_strided("dtable", dtable, e->table_dtype, 1, e->vocab, e->cols, e->ld, 0)) != MUON_OK) return st;
+    EmbeddingArgs a = embedding_args(e);
+    const size_t need = embedding_workspace(a, nullptr);
+    if ((st = check_workspace(workspace, workspace_bytes, need, 16)) != MUON_OK) return st;
+    if (e->cols == 0 || (e->tokens == 0 && accumulate)) return MUON_OK;
+    if ((st = check_outputs({matrix_span(dtable, e->table_dtype, e->vocab, e->cols, e->ld, "dtable"),
+                             span_of(workspace, static_cast<int64_t>(need), "workspace")},
+                            {matrix_span(dy, dtype, e->tokens, e->cols, ld_dy, "dy"),
+                             span_of(e->ids, e->tokens * e->id_bytes, "ids")})) != MUON_OK)
+      return st;
+    const int64_t chunks = (e->tokens + kEmbeddingChunk - 1) / kEmbeddingChunk;
+    if (chunks * ((e->cols + 511) / 512) + e->vocab > 0x7fffffffLL)
+      return fail(MUON_ERR_BAD_SHAPE, "too many tokens and columns for a launch");
+    embedding_workspace(a, static_cast<char*>(workspace));
+    if (accumulate) a.touched = nullptr;
+    a.accumulate = accumulate != 0;
+    a.dy = dy;
+    a.ld_y = ld_dy;
+    a.dtable = dtable;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (a.blocks == 1) {
+      MUON_LAUNCH("sort_all", s, launch_sort_all(a, s));
+    } else {
+      for (int p = 0; p < a.passes; ++p) {
+        MUON_LAUNCH("sort_hist", s, launch_sort_hist(a, p, s));
+        MUON_LAUNCH("sort_place", s, launch_sort_place(a, p, s));
+      }
+    }
+    MUON_LAUNCH("embedding_sum", s, launch_embedding_sum(dtype, a, s));
+    MUON_LAUNCH("embedding_join", s, launch_embedding_join(a, s));
+    return MUON_OK;
+  });
+}
+
+int muon_grad_sumsq_workspace_size(const muon_tensor_t* grads, int32_t n, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (bytes_out == nullptr) return fail(MUON_ERR_NULL, "bytes_out is NULL");
+    int64_t elements;
+    const int st = check_tensors(grads, n, "grads", elements);
+    if (st != MUON_OK) return st;
+    *bytes_out = static_cast<size_t>(clip_blocks(grads, n, clip_chunk(elements))) * sizeof(double);
+    return MUON_OK;
+  });
+}
+
+int muon_grad_sumsq(const muon_tensor_t* grads, int32_t n, int32_t accumulate, double* sumsq, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int64_t elements;
+    int st = check_tensors(grads, n, "grads", elements);
+    if (st != MUON_OK) return st;
+    if (sumsq == nullptr) return fail(MUON_ERR_NULL, "sumsq is NULL");
+    if (misaligned(sumsq, 8)) return fail(MUON_ERR_ALIGN, "sumsq is not 8-byte aligned");
+    const int32_t chunk = clip_chunk(elements);
+    const int64_t blocks = clip_blocks(grads, n, chunk);
+    const size_t need = static_cast<size_t>(blocks) * sizeof(double);
+    if ((st = check_workspace(workspace, workspace_bytes, need, 8)) != MUON_OK) return st;
+    std::vector<Span> ins;
+    for (int32_t i = 0; i < n; ++i) ins.push_back(span_of(grads[i].data, grads[i].numel * element_size(grads[i].dtype), "a gradient"));
+    if ((st = check_outputs({span_of(sumsq, 8, "sumsq"), span_of(workspace, static_cast<int64_t>(need), "workspace")}, ins)) != MUON_OK)
+      return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = each_clip_launch(grads, grads, n, chunk, [&](ClipArgs& a, int64_t before) -> int {
+      a.partial = static_cast<double*>(workspace) + before;
+      MUON_LAUNCH("grad_sumsq", s, launch_grad_sumsq(a, s));
+      return MUON_OK;
+    });
+    if (st != MUON_OK) return st;
+    MUON_LAUNCH("sum_partials", s, launch_sum_partials(static_cast<const double*>(workspace), blocks, accumulate != 0, sumsq, s));
+    return MUON_OK;
+  });
+}
+
+int muon_grad_clip(const muon_tensor_t* grads, const muon_tensor_t* outs, int32_t n, const double* sumsq,
+                   float max_norm, float* norm, void* stream) {
+  return guarded([&]() -> int {
+    int64_t elements, other;
+    int st = check_tensors(grads, n, "grads", elements);
+    if (st != MUON_OK) return st;
+    if (outs == nullptr) outs = grads;
+    if (outs != grads && (st = check_tensors(outs, n, "outs", other)) != MUON_OK) return st;
+    if (!(max_norm >= 0.0f)) return fail(MUON_ERR_BAD_HYPER, "max_norm must not be negative or NaN");
+    if (sumsq == nullptr) return fail(MUON_ERR_NULL, "sumsq is NULL");
+    if (misaligned(sumsq, 8) || misaligned(norm, 4)) return fail(MUON_ERR_ALIGN, "sumsq or norm is not aligned to its element");
+    // outputs may be their own inputs and nothing else: sorted by address, nobody begins
+    // before an output in front of it ends, and no output before anybody in front of it does
+    struct Part {
+      const char *lo, *hi;
+      bool out;
+    };
+    std::vector<Part> parts;
+    parts.reserve(2 * static_cast<size_t>(n) + 2);
+    auto add = [&](const void* p, int64_t bytes, bool out) {
+      if (bytes > 0) parts.push_back({static_cast<const char*>(p), static_cast<const char*>(p) + bytes, out});
+    };
+    for (int32_t i = 0; i < n; ++i) {
+      if (outs[i].numel != grads[i].numel) return fail(MUON_ERR_BAD_SHAPE, "outs[" + std::to_string(i) + "] has another number of elements");
+      add(outs[i].data, outs[i].numel * element_size(outs[i].dtype), true);
+      if (outs[i].data != grads[i].data || outs[i].dtype != grads[i].dtype)
+        add(grads[i].data, grads[i].numel * element_size(grads[i].dtype), false);
+    }
+    add(sumsq, 8, false);
+    if (norm != nullptr) add(norm, 4, true);
+    std::sort(parts.begin(), parts.end(), [](const Part& x, const Part& y) { return x.lo < y.lo; });
+    const char *end = nullptr, *end_out = nullptr;
+    for (const Part& p : parts) {
+      if (p.lo < (p.out ? end : end_out)) return fail(MUON_ERR_OVERLAP, "an output overlaps another buffer");
+      end = std::max(end, p.hi);
+      if (p.out) end_out = std::max(end_out, p.hi);
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    bool told = false;   // the first launch writes the norm
+    auto launch = [&](ClipArgs& a, int64_t) -> int {
+      a.sumsq = sumsq;
+      a.max_norm = max_norm;
+      a.norm = told ? nullptr : norm;
+      MUON_LAUNCH("grad_clip", s, launch_grad_clip(a, s));
+      told = true;
+      return MUON_OK;
+    };
+    if ((st = each_clip_launch(grads, outs, n, clip_chunk(elements), launch)) != MUON_OK) return st;
+    if (!told && norm != nullptr) {   // no elements at all
+      ClipArgs a{};
+      return launch(a, 0);
+    }
+    return MUON_OK;
+  });
+}
+
+}  // extern "C"

@@ -2,15 +2,9 @@
 // experts' outputs (gfx950).
 #include "common.hpp"
 #include "fp8.hpp"
+#include "rows.hpp"
 
 namespace muon {
-
-template <int DT> __device__ __forceinline__ float load1(const void* p, int64_t i) { return grad_to_f32<DT>(p, i); }
-template <int DT> __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-  if constexpr (DT == MUON_DTYPE_F32) static_cast<float*>(p)[i] = v;
-  else if constexpr (DT == MUON_DTYPE_BF16) static_cast<__bf16*>(p)[i] = static_cast<__bf16>(v);
-  else static_cast<_Float16*>(p)[i] = static_cast<_Float16>(v);
-}
 
 // ---------------------------------------------------------------------------
 // Reductions over a team of 64 or 32 neighbouring lanes with row shifts and broadcasts (no
@@ -549,51 +543,6 @@ hipError_t launch_order_place(const OrderArgs& a, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // Combination: one workgroup per token, eight columns per thread and pass, 16 bytes at any
 // element-aligned place.
-
-typedef u16x8 u16x8_any __attribute__((aligned(2)));
-typedef f32x4 f32x4_any __attribute__((aligned(4)));
-
-template <int DT>
-__device__ __forceinline__ void read8(const void* p, int64_t i, int n, float (&v)[8]) {
-  if (n == 8) {
-    if constexpr (DT == MUON_DTYPE_F32) {
-      const f32x4_any* q = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i);
-      const f32x4 a = q[0], b = q[1];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
-    } else {
-      const u16x8 u = *reinterpret_cast<const u16x8_any*>(static_cast<const unsigned short*>(p) + i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = DT == MUON_DTYPE_BF16 ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = e < n ? load1<DT>(p, i + e) : 0.0f;
-}
-
-template <int DT>
-__device__ __forceinline__ void write8(void* p, int64_t i, int n, const float (&v)[8]) {
-  if (n == 8) {
-    if constexpr (DT == MUON_DTYPE_F32) {
-      f32x4_any* q = reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + i);
-      q[0] = f32x4{v[0], v[1], v[2], v[3]};
-      q[1] = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-      using T = std::conditional_t<DT == MUON_DTYPE_BF16, __bf16, _Float16>;
-      T o[8];
-      rne<T, 8>(v, o);
-      u16x8 u;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = __builtin_bit_cast(unsigned short, o[e]);
-      *reinterpret_cast<u16x8_any*>(static_cast<unsigned short*>(p) + i) = u;
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < n) store1<DT>(p, i + e, v[e]);
-}
 
 // Bound by memory: every row of o once. Four rows at a time are in flight. 8192 tokens of 6
 // rows of 2048 bf16: 49 us (4.8 TB/s, a large copy reaches 5.1).

@@ -1,0 +1,283 @@
+// RMS norm of rows with the residual's addition and an output in 8 bits, and its gradient
+// (gfx950).
+//
+//   s = x + r, rounded to the rows' type;   rstd = (mean(s^2) + eps)^(-1/2);   y = s rstd w
+// With n = s rstd and g = dy w the gradient is
+//   dx = rstd (g - n mean(g n)) + ds,   dw = sum over rows of dy n.
+// Sums are in fp32, in a fixed order. Bound by memory: every row is read once into registers,
+// a team of 1, 4 or 8 waves per row, eight columns per lane and load.
+#include "fp8.hpp"
+#include "layer.hpp"
+#include "quant8.hpp"
+#include "rows.hpp"
+
+namespace muon {
+
+__device__ __forceinline__ void read8_as(int dtype, const void* p, int64_t i, int n, float (&v)[8]) {
+  if (dtype == MUON_DTYPE_F32) read8<MUON_DTYPE_F32>(p, i, n, v);
+  else if (dtype == MUON_DTYPE_BF16) read8<MUON_DTYPE_BF16>(p, i, n, v);
+  else read8<MUON_DTYPE_F16>(p, i, n, v);
+}
+
+// v rounded to the type DT and back.
+template <int DT>
+__device__ __forceinline__ void round8(float (&v)[8]) {
+  if constexpr (DT != MUON_DTYPE_F32) {
+    using T = std::conditional_t<DT == MUON_DTYPE_BF16, __bf16, _Float16>;
+    T o[8];
+    rne<T, 8>(v, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(o[e]);
+  }
+}
+
+// The sum over a team's lanes, in all of them. `scratch`: a float per wave of the workgroup.
+template <int WAVES>
+__device__ __forceinline__ float team_sum(float v, float* scratch) {
+  v = wave_sum(v);
+  if constexpr (WAVES > 1) {
+    if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += scratch[w];
+    __syncthreads();
+  }
+  return v;
+}
+
+template <int WAVES> constexpr int kNormRows = WAVES < 4 ? 4 / WAVES : 1;   // rows of a workgroup
+template <int WAVES> constexpr int kNormThreads = kNormRows<WAVES> * WAVES * 64;
+
+template <int XT, int WAVES, int V>
+__global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_kernel(NormArgs a) {
+  constexpr int TEAM = WAVES * 64;
+  __shared__ float scratch[WAVES];
+  const int64_t row = static_cast<int64_t>(flat_block()) * kNormRows<WAVES> + threadIdx.x / TEAM;
+  if (row >= a.rows) return;   // whole teams; with several waves per row, whole workgroups
+  const int lane = threadIdx.x % TEAM;
+
+  Raw8<XT> x[V], r[V];
+  float w[V][8], v[V][8];
+  int n[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t c = (static_cast<int64_t>(i) * TEAM + lane) * 8;
+    n[i] = static_cast<int>(max<int64_t>(0, min<int64_t>(8, a.cols - c)));
+    x[i].load(a.x, n[i] > 0 ? row * a.ld_x + c : 0, n[i]);
+    if (a.residual != nullptr) r[i].load(a.residual, n[i] > 0 ? row * a.ld_residual + c : 0, n[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (a.weight != nullptr) {
+      read8_as(a.weight_dtype, a.weight, (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], w[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[i][e] = 1.0f;
+    }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = x[i].get(e);
+    if (a.residual != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += r[i].get(e);
+      round8<XT>(v[i]);
+    }
+    if (a.sum != nullptr) write8<XT>(a.sum, row * a.ld_sum + (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], v[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += v[i][e] * v[i][e];
+  }
+  const float rstd = 1.0f / sqrtf(team_sum<WAVES>(sum, scratch) / static_cast<float>(a.cols) + a.eps);
+  if (a.rstd != nullptr && lane == 0) a.rstd[row] = rstd;
+
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t chunk = static_cast<int64_t>(i) * TEAM + lane;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = e < n[i] ? v[i][e] * rstd * w[i][e] : 0.0f;
+    round8<XT>(v[i]);
+    if (a.y != nullptr) write8<XT>(a.y, row * a.ld_y + chunk * 8, n[i], v[i]);
+    if (a.q != nullptr) {
+      // 16 neighbouring lanes hold a block of 128; what is behind the last column is zeros
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(v[i][e]));
+      m = row_max(m);
+      const bool e4m3 = a.format == MUON_FP8_E4M3;
+      const int byte = e4m3 ? scale_byte<MUON_FP8_E4M3>(m) : scale_byte<MUON_FP8_E5M2>(m);
+      if (chunk * 8 < a.qp) {
+        const float inv = inverse_scale(byte);
+        *reinterpret_cast<u32x2*>(a.q + row * a.qp + chunk * 8) =
+            e4m3 ? pack8<MUON_FP8_E4M3>(v[i], inv) : pack8<MUON_FP8_E5M2>(v[i], inv);
+        const int64_t block = chunk >> 4, of = chunk & 15;
+        if (of == 0) a.s[row * a.qs + block] = static_cast<uint8_t>(byte);
+        if ((block + 1) * MUON_FP8_BLOCK == a.qp && of > 0 && block + of < a.qs) a.s[row * a.qs + block + of] = 127;
+      }
+    }
+  }
+}
+
+// Workgroups walk over rows, so that a lane's columns of the weight gradient are summed in
+// registers; what is left is a row of partial sums per workgroup, joined by norm_weight_kernel.
+template <int XT, int WAVES, int V>
+__global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_backward_kernel(NormArgs a) {
+  constexpr int TEAM = WAVES * 64, ROWS = kNormRows<WAVES>;
+  __shared__ float scratch[WAVES];
+  __shared__ float joined[ROWS > 1 ? TEAM * V * 8 : 1];
+  const int team = threadIdx.x / TEAM, lane = threadIdx.x % TEAM;
+  int n[V];
+  float w[V][8], acc[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t c = (static_cast<int64_t>(i) * TEAM + lane) * 8;
+    n[i] = static_cast<int>(max<int64_t>(0, min<int64_t>(8, a.cols - c)));
+    if (a.weight != nullptr) {
+      read8_as(a.weight_dtype, a.weight, c, n[i], w[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[i][e] = 1.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+  }
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + team; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * ROWS) {
+    Raw8<XT> dy[V], s[V], ds[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int64_t c = (static_cast<int64_t>(i) * TEAM + lane) * 8;
+      dy[i].load(a.dy, n[i] > 0 ? row * a.ld_dy + c : 0, n[i]);
+      s[i].load(a.x, n[i] > 0 ? row * a.ld_x + c : 0, n[i]);
+      if (a.dsum != nullptr) ds[i].load(a.dsum, n[i] > 0 ? row * a.ld_dsum + c : 0, n[i]);
+    }
+    const float rstd = a.rstd_in[row];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float gn = dy[i].get(e) * (s[i].get(e) * rstd);
+        acc[i][e] += gn;
+        dot += gn * w[i][e];
+      }
+    const float mean = team_sum<WAVES>(dot, scratch) * inv;
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = rstd * (dy[i].get(e) * w[i][e] - s[i].get(e) * rstd * mean);
+        if (a.dsum != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] += ds[i].get(e);
+        }
+        write8<XT>(a.dx, row * a.ld_dx + (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], d);
+      }
+    }
+  }
+  if (a.partial == nullptr) return;
+  if constexpr (ROWS > 1) {   // the teams' sums, one after the other
+    for (int r = 0; r < ROWS; ++r) {
+      if (team == r) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float* at = joined + (i * 8 + e) * TEAM + lane;
+            if (r > 0) acc[i][e] += *at;
+            *at = acc[i][e];
+          }
+      }
+      __syncthreads();
+    }
+    if (team != ROWS - 1) return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    write8<MUON_DTYPE_F32>(a.partial, blockIdx.x * a.cols + (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], acc[i]);
+}
+
+// 64 columns per workgroup, its 16 waves share the partial rows.
+__global__ __launch_bounds__(1024) void norm_weight_kernel(NormArgs a, int32_t blocks) {
+  __shared__ float part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  float v = 0.0f;
+  if (c < a.cols) {
+#pragma unroll 8
+    for (int b = wave; b < blocks; b += 16) v += a.partial[b * a.cols + c];
+  }
+  part[wave][lane] = v;
+  __syncthreads();
+  if (wave != 0 || c >= a.cols) return;
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v += part[i][lane];
+  if (a.dweight_dtype == MUON_DTYPE_F32) {
+    store1<MUON_DTYPE_F32>(a.dweight, c, v + (a.accumulate ? load1<MUON_DTYPE_F32>(a.dweight, c) : 0.0f));
+  } else if (a.dweight_dtype == MUON_DTYPE_BF16) {
+    store1<MUON_DTYPE_BF16>(a.dweight, c, v + (a.accumulate ? load1<MUON_DTYPE_BF16>(a.dweight, c) : 0.0f));
+  } else {
+    store1<MUON_DTYPE_F16>(a.dweight, c, v + (a.accumulate ? load1<MUON_DTYPE_F16>(a.dweight, c) : 0.0f));
+  }
+}
+
+// The smallest team whose registers hold a row (of whole blocks of 128).
+template <int W, int V> struct Team {
+  static constexpr int waves = W, loads = V;
+};
+template <typename F>
+static hipError_t with_team(int64_t cols, F&& f) {
+  if (cols <= 512) return f(Team<1, 1>());
+  if (cols <= 1024) return f(Team<1, 2>());
+  if (cols <= 2048) return f(Team<1, 4>());
+  if (cols <= 4096) return f(Team<4, 2>());
+  if (cols <= 8192) return f(Team<4, 4>());
+  return f(Team<8, 4>());
+}
+
+template <int XT>
+static hipError_t launch_forward(const NormArgs& a, hipStream_t s) {
+  return with_team(a.cols, [&](auto team) {
+    constexpr int W = decltype(team)::waves, V = decltype(team)::loads;
+    hipLaunchKernelGGL((rms_norm_kernel<XT, W, V>), flat_grid((a.rows + kNormRows<W> - 1) / kNormRows<W>),
+                       dim3(kNormThreads<W>), 0, s, a);
+    return hipGetLastError();
+  });
+}
+hipError_t launch_rms_norm(int dtype, const NormArgs& a, hipStream_t s) {
+  if (dtype == MUON_DTYPE_F32) return launch_forward<MUON_DTYPE_F32>(a, s);
+  if (dtype == MUON_DTYPE_BF16) return launch_forward<MUON_DTYPE_BF16>(a, s);
+  return launch_forward<MUON_DTYPE_F16>(a, s);
+}
+
+int32_t norm_blocks(int64_t rows, int64_t cols) {
+  const int64_t per = cols <= 2048 ? 4 : 1;
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, 768)));
+}
+
+template <int XT>
+static hipError_t launch_backward(const NormArgs& a, hipStream_t s) {
+  return with_team(a.cols, [&](auto team) {
+    constexpr int W = decltype(team)::waves, V = decltype(team)::loads;
+    hipLaunchKernelGGL((rms_norm_backward_kernel<XT, W, V>), dim3(norm_blocks(a.rows, a.cols)), dim3(kNormThreads<W>), 0,
+                       s, a);
+    return hipGetLastError();
+  });
+}
+hipError_t launch_rms_norm_backward(int dtype, const NormArgs& a, hipStream_t s) {
+  if (dtype == MUON_DTYPE_F32) return launch_backward<MUON_DTYPE_F32>(a, s);
+  if (dtype == MUON_DTYPE_BF16) return launch_backward<MUON_DTYPE_BF16>(a, s);
+  return launch_backward<MUON_DTYPE_F16>(a, s);
+}
+hipError_t launch_norm_weight(const NormArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(norm_weight_kernel, dim3(static_cast<unsigned>((a.cols + 63) / 64)), dim3(1024), 0, s, a,
+                     norm_blocks(a.rows, a.cols));
+  return hipGetLastError();
+}
+
+}  // namespace muon
