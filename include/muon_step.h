@@ -685,6 +685,73 @@ int muon_grad_sumsq_workspace_size(const muon_tensor_t* grads, int32_t n, size_t
 int muon_grad_clip(const muon_tensor_t* grads, const muon_tensor_t* outs, int32_t n, const double* sumsq,
                    float max_norm, float* norm, void* stream);
 
+/* ---- Attention ------------------------------------------------------------ */
+
+/* Limits: tokens <= MUON_ATTENTION_MAX_TOKENS, heads <= MUON_ATTENTION_MAX_HEADS,
+ * head dimension a multiple of 8 up to MUON_ATTENTION_MAX_DIM. */
+#define MUON_ATTENTION_MAX_TOKENS (1 << 30)
+#define MUON_ATTENTION_MAX_HEADS 1024
+#define MUON_ATTENTION_MAX_DIM 128
+
+/* Heads of all tokens, 16-bit elements: element (token, head, column) at
+ * data + token * token_stride + head * head_stride + column (strides in
+ * elements, multiples of 8; token_stride dim .. 2^22). data: device, 16-byte
+ * aligned. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} muon_heads_t;
+
+/* Self-attention over packed sequences. Sequence s is the tokens
+ * [offsets[s], offsets[s + 1]) (device int32[sequences + 1], ascending; clamped
+ * to [0, tokens], and one that is less than an earlier one counts as the
+ * largest before it; a sequence may be empty). offsets NULL: all tokens are one
+ * sequence. Query head h looks at key head h / (heads / kv_heads).
+ * Token i of a sequence sees all of its tokens, with `causal` those j <= i, with
+ * window > 0 (causal only) those with i - j < window. */
+typedef struct {
+  int64_t tokens;
+  const int32_t* offsets;
+  int32_t sequences;      /* ignored without offsets */
+  int32_t heads;
+  int32_t kv_heads;       /* divides heads */
+  int32_t dim;
+  int32_t dtype;          /* BF16 | F16, of all operands */
+  int32_t causal;
+  int32_t window;
+  float scale;            /* > 0, of the scores */
+} muon_attention_t;
+
+/* o = softmax(scale * q k^T) v per sequence and head; scores, their softmax and
+ * all sums in fp32, the probabilities rounded to dtype for their product with v.
+ *   lse  device float32[heads x tokens] or NULL: the natural logarithm of each
+ *        row's sum of exponentials, for the gradient.
+ * Tokens outside every sequence are not read, and their rows of o and lse are not
+ * written. Values must be finite: one that is not can reach every row of its
+ * own sequence (never another sequence).
+ *   workspace  device, muon_attention_workspace_size(a, 0) bytes, 16-byte
+ *              aligned (NULL where that is 0: without offsets).
+ * Errors: MUON_ERR_NULL, BAD_SHAPE, UNSUPPORTED (dtype, a window without causal),
+ * ALIGN, OVERLAP, BAD_HYPER (scale), WORKSPACE. */
+int muon_attention(const muon_attention_t* a, const muon_heads_t* q, const muon_heads_t* k, const muon_heads_t* v,
+                   const muon_heads_t* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient, from the gradient d_o of o and the forward call's o and lse; the
+ * probabilities are computed again from q, k and lse. With
+ * P = exp(scale * q k^T - lse) and delta = rowsum(d_o o):
+ *   dv = P^T d_o,  dS = P (d_o v^T - delta),  dq = scale dS k,  dk = scale dS^T q,
+ * dk and dv summed over the query heads that share them. P and dS are rounded to
+ * dtype for their products (in F16 under powers of two that keep them in its
+ * range), all sums are in fp32 in an order that the sizes alone decide. dq, dk
+ * and dv may be interleaved, as the parts of one gradient of a joint projection
+ * are. Workspace: muon_attention_workspace_size(a, 1). */
+int muon_attention_backward(const muon_attention_t* a, const muon_heads_t* d_o, const muon_heads_t* q,
+                            const muon_heads_t* k, const muon_heads_t* v, const muon_heads_t* o, const float* lse,
+                            const muon_heads_t* dq, const muon_heads_t* dk, const muon_heads_t* dv, void* workspace,
+                            size_t workspace_bytes, void* stream);
+int muon_attention_workspace_size(const muon_attention_t* a, int32_t backward, size_t* bytes_out);
+
 /* Message for the last failing call on this thread ("" if none). Valid until the
  * next call on this thread. */
 const char* muon_last_error(void);

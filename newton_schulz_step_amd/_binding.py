@@ -42,6 +42,7 @@ EXPORTED = (
     "muon_rms_norm", "muon_rms_norm_backward", "muon_rms_norm_backward_workspace_size",
     "muon_embedding", "muon_embedding_backward", "muon_embedding_backward_workspace_size",
     "muon_grad_sumsq", "muon_grad_sumsq_workspace_size", "muon_grad_clip",
+    "muon_attention", "muon_attention_backward", "muon_attention_workspace_size",
 )
 NOALLOC_WORKSPACE_BYTES = 64 << 20     # MUON_NOALLOC_WORKSPACE_BYTES
 
@@ -138,6 +139,17 @@ class EmbeddingTokens(ctypes.Structure):
                 ("table_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class AttentionRows(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("sequences", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -207,7 +219,12 @@ def load() -> ctypes.CDLL:
         lib.muon_grad_sumsq.argtypes = [vp, i32, i32, vp, vp, sz, vp]   # the tensors as a c_int64 array
         lib.muon_grad_sumsq_workspace_size.argtypes = [vp, i32, psz]
         lib.muon_grad_clip.argtypes = [vp, vp, i32, vp, ctypes.c_float, vp, vp]
-        for name in ("muon_rms_norm", "muon_rms_norm_backward", "muon_rms_norm_backward_workspace_size",
+        pa, ph3 = ctypes.POINTER(AttentionRows), ctypes.POINTER(Heads)
+        lib.muon_attention.argtypes = [pa, ph3, ph3, ph3, ph3, vp, vp, sz, vp]
+        lib.muon_attention_backward.argtypes = [pa, ph3, ph3, ph3, ph3, ph3, vp, ph3, ph3, ph3, vp, sz, vp]
+        lib.muon_attention_workspace_size.argtypes = [pa, i32, psz]
+        for name in ("muon_attention", "muon_attention_backward", "muon_attention_workspace_size",
+                     "muon_rms_norm", "muon_rms_norm_backward", "muon_rms_norm_backward_workspace_size",
                      "muon_embedding", "muon_embedding_backward", "muon_embedding_backward_workspace_size",
                      "muon_grad_sumsq", "muon_grad_sumsq_workspace_size", "muon_grad_clip"):
             getattr(lib, name).restype = ctypes.c_int
@@ -1250,3 +1267,90 @@ def clip_gradients(grads: Sequence, max_norm: float, sumsq=None, out: Optional[S
         norm = _given(norm, (), torch.float32, on, "norm")
         _check(load().muon_grad_clip(arr, outs, n, _flat(sumsq), max_norm, _flat(norm), on.handle))
     return norm
+
+
+# ----------------------------------------------------------------------------- attention
+
+def _heads(t, name):
+    """muon_heads_t of a tensor [tokens, heads, dim] whose columns are contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim]")
+    tokens, heads, dim = t.shape
+    ts, hs, cs = t.stride()
+    if dim > 1 and cs != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if heads <= 1:
+        hs = dim
+    if tokens <= 1:
+        ts = max(dim, 8)
+    return Heads(t.data_ptr(), ts, hs)
+
+
+def _attention_rows(q, k, v, offsets, causal, window, scale):
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [tokens, heads, dim], k and v [tokens, kv_heads, dim]")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one type")
+    if offsets is not None:
+        _int32(offsets, None, "offsets")
+        if offsets.numel() < 1:
+            raise ValueError("offsets must have one element more than there are sequences")
+    tokens, heads, dim = q.shape
+    return AttentionRows(tokens, _flat(offsets), 0 if offsets is None else offsets.numel() - 1, heads, k.shape[1], dim,
+                         _dtype_code(q), int(bool(causal)), _i32(window, "window"),
+                         dim ** -0.5 if scale is None else scale)
+
+
+def _attention_workspace(a, backward):
+    need = ctypes.c_size_t(0)
+    _check(load().muon_attention_workspace_size(ctypes.byref(a), backward, ctypes.byref(need)))
+    return need.value
+
+
+def attention(q, k, v, offsets=None, causal: bool = True, window: int = 0, scale: Optional[float] = None, out=None,
+              lse=None, ws=None, stream=None):
+    """Self-attention over packed sequences (muon_attention): (out like q, lse float32 [heads,
+    tokens]). q: [tokens, heads, dim], k and v: [tokens, kv_heads, dim], bfloat16 or float16,
+    each with any strides that are multiples of 8 (the parts of a joint projection will do);
+    kv_heads divides heads. offsets: int32 [sequences + 1], the tokens where each sequence
+    begins and the last ends; None: one sequence. causal: tokens see themselves and earlier
+    ones, with window > 0 the last `window` of these. scale: dim ** -0.5 by default. Rows of
+    tokens outside every sequence are not written (a new result is not initialised there)."""
+    torch = _torch()
+    a = _attention_rows(q, k, v, offsets, causal, window, scale)
+    dev = _same_device(q, k, v, offsets, out, lse, ws)
+    with _on(dev, stream) as on:
+        out = _given(out, tuple(q.shape), q.dtype, on, "out")
+        lse = _given(lse, (q.shape[1], q.shape[0]), torch.float32, on, "lse")
+        ws = on.scratch(_attention_workspace(a, 0) if offsets is not None else 0, ws)
+        _check(load().muon_attention(ctypes.byref(a), ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(k, "k")),
+                                     ctypes.byref(_heads(v, "v")), ctypes.byref(_heads(out, "out")), _flat(lse), _flat(ws),
+                                     0 if ws is None else ws.numel() * ws.element_size(), on.handle))
+    return out, lse
+
+
+def attention_backward(do, q, k, v, out, lse, offsets=None, causal: bool = True, window: int = 0,
+                       scale: Optional[float] = None, dq=None, dk=None, dv=None, ws=None, stream=None):
+    """Gradient of attention (muon_attention_backward): (dq, dk, dv), from the gradient `do`
+    of its output and what the forward call returned; offsets, causal, window and scale as
+    in that call. dq, dk, dv: results to write into, such as the parts of the gradient of
+    a joint projection."""
+    torch = _torch()
+    a = _attention_rows(q, k, v, offsets, causal, window, scale)
+    for t, name in ((do, "do"), (out, "out")):
+        if t.dtype != q.dtype or t.shape != q.shape:
+            raise ValueError(f"{name} must be {q.dtype} of shape {tuple(q.shape)}")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (q.shape[1], q.shape[0]):
+        raise ValueError(f"lse must be float32 of shape {(q.shape[1], q.shape[0])}")
+    dev = _same_device(q, do, k, v, out, lse, offsets, dq, dk, dv, ws)
+    with _on(dev, stream) as on:
+        dq = _given(dq, tuple(q.shape), q.dtype, on, "dq")
+        dk = _given(dk, tuple(k.shape), q.dtype, on, "dk")
+        dv = _given(dv, tuple(k.shape), q.dtype, on, "dv")
+        ws = on.scratch(_attention_workspace(a, 1), ws)
+        _check(load().muon_attention_backward(
+            ctypes.byref(a), ctypes.byref(_heads(do, "do")), ctypes.byref(_heads(q, "q")), ctypes.byref(_heads(k, "k")),
+            ctypes.byref(_heads(v, "v")), ctypes.byref(_heads(out, "out")), _flat(lse), ctypes.byref(_heads(dq, "dq")),
+            ctypes.byref(_heads(dk, "dk")), ctypes.byref(_heads(dv, "dv")), _flat(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), on.handle))
+    return dq, dk, dv

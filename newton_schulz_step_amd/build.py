@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuonstep.so")
 
 SOURCES = ["capi.hip", "capi_moe.hip", "plan.cpp", "planner.cpp", "gemm.hip", "elementwise.hip", "fp8.hip",
-           "fp8_gemm.hip", "moe.hip", "capi_layer.hip", "norm.hip", "embedding.hip", "clip.hip"]
+           "fp8_gemm.hip", "moe.hip", "capi_layer.hip", "norm.hip", "embedding.hip", "clip.hip",
+           "attention.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

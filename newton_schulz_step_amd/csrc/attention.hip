@@ -1,0 +1,736 @@
+// Attention over packed sequences and its gradient (gfx950).
+//
+//   S = c Q K^T,  P = exp(S - lse),  O = P V          (rows of P over the keys that are seen)
+//   delta = rowsum(dO O),  dV = P^T dO,  dP = dO V^T,  dS = P (dP - delta),
+//   dQ = c dS K,  dK = c dS^T Q
+//
+// Every product runs on the 32x32x16 matrix instructions. A wave owns 32 columns of a
+// transposed score tile, one per lane (and its twin 32 lanes on): queries in the forward pass
+// and in dQ, keys in dK and dV. The instruction returns 4 consecutive rows of a column in 4
+// registers, rows 8 g + 4 (lane / 32) + 0..3, so that, rounded to 16 bits, the tile is the next
+// product's right operand as it stands, with the contraction in the order
+//   slot 8 h + e  <->  row 4 h + e (e < 4),  8 + 4 h + e - 4 (e >= 4)     of 16 rows,
+// and the left operand is read out of LDS in that order by transposed reads. No score leaves the
+// registers. The gradient is two kernels, one that walks over keys (dQ) and one that walks over
+// queries (dK, dV): scores and dP are computed twice, 7 products instead of 5, and in turn
+// every sum has one owner and one order, without atomics, and a group's query heads are
+// summed in registers.
+#include <algorithm>
+#include <type_traits>
+
+#include "attention.hpp"
+#include "fp8.hpp"
+#include "rows.hpp"
+
+namespace muon {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256, kWaves = 4;
+constexpr int kWaveRows = 32;      // columns of the transposed tile that a wave owns
+constexpr int kStage = 64;         // rows of a tile in LDS
+
+template <typename T> struct Half;
+template <> struct Half<__bf16> {
+  typedef bf16x8 v8;
+  typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 v4;
+  static constexpr bool narrow = false;   // fp32's range
+  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+  static __device__ __forceinline__ v4 transposed(MUON_LDS const char* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((MUON_LDS v4*)(p));
+  }
+};
+template <> struct Half<_Float16> {
+  typedef f16x8 v8;
+  typedef __attribute__((__vector_size__(4 * sizeof(__fp16)))) __fp16 v4;
+  static constexpr bool narrow = true;
+  static __device__ __forceinline__ f32x16 mfma(v8 a, v8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+  static __device__ __forceinline__ v4 transposed(MUON_LDS const char* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4f16((MUON_LDS v4*)(p));
+  }
+};
+
+// x of this lane and of its twin 32 lanes on.
+__device__ __forceinline__ float twin_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float twin_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles in LDS: rows of DP elements in 16-byte chunks, chunk c of row r at place c ^ swizzle(r).
+// A row operand is read with one row per lane and the same chunk in all of them, a transposed
+// one with four chunks of four consecutive rows per half wave; in both the swizzle spreads the
+// lanes that are served together over all banks.
+template <int DP> struct Tile {
+  static constexpr int CHUNKS = DP / 8, PITCH = DP * 2, BYTES = kStage * PITCH;
+  static constexpr int KS = DP / 16;    // steps of a contraction over the columns
+  static constexpr int DB = DP / 32;    // blocks of 32 columns
+  static constexpr int LOADS = BYTES / 1024 / kWaves;   // loads of a wave
+  static __device__ __forceinline__ int swizzle(int r) {
+    return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  }
+  // Byte offset of row `lane % 32`'s chunk lane / 32; step ks is at ^ (ks * 32).
+  static __device__ __forceinline__ int row_offset() {
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    return r * PITCH + ((h ^ swizzle(r)) << 4);
+  }
+  // Byte offset of the lane's part of a transposed read of rows 0 .. 15 and columns 0 .. 31;
+  // part e (slots 4 e ..) is at (^ (e * 32)) + e * 8 * PITCH, column block b at ^ (b * 64).
+  static __device__ __forceinline__ int column_offset() {
+    const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
+    const int r = 4 * (g >> 1) + (s >> 2), c = (g & 1) * 2 + ((s & 3) >> 1);
+    return r * PITCH + ((c ^ swizzle(r)) << 4) + (s & 1) * 8;
+  }
+};
+
+#define MUON_HEAD_RSRC(p, n) __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, n, 0x00027000)
+
+// The loads of one operand's tiles straight to LDS: columns behind `dim` and rows behind the
+// last one arrive as zeros (no bytes there).
+template <int DP> struct TileLoads {
+  int at[Tile<DP>::LOADS];
+  int stride, dim;   // bytes between rows, elements
+  __device__ __forceinline__ void init(int64_t token_stride, int d) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    stride = static_cast<int>(token_stride * 2);
+    dim = d;
+#pragma unroll
+    for (int i = 0; i < Tile<DP>::LOADS; ++i) {
+      const int place = (wave * Tile<DP>::LOADS + i) * 64 + lane;
+      const int r = place / Tile<DP>::CHUNKS, c = (place % Tile<DP>::CHUNKS) ^ Tile<DP>::swizzle(r);
+      at[i] = c * 8 < d ? r * stride + c * 16 : static_cast<int>(0x80000000u);
+    }
+  }
+  // `rows` rows from `from` on (none or fewer than none: zeros)
+  __device__ __forceinline__ void issue(const char* from, int rows, MUON_LDS char* to) const {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    rows = min(rows, kStage);
+    const auto rsrc = MUON_HEAD_RSRC(from, rows > 0 ? (rows - 1) * stride + dim * 2 : 0);
+#pragma unroll
+    for (int i = 0; i < Tile<DP>::LOADS; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(to + (wave * Tile<DP>::LOADS + i) * 1024), 16, at[i], 0, 0, 0);
+  }
+};
+
+__device__ __forceinline__ void arrived() {   // own loads to LDS and reads of it are done, then everybody's
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ typename Half<T>::v8 row_part(MUON_LDS const char* tile, int offset) {
+  return *reinterpret_cast<MUON_LDS const typename Half<T>::v8*>(tile + offset);
+}
+// Rows `16 k` .. of the tile, column block b, as a left operand with the rows contracted.
+template <typename T, int DP>
+__device__ __forceinline__ typename Half<T>::v8 column_part(MUON_LDS const char* tile, int offset, int k, int b) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  const u2 lo = __builtin_bit_cast(u2, Half<T>::transposed(tile + (offset ^ (b * 64)) + k * 16 * Tile<DP>::PITCH));
+  const u2 hi = __builtin_bit_cast(u2, Half<T>::transposed(tile + (offset ^ (b * 64) ^ 32) + (k * 16 + 8) * Tile<DP>::PITCH));
+  return __builtin_bit_cast(typename Half<T>::v8, u4{lo[0], lo[1], hi[0], hi[1]});
+}
+
+// 16 rows (two groups of four registers) of a column as a right operand, rounded to T. The
+// products' operands have 16 bits: half a step of T per probability or score gradient, which
+// adds up like noise over the keys, while all sums stay in fp32.
+template <typename T>
+__device__ __forceinline__ typename Half<T>::v8 operand(const f32x16& x, int k) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = x[8 * k + e];
+  T o[8];
+  rne<T, 8>(v, o);
+  typename Half<T>::v8 r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = o[e];
+  return r;
+}
+
+// The right operand of a lane's row: 8 columns per step, 16 apart.
+template <typename T, int DP>
+__device__ __forceinline__ void load_rows(typename Half<T>::v8 (&f)[Tile<DP>::KS], const char* base, int64_t row, bool there,
+                                          int64_t stride, int dim) {
+  const int h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+  for (int ks = 0; ks < Tile<DP>::KS; ++ks) {
+    const int c = ks * 16 + h * 8;
+    if (there && c < dim) {
+      f[ks] = *reinterpret_cast<const typename Half<T>::v8*>(base + (row * stride + c) * 2);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[ks][e] = static_cast<T>(0.0f);
+    }
+  }
+}
+
+// A wave's transposed result (rows = columns of the head, one of its 32 rows per lane), rounded
+// and written through LDS in whole rows. `lds`: 32 rows of the wave's own.
+template <typename T, int DP>
+__device__ __forceinline__ void store_rows(const f32x16 (&acc)[Tile<DP>::DB], float factor, MUON_LDS char* lds, char* base,
+                                           int64_t row, int64_t rows, int64_t stride, int dim) {
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  constexpr int CH = Tile<DP>::CHUNKS;
+  typedef T t4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int b = 0; b < Tile<DP>::DB; ++b)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = acc[b][4 * g + e] * factor;
+      T o[4];
+      rne<T, 4>(v, o);
+      *reinterpret_cast<MUON_LDS t4*>(lds + r * Tile<DP>::PITCH + (((b * 4 + g) ^ (r & (CH - 1))) << 4) + h * 8) =
+          t4{o[0], o[1], o[2], o[3]};
+    }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < kWaveRows * CH / 64; ++i) {
+    const int place = i * 64 + lane, k = place / CH, c = place % CH;
+    const auto v = *reinterpret_cast<MUON_LDS const typename Half<T>::v8*>(lds + k * Tile<DP>::PITCH + ((c ^ (k & (CH - 1))) << 4));
+    if (row + k < rows && c * 8 < dim) *reinterpret_cast<typename Half<T>::v8*>(base + ((row + k) * stride + c * 8) * 2) = v;
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
+// ---------------------------------------------------------------------------
+// Which rows of which sequence and which head a workgroup takes. Workgroups that follow each
+// other go to the 8 XCDs in turn, each with its own L2; with a multiple of 8 heads, a head's
+// tiles all go to one XCD, and neighbouring heads, which share keys, with it. The tiles
+// with the most work come first.
+struct Place {
+  int64_t start;   // first token of the sequence
+  int len;         // its tokens
+  int row;         // first row of the tile
+  int head;
+};
+
+__device__ __forceinline__ Place place_of(const AttentionArgs& a, int heads, bool keys) {
+  Place p;
+  const uint32_t b = flat_block();
+  uint32_t tile;
+  if ((heads & 7) == 0) {
+    const uint32_t per = heads >> 3, k = b >> 3;
+    tile = k / per;
+    p.head = static_cast<int>((b & 7) * per + k % per);
+  } else {
+    tile = b / heads;
+    p.head = static_cast<int>(b % heads);
+  }
+  if (tile >= static_cast<uint32_t>(a.tiles)) {
+    p.len = 0;
+    p.start = p.row = 0;
+    return p;
+  }
+  int t;
+  if (a.list != nullptr) {
+    const int4 e = a.list[tile];
+    p.start = e.x;
+    p.len = e.y;
+    t = e.z;
+  } else {
+    p.start = 0;
+    p.len = static_cast<int>(a.tokens);
+    t = a.tiles - 1 - static_cast<int>(tile);
+  }
+  // a query tile's work grows with its place, a key tile's shrinks
+  p.row = (keys && p.len > 0 ? (p.len - 1) / kAttentionRows - t : t) * kAttentionRows;
+  return p;
+}
+
+// A workgroup of the list: prefix sums over the sequences' tiles, then the tiles by work.
+constexpr int kListThreads = 1024, kListClasses = 256;
+
+__global__ __launch_bounds__(kListThreads) void attention_list_kernel(AttentionArgs a) {
+  __shared__ int wave_top[kListThreads / 64], wave_sum_[kListThreads / 64];
+  __shared__ int count[kListClasses];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int tokens = static_cast<int>(a.tokens);
+  int top = min(max(a.offsets[0], 0), tokens), tiles = 0;   // of the sequences so far
+  if (t < kListClasses) count[t] = 0;
+  for (int s0 = 0; s0 < a.sequences; s0 += kListThreads) {
+    const int s = s0 + t;
+    // an offset that falls counts as the largest before it
+    int end = s < a.sequences ? min(max(a.offsets[s + 1], 0), tokens) : 0;
+    int incl = end;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o, 64);
+      if (lane >= o) incl = max(incl, up);
+    }
+    if (lane == 63) wave_top[wave] = incl;
+    __syncthreads();
+    int before = top, all = top;
+    for (int w = 0; w < kListThreads / 64; ++w) {
+      if (w < wave) before = max(before, wave_top[w]);
+      all = max(all, wave_top[w]);
+    }
+    end = max(incl, before);
+    const int prev = __shfl_up(end, 1, 64);
+    const int start = lane > 0 ? prev : before;
+    const int n = s < a.sequences ? (end - start + kAttentionRows - 1) / kAttentionRows : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += up;
+    }
+    if (lane == 63) wave_sum_[wave] = sum;
+    __syncthreads();
+    int first = tiles + sum - n, total = tiles;
+    for (int w = 0; w < kListThreads / 64; ++w) {
+      if (w < wave) first += wave_sum_[w];
+      total += wave_sum_[w];
+    }
+    if (s < a.sequences) a.sequence_list[s] = int4{start, end - start, first, 0};
+    top = all;
+    tiles = total;
+    __syncthreads();
+  }
+  __threadfence_block();
+  __syncthreads();
+  // each tile's sequence by bisection, its work in classes
+  auto tile_of = [&](int x, int& cls) {
+    int lo = 0, hi = a.sequences - 1;   // the last sequence that begins at or before tile x and has tiles
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.sequence_list[mid].z <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    const int4 s = a.sequence_list[lo];
+    const int tile = x - s.z;
+    const int64_t keys = a.causal ? min<int64_t>((tile + 1) * static_cast<int64_t>(kAttentionRows), a.window + kAttentionRows) : s.y;
+    cls = kListClasses - 1 - static_cast<int>(min<int64_t>(kListClasses - 1, keys * kListClasses / (a.tokens + kAttentionRows)));
+    return int4{s.x, s.y, tile, 0};
+  };
+  for (int x = t; x < tiles; x += kListThreads) {
+    int cls;
+    tile_of(x, cls);
+    atomicAdd(&count[cls], 1);
+  }
+  __syncthreads();
+  if (wave == 0) {   // where each class begins
+    int base = 0;
+    for (int c0 = 0; c0 < kListClasses; c0 += 64) {
+      const int n = count[c0 + lane];
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += up;
+      }
+      count[c0 + lane] = base + sum - n;
+      base += __shfl(sum, 63, 64);
+    }
+  }
+  __syncthreads();
+  // the order within a class does not matter: every tile has its own results
+  for (int x = t; x < tiles; x += kListThreads) {
+    int cls;
+    const int4 e = tile_of(x, cls);
+    a.list[atomicAdd(&count[cls], 1)] = e;
+  }
+  for (int x = tiles + t; x < a.tiles; x += kListThreads) a.list[x] = int4{0, 0, 0, 0};
+}
+
+// Whether every row of [r0, r1] sees every key of [k0, k1].
+__device__ __forceinline__ bool all_seen(const AttentionArgs& a, int len, int r0, int r1, int k0, int k1) {
+  return k1 < len && (!a.causal || (k1 <= r0 && r1 - k0 < a.window));
+}
+__device__ __forceinline__ bool seen(const AttentionArgs& a, int len, int row, int key) {
+  return key < len && (!a.causal || (key <= row && row - key < a.window));
+}
+
+// ---------------------------------------------------------------------------
+// Forward: 128 queries per workgroup, keys and values in tiles of 64, two in LDS. The running
+// maximum that exponents refer to follows the true one only when it is 2^8 behind: the
+// exponentials stay below 2^8, and the sums are scaled again a few times per row at most.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
+  using H = Half<T>;
+  using TL = Tile<DP>;
+  __shared__ __align__(1024) char smem[4 * TL::BYTES];
+  MUON_LDS char* lds = (MUON_LDS char*)smem;
+  const Place p = place_of(a, a.heads, false);
+  if (p.row >= p.len) return;
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kv = p.head / a.group;
+  const char* q = static_cast<const char*>(a.q.data) + (p.start * a.q.token_stride + p.head * a.q.head_stride) * 2;
+  const char* k = static_cast<const char*>(a.k.data) + (p.start * a.k.token_stride + kv * a.k.head_stride) * 2;
+  const char* v = static_cast<const char*>(a.v.data) + (p.start * a.v.token_stride + kv * a.v.head_stride) * 2;
+  const int r0 = p.row + wave * kWaveRows, row = r0 + (lane & 31);
+  typename H::v8 qf[TL::KS];
+  load_rows<T, DP>(qf, q, row, row < p.len, a.q.token_stride, a.dim);
+
+  const int last = min(p.row + kAttentionRows, p.len) - 1;   // row of the workgroup
+  const int begin = a.causal ? max(0, p.row - a.window + 1) / kStage : 0;
+  const int end = (a.causal ? last : p.len - 1) / kStage + 1;
+  TileLoads<DP> lk, lv;
+  lk.init(a.k.token_stride, a.dim);
+  lv.init(a.v.token_stride, a.dim);
+  auto issue = [&](int t, int buf) {
+    const int j = t * kStage;
+    lk.issue(k + static_cast<int64_t>(j) * lk.stride, p.len - j, lds + buf * 2 * TL::BYTES);
+    lv.issue(v + static_cast<int64_t>(j) * lv.stride, p.len - j, lds + (buf * 2 + 1) * TL::BYTES);
+  };
+  const int ro = TL::row_offset(), co = TL::column_offset();
+  const float c = a.scale * kLog2e;
+  f32x16 acc[TL::DB];
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[b][e] = 0.0f;
+  float m = -__builtin_huge_valf(), sum = 0.0f;   // the maximum that exponents refer to; this lane's part of the sum
+
+  issue(begin, begin & 1);
+  for (int t = begin; t < end; ++t) {
+    arrived();
+    if (t + 1 < end) issue(t + 1, (t + 1) & 1);
+    const int j0 = t * kStage;
+    // the wave has no row, or none that sees these keys
+    if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
+    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
+    MUON_LDS const char* vt = kt + TL::BYTES;
+    f32x16 s[2];
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[jb][e] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < TL::KS; ++ks)
+        s[jb] = H::mfma(row_part<T>(kt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), qf[ks], s[jb]);
+    }
+    if (!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1)) {
+#pragma unroll
+      for (int jb = 0; jb < 2; ++jb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!seen(a, p.len, row, j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3))) s[jb][e] = -__builtin_huge_valf();
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[jb][e]);
+    top = twin_max(top);
+    if (__any((top - m) * c > 8.0f)) {   // also the first keys, after m = -inf
+      const float to = fmaxf(m, top);
+      const float keep = to == -__builtin_huge_valf() ? 1.0f : exp2f((m - to) * c);
+      m = to;
+      sum *= keep;
+#pragma unroll
+      for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[b][e] *= keep;
+    }
+    const float mc = m == -__builtin_huge_valf() ? 0.0f : m * c;   // no key seen so far: every term is 0
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[jb][e] = __builtin_amdgcn_exp2f(fmaf(s[jb][e], c, -mc));
+        sum += s[jb][e];
+      }
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const auto w = operand<T>(s[jb], kk);
+#pragma unroll
+        for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(vt, co, jb * 2 + kk, b), w, acc[b]);
+      }
+    }
+  }
+  sum = twin_sum(sum);
+  if (a.lse_out != nullptr && h == 0 && row < p.len) a.lse_out[p.head * a.tokens + p.start + row] = m * a.scale + logf(sum);
+  arrived();   // the tiles are read: their place takes the results
+  char* o = static_cast<char*>(a.o.data) + (p.start * a.o.token_stride + p.head * a.o.head_stride) * 2;
+  store_rows<T, DP>(acc, 1.0f / sum, lds + wave * kWaveRows * TL::PITCH, o, r0, p.len, a.o.token_stride, a.dim);
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// Gradient. First, per row and head, delta and the log-sum-exp in units of log 2: 16 lanes per row.
+template <int DT>
+__global__ __launch_bounds__(256) void attention_delta_kernel(AttentionArgs a) {
+  const int lane = threadIdx.x & 15;
+  const int64_t item = static_cast<int64_t>(flat_block()) * 16 + (threadIdx.x >> 4);
+  const int64_t t = item / a.heads;
+  const int h = static_cast<int>(item - t * a.heads);
+  const bool in = t < a.tokens && lane * 8 < a.dim;
+  float x[8], y[8];
+  read8<DT>(a.d_o.data, in ? t * a.d_o.token_stride + h * a.d_o.head_stride + lane * 8 : 0, in ? 8 : 0, x);
+  read8<DT>(a.o.data, in ? t * a.o.token_stride + h * a.o.head_stride + lane * 8 : 0, in ? 8 : 0, y);
+  float d = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) d += x[e] * y[e];
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) d += __shfl_xor(d, o, 64);
+  if (lane == 0 && t < a.tokens) {
+    a.delta[h * a.tokens + t] = d;
+    a.lse2[h * a.tokens + t] = a.lse[h * a.tokens + t] * kLog2e;
+  }
+}
+
+// Score gradients in fp16 would leave its range at either end: they carry a power of two per
+// column, found from the first ones and lowered when they grow, which the column's sums
+// carry too. bf16 has fp32's range and needs none.
+template <typename T> struct ColumnScale {
+  float up = 1.0f, down = 1.0f;
+  bool set = !Half<T>::narrow;
+  template <int N>
+  __device__ __forceinline__ void apply(f32x16& x, f32x16 (&acc)[N]) {
+    if constexpr (Half<T>::narrow) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+      if (__any(set ? top * up > 32768.0f : top > 0.0f)) {
+        top = twin_max(top);
+        if (top > 0.0f && (!set || top * up > 32768.0f)) {
+          // the largest goes to 2^10 .. 2^11
+          const int e = min(max(127 + 10 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 1), 253);
+          const float to = __uint_as_float(static_cast<uint32_t>(e) << 23);
+          const float ratio = set ? to * down : 1.0f;
+          up = to;
+          down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+          set = true;
+#pragma unroll
+          for (int b = 0; b < N; ++b)
+#pragma unroll
+            for (int e2 = 0; e2 < 16; ++e2) acc[b][e2] *= ratio;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] *= up;
+    }
+  }
+};
+
+// dQ: 128 queries per workgroup, keys and values in tiles of 64.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
+  using H = Half<T>;
+  using TL = Tile<DP>;
+  __shared__ __align__(1024) char smem[4 * TL::BYTES];
+  MUON_LDS char* lds = (MUON_LDS char*)smem;
+  const Place p = place_of(a, a.heads, false);
+  if (p.row >= p.len) return;
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kv = p.head / a.group;
+  const char* q = static_cast<const char*>(a.q.data) + (p.start * a.q.token_stride + p.head * a.q.head_stride) * 2;
+  const char* g = static_cast<const char*>(a.d_o.data) + (p.start * a.d_o.token_stride + p.head * a.d_o.head_stride) * 2;
+  const char* k = static_cast<const char*>(a.k.data) + (p.start * a.k.token_stride + kv * a.k.head_stride) * 2;
+  const char* v = static_cast<const char*>(a.v.data) + (p.start * a.v.token_stride + kv * a.v.head_stride) * 2;
+  const int r0 = p.row + wave * kWaveRows, row = r0 + (lane & 31);
+  typename H::v8 qf[TL::KS], gf[TL::KS];
+  load_rows<T, DP>(qf, q, row, row < p.len, a.q.token_stride, a.dim);
+  load_rows<T, DP>(gf, g, row, row < p.len, a.d_o.token_stride, a.dim);
+  const int64_t stat = p.head * a.tokens + p.start + min(row, p.len - 1);
+  const float lse2 = a.lse2[stat], delta = a.delta[stat];
+
+  const int last = min(p.row + kAttentionRows, p.len) - 1;
+  const int begin = a.causal ? max(0, p.row - a.window + 1) / kStage : 0;
+  const int end = (a.causal ? last : p.len - 1) / kStage + 1;
+  TileLoads<DP> lk, lv;
+  lk.init(a.k.token_stride, a.dim);
+  lv.init(a.v.token_stride, a.dim);
+  auto issue = [&](int t, int buf) {
+    const int j = t * kStage;
+    lk.issue(k + static_cast<int64_t>(j) * lk.stride, p.len - j, lds + buf * 2 * TL::BYTES);
+    lv.issue(v + static_cast<int64_t>(j) * lv.stride, p.len - j, lds + (buf * 2 + 1) * TL::BYTES);
+  };
+  const int ro = TL::row_offset(), co = TL::column_offset();
+  const float c = a.scale * kLog2e;
+  f32x16 acc[TL::DB];
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[b][e] = 0.0f;
+  ColumnScale<T> cs;
+
+  issue(begin, begin & 1);
+  for (int t = begin; t < end; ++t) {
+    arrived();
+    if (t + 1 < end) issue(t + 1, (t + 1) & 1);
+    const int j0 = t * kStage;
+    if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
+    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
+    MUON_LDS const char* vt = kt + TL::BYTES;
+    const bool whole = all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1);
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb) {
+      f32x16 s, d;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = d[e] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < TL::KS; ++ks) {
+        s = H::mfma(row_part<T>(kt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), qf[ks], s);
+        d = H::mfma(row_part<T>(vt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), gf[ks], d);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (d[e] - delta);
+        if (!whole && !seen(a, p.len, row, j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3))) w = 0.0f;
+        s[e] = w;
+      }
+      cs.apply(s, acc);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const auto w = operand<T>(s, kk);
+#pragma unroll
+        for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(kt, co, jb * 2 + kk, b), w, acc[b]);
+      }
+    }
+  }
+  arrived();
+  char* o = static_cast<char*>(a.dq.data) + (p.start * a.dq.token_stride + p.head * a.dq.head_stride) * 2;
+  store_rows<T, DP>(acc, a.scale * cs.down, lds + wave * kWaveRows * TL::PITCH, o, r0, p.len, a.dq.token_stride, a.dim);
+#endif
+}
+
+// dK and dV: 128 keys per workgroup, the queries of all heads of the group in tiles of 64.
+// Rows behind the sequence arrive as zeros (Q, dO, delta and the log-sum-exp), and add nothing.
+template <typename T, int DP>
+__global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttentionArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
+  using H = Half<T>;
+  using TL = Tile<DP>;
+  constexpr int BUF = 2 * TL::BYTES + 1024;   // Q, dO, then log-sum-exp and delta of the 64 rows
+  __shared__ __align__(1024) char smem[2 * BUF];
+  MUON_LDS char* lds = (MUON_LDS char*)smem;
+  const Place p = place_of(a, a.kv_heads, true);
+  if (p.row >= p.len) return;
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const char* k = static_cast<const char*>(a.k.data) + (p.start * a.k.token_stride + p.head * a.k.head_stride) * 2;
+  const char* v = static_cast<const char*>(a.v.data) + (p.start * a.v.token_stride + p.head * a.v.head_stride) * 2;
+  const int k0 = p.row + wave * kWaveRows, key = k0 + (lane & 31);
+  typename H::v8 kf[TL::KS], vf[TL::KS];
+  load_rows<T, DP>(kf, k, key, key < p.len, a.k.token_stride, a.dim);
+  load_rows<T, DP>(vf, v, key, key < p.len, a.v.token_stride, a.dim);
+
+  const int last = min(p.row + kAttentionRows, p.len) - 1;   // key of the workgroup
+  const int begin = a.causal ? p.row / kStage : 0;
+  const int rows_end = a.causal && a.window < p.len - last ? last + a.window : p.len;   // rows before it see a key
+  const int tiles = (rows_end - 1) / kStage + 1 - begin;
+  TileLoads<DP> lq, lg;
+  lq.init(a.q.token_stride, a.dim);
+  lg.init(a.d_o.token_stride, a.dim);
+  auto issue = [&](int n, int buf) {   // tile n of all heads'
+    const int hq = p.head * a.group + n / tiles, i = (begin + n % tiles) * kStage, rows = p.len - i;
+    MUON_LDS char* to = lds + buf * BUF;
+    lq.issue(static_cast<const char*>(a.q.data) + ((p.start + i) * a.q.token_stride + hq * a.q.head_stride) * 2, rows, to);
+    lg.issue(static_cast<const char*>(a.d_o.data) + ((p.start + i) * a.d_o.token_stride + hq * a.d_o.head_stride) * 2, rows,
+             to + TL::BYTES);
+    if (wave < 2) {
+      const float* from = (wave == 0 ? a.lse2 : a.delta) + hq * a.tokens + p.start + i;
+      const auto rsrc = MUON_HEAD_RSRC(reinterpret_cast<const char*>(from), min(rows, kStage) * 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(to + 2 * TL::BYTES + wave * 256), 4, lane * 4, 0, 0, 0);
+    }
+  };
+  const int ro = TL::row_offset(), co = TL::column_offset();
+  const float c = a.scale * kLog2e;
+  // probabilities in fp16 carry 2^8, so that small ones keep their bits
+  constexpr float PUP = H::narrow ? 256.0f : 1.0f;
+  f32x16 dk[TL::DB], dv[TL::DB];
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dk[b][e] = dv[b][e] = 0.0f;
+  ColumnScale<T> cs;
+
+  const int all = tiles * a.group;
+  issue(0, 0);
+  for (int n = 0; n < all; ++n) {
+    arrived();
+    if (n + 1 < all) issue(n + 1, (n + 1) & 1);
+    const int i0 = (begin + n % tiles) * kStage;
+    if (k0 >= p.len || (a.causal && (i0 + kStage - 1 < k0 || i0 - (k0 + kWaveRows - 1) >= a.window))) continue;
+    MUON_LDS const char* qt = lds + (n & 1) * BUF;
+    MUON_LDS const char* gt = qt + TL::BYTES;
+    MUON_LDS const char* st = gt + TL::BYTES;
+    const bool whole = all_seen(a, 0x7fffffff, i0, i0 + kStage - 1, k0, k0 + kWaveRows - 1);
+#pragma unroll
+    for (int ib = 0; ib < 2; ++ib) {
+      f32x16 s, d;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = d[e] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < TL::KS; ++ks) {
+        s = H::mfma(row_part<T>(qt, (ro ^ (ks * 32)) + ib * 32 * TL::PITCH), kf[ks], s);
+        d = H::mfma(row_part<T>(gt, (ro ^ (ks * 32)) + ib * 32 * TL::PITCH), vf[ks], d);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const f32x4 l = *reinterpret_cast<MUON_LDS const f32x4*>(st + (ib * 32 + u * 8 + h * 4) * 4);
+        const f32x4 x = *reinterpret_cast<MUON_LDS const f32x4*>(st + 256 + (ib * 32 + u * 8 + h * 4) * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float w = __builtin_amdgcn_exp2f(fmaf(s[4 * u + e], c, -l[e]));
+          float y = w * (d[4 * u + e] - x[e]);
+          if (!whole && !seen(a, 0x7fffffff, i0 + ib * 32 + u * 8 + h * 4 + e, key)) w = y = 0.0f;
+          d[4 * u + e] = y;
+          s[4 * u + e] = w * PUP;
+        }
+      }
+      cs.apply(d, dk);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const auto wp = operand<T>(s, kk), wd = operand<T>(d, kk);
+#pragma unroll
+        for (int b = 0; b < TL::DB; ++b) {
+          dv[b] = H::mfma(column_part<T, DP>(gt, co, ib * 2 + kk, b), wp, dv[b]);
+          dk[b] = H::mfma(column_part<T, DP>(qt, co, ib * 2 + kk, b), wd, dk[b]);
+        }
+      }
+    }
+  }
+  arrived();
+  MUON_LDS char* own = lds + wave * kWaveRows * TL::PITCH;
+  store_rows<T, DP>(dk, a.scale * cs.down, own,
+                    static_cast<char*>(a.dk.data) + (p.start * a.dk.token_stride + p.head * a.dk.head_stride) * 2, k0, p.len,
+                    a.dk.token_stride, a.dim);
+  store_rows<T, DP>(dv, 1.0f / PUP, own,
+                    static_cast<char*>(a.dv.data) + (p.start * a.dv.token_stride + p.head * a.dv.head_stride) * 2, k0, p.len,
+                    a.dv.token_stride, a.dim);
+#endif
+}
+
+// ---------------------------------------------------------------------------
+
+#define MUON_ATTENTION(kernel, heads)                                                                   \
+  do {                                                                                                  \
+    const dim3 grid = flat_grid(static_cast<int64_t>(a.tiles) * (heads));                               \
+    if (a.dtype == MUON_DTYPE_BF16) {                                                                   \
+      if (a.dim <= 64) hipLaunchKernelGGL((kernel<__bf16, 64>), grid, dim3(kThreads), 0, s, a);         \
+      else hipLaunchKernelGGL((kernel<__bf16, 128>), grid, dim3(kThreads), 0, s, a);                    \
+    } else {                                                                                            \
+      if (a.dim <= 64) hipLaunchKernelGGL((kernel<_Float16, 64>), grid, dim3(kThreads), 0, s, a);       \
+      else hipLaunchKernelGGL((kernel<_Float16, 128>), grid, dim3(kThreads), 0, s, a);                  \
+    }                                                                                                   \
+    return hipGetLastError();                                                                           \
+  } while (0)
+
+hipError_t launch_attention_list(const AttentionArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(attention_list_kernel, dim3(1), dim3(kListThreads), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_kernel, a.heads); }
+hipError_t launch_attention_delta(const AttentionArgs& a, hipStream_t s) {
+  const dim3 grid = flat_grid((a.tokens * a.heads + 15) / 16);
+  if (a.dtype == MUON_DTYPE_BF16) hipLaunchKernelGGL((attention_delta_kernel<MUON_DTYPE_BF16>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attention_delta_kernel<MUON_DTYPE_F16>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dq_kernel, a.heads); }
+hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dkv_kernel, a.kv_heads); }
+
+}  // namespace muon

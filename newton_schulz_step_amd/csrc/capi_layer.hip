@@ -1,4 +1,4 @@
-// C ABI of the norm, embedding and clipping operators: argument checks (all before the
+// C ABI of the norm, embedding, clipping and attention operators: argument checks (all before the
 // first launch) and launch arguments.
 #include <math.h>
 
@@ -6,6 +6,7 @@
 #include <string>
 #include <vector>
 
+#include "attention.hpp"
 #include "capi_util.hpp"
 #include "fp8.hpp"
 #include "layer.hpp"
@@ -198,6 +199,130 @@ static int each_clip_launch(const muon_tensor_t* in, const muon_tensor_t* out, i
     before += blocks;
   }
   return MUON_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+
+static int check_attention(const muon_attention_t* a) {
+  if (a == nullptr) return fail(MUON_ERR_NULL, "the attention's description is NULL");
+  if (a->tokens < 0 || a->tokens > MUON_ATTENTION_MAX_TOKENS)
+    return fail(MUON_ERR_BAD_SHAPE, "tokens must lie in [0, MUON_ATTENTION_MAX_TOKENS]");
+  if (a->offsets != nullptr && (a->sequences < 0 || a->sequences > MUON_ATTENTION_MAX_TOKENS))
+    return fail(MUON_ERR_BAD_SHAPE, "sequences must lie in [0, MUON_ATTENTION_MAX_TOKENS]");
+  if (a->heads < 1 || a->heads > MUON_ATTENTION_MAX_HEADS || a->kv_heads < 1 || a->heads % a->kv_heads != 0)
+    return fail(MUON_ERR_BAD_SHAPE, "heads must lie in [1, MUON_ATTENTION_MAX_HEADS] and be a multiple of kv_heads");
+  if (a->dim < 8 || a->dim > MUON_ATTENTION_MAX_DIM || a->dim % 8 != 0)
+    return fail(MUON_ERR_BAD_SHAPE, "dim must be a multiple of 8 in [8, MUON_ATTENTION_MAX_DIM]");
+  if (a->dtype != MUON_DTYPE_BF16 && a->dtype != MUON_DTYPE_F16) return fail(MUON_ERR_UNSUPPORTED, "attention: dtype must be BF16 or F16");
+  if (a->window < 0) return fail(MUON_ERR_BAD_SHAPE, "window must not be negative");
+  if (a->window > 0 && !a->causal) return fail(MUON_ERR_UNSUPPORTED, "a window needs causal");
+  if (!std::isfinite(a->scale) || !(a->scale > 0.0f)) return fail(MUON_ERR_BAD_HYPER, "scale must be finite and greater than 0");
+  if (misaligned(a->offsets, 4)) return fail(MUON_ERR_ALIGN, "offsets is not 4-byte aligned");
+  return MUON_OK;
+}
+
+// The heads of one operand as they lie in memory.
+struct HeadsSpan {
+  const muon_heads_t* t;
+  int64_t tokens, heads, dim;
+  const char* name;
+  // columns between the first and the last of a token
+  int64_t width() const { return (heads - 1) * t->head_stride + dim; }
+  const char* lo() const { return static_cast<const char*>(t->data); }
+  const char* hi() const { return lo() + ((tokens - 1) * t->token_stride + width()) * 2; }
+};
+
+static bool heads_meet(const HeadsSpan& a, const HeadsSpan& b) {
+  if (!(a.lo() < b.hi() && b.lo() < a.hi())) return false;
+  // parts of the same rows, such as those of a joint projection
+  const int64_t pitch = a.t->token_stride;
+  if (b.t->token_stride != pitch || a.width() > pitch || b.width() > pitch || (b.lo() - a.lo()) % 2 != 0) return true;
+  const int64_t d = (((b.lo() - a.lo()) / 2) % pitch + pitch) % pitch;
+  return !(d >= a.width() && d + b.width() <= pitch);
+}
+
+static int check_heads(const HeadsSpan& x, bool output) {
+  const std::string n(x.name);
+  const muon_heads_t* t = x.t;
+  if (t == nullptr) return fail(MUON_ERR_NULL, n + " is NULL");
+  if (x.tokens == 0) return MUON_OK;
+  if (t->data == nullptr) return fail(MUON_ERR_NULL, n + ": data is NULL");
+  if (misaligned(t->data, 16) || t->token_stride % 8 != 0 || t->head_stride % 8 != 0)
+    return fail(MUON_ERR_ALIGN, n + ": data must be 16-byte aligned and strides multiples of 8");
+  if (t->token_stride < x.dim || t->token_stride > (1 << 22))
+    return fail(MUON_ERR_BAD_SHAPE, n + ": token stride outside [dim, 2^22]");
+  if (t->head_stride < 0 || t->head_stride > (int64_t(1) << 40)) return fail(MUON_ERR_BAD_SHAPE, n + ": head stride outside [0, 2^40]");
+  if (output && x.heads > 1) {   // rows of tokens, each with all heads, or of heads, each with all tokens
+    const bool by_token = t->head_stride >= x.dim && t->token_stride >= x.width();
+    const bool by_head = t->head_stride >= (x.tokens - 1) * t->token_stride + x.dim;
+    if (!by_token && !by_head) return fail(MUON_ERR_BAD_SHAPE, n + ": heads and tokens overlap");
+  }
+  return MUON_OK;
+}
+
+// No output may meet another operand, nor a flat buffer.
+static int check_heads_apart(const std::vector<HeadsSpan>& outs, const std::vector<HeadsSpan>& ins, const std::vector<Span>& flat_outs,
+                             const std::vector<Span>& flat_ins) {
+  auto both = [](const char* x, const char* y) { return fail(MUON_ERR_OVERLAP, std::string("buffers overlap: ") + x + " and " + y); };
+  auto hits = [](const HeadsSpan& x, const Span& s) { return s.lo < s.hi && x.lo() < s.hi && s.lo < x.hi(); };
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (size_t j = i + 1; j < outs.size(); ++j)
+      if (heads_meet(outs[i], outs[j])) return both(outs[i].name, outs[j].name);
+    for (const HeadsSpan& x : ins)
+      if (heads_meet(outs[i], x)) return both(outs[i].name, x.name);
+    for (const Span& s : flat_ins)
+      if (hits(outs[i], s)) return both(outs[i].name, s.name);
+  }
+  for (const Span& s : flat_outs) {
+    for (const HeadsSpan& x : outs)
+      if (hits(x, s)) return both(x.name, s.name);
+    for (const HeadsSpan& x : ins)
+      if (hits(x, s)) return both(x.name, s.name);
+  }
+  return check_outputs(flat_outs, flat_ins);
+}
+
+static HeadsArg heads_arg(const muon_heads_t* t) { return {t->data, t->token_stride, t->head_stride}; }
+
+static AttentionArgs attention_args(const muon_attention_t* m) {
+  AttentionArgs a{};
+  a.tokens = m->tokens;
+  a.offsets = m->offsets;
+  a.sequences = m->offsets != nullptr ? m->sequences : 1;
+  // as many tiles as any sequences of so many tokens can have
+  const int64_t tiles = m->offsets != nullptr ? m->tokens / kAttentionRows + std::min<int64_t>(m->sequences, m->tokens)
+                                              : (m->tokens + kAttentionRows - 1) / kAttentionRows;
+  a.tiles = static_cast<int32_t>(tiles);
+  a.heads = m->heads;
+  a.kv_heads = m->kv_heads;
+  a.group = m->heads / m->kv_heads;
+  a.dim = m->dim;
+  a.causal = m->causal != 0;
+  a.window = m->window > 0 ? std::min(m->window, 1 << 30) : 1 << 30;
+  a.dtype = m->dtype;
+  a.scale = m->scale;
+  return a;
+}
+
+// Lays the workspace out from `base`; returns its size.
+static size_t attention_workspace(AttentionArgs& a, bool backward, char* base) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base == nullptr ? nullptr : base + at;
+    at += (bytes + 15) / 16 * 16;
+    return p;
+  };
+  if (a.offsets != nullptr) {
+    a.sequence_list = reinterpret_cast<int4*>(take(static_cast<size_t>(a.sequences) * sizeof(int4)));
+    a.list = reinterpret_cast<int4*>(take(static_cast<size_t>(a.tiles) * sizeof(int4)));
+  }
+  if (backward) {
+    const size_t rows = static_cast<size_t>(a.tokens) * static_cast<size_t>(a.heads) * sizeof(float);
+    a.lse2 = reinterpret_cast<float*>(take(rows));
+    a.delta = reinterpret_cast<float*>(take(rows));
+  }
+  return at;
 }
 
 }  // namespace muon
@@ -479,6 +604,96 @@ int muon_grad_clip(const muon_tensor_t* grads, const muon_tensor_t* outs, int32_
       ClipArgs a{};
       return launch(a, 0);
     }
+    return MUON_OK;
+  });
+}
+
+int muon_attention_workspace_size(const muon_attention_t* m, int32_t backward, size_t* bytes_out) {
+  return guarded([&]() -> int {
+    if (bytes_out == nullptr) return fail(MUON_ERR_NULL, "bytes_out is NULL");
+    const int st = check_attention(m);
+    if (st != MUON_OK) return st;
+    AttentionArgs a = attention_args(m);
+    *bytes_out = attention_workspace(a, backward != 0, nullptr);
+    return MUON_OK;
+  });
+}
+
+int muon_attention(const muon_attention_t* m, const muon_heads_t* q, const muon_heads_t* k, const muon_heads_t* v,
+                   const muon_heads_t* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int st = check_attention(m);
+    if (st != MUON_OK) return st;
+    const int64_t T = m->tokens;
+    const HeadsSpan sq{q, T, m->heads, m->dim, "q"}, sk{k, T, m->kv_heads, m->dim, "k"}, sv{v, T, m->kv_heads, m->dim, "v"},
+        so{o, T, m->heads, m->dim, "o"};
+    for (const HeadsSpan* x : {&sq, &sk, &sv})
+      if ((st = check_heads(*x, false)) != MUON_OK) return st;
+    if ((st = check_heads(so, true)) != MUON_OK) return st;
+    if (misaligned(lse, 4)) return fail(MUON_ERR_ALIGN, "lse is not 4-byte aligned");
+    AttentionArgs a = attention_args(m);
+    const size_t need = attention_workspace(a, false, nullptr);
+    if ((st = check_workspace(workspace, workspace_bytes, need, 16)) != MUON_OK) return st;
+    if (T == 0 || a.sequences == 0) return MUON_OK;
+    std::vector<Span> outs, ins;
+    if (lse != nullptr) outs.push_back(span_of(lse, T * m->heads * 4, "lse"));
+    if (need > 0) outs.push_back(span_of(workspace, static_cast<int64_t>(need), "workspace"));
+    if (m->offsets != nullptr) ins.push_back(span_of(m->offsets, (static_cast<int64_t>(m->sequences) + 1) * 4, "offsets"));
+    if ((st = check_heads_apart({so}, {sq, sk, sv}, outs, ins)) != MUON_OK) return st;
+    if (static_cast<int64_t>(a.tiles) * a.heads > 0x7fffffffLL) return fail(MUON_ERR_BAD_SHAPE, "too many tokens and heads for a launch");
+    attention_workspace(a, false, static_cast<char*>(workspace));
+    a.q = heads_arg(q);
+    a.k = heads_arg(k);
+    a.v = heads_arg(v);
+    a.o = heads_arg(o);
+    a.lse_out = lse;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (a.list != nullptr) MUON_LAUNCH("attention_list", s, launch_attention_list(a, s));
+    MUON_LAUNCH("attention", s, launch_attention(a, s));
+    return MUON_OK;
+  });
+}
+
+int muon_attention_backward(const muon_attention_t* m, const muon_heads_t* d_o, const muon_heads_t* q,
+                            const muon_heads_t* k, const muon_heads_t* v, const muon_heads_t* o, const float* lse,
+                            const muon_heads_t* dq, const muon_heads_t* dk, const muon_heads_t* dv, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int st = check_attention(m);
+    if (st != MUON_OK) return st;
+    const int64_t T = m->tokens;
+    const int32_t H = m->heads, K = m->kv_heads, D = m->dim;
+    const std::vector<HeadsSpan> ins = {{d_o, T, H, D, "d_o"}, {q, T, H, D, "q"}, {k, T, K, D, "k"}, {v, T, K, D, "v"}, {o, T, H, D, "o"}};
+    const std::vector<HeadsSpan> outs = {{dq, T, H, D, "dq"}, {dk, T, K, D, "dk"}, {dv, T, K, D, "dv"}};
+    for (const HeadsSpan& x : ins)
+      if ((st = check_heads(x, false)) != MUON_OK) return st;
+    for (const HeadsSpan& x : outs)
+      if ((st = check_heads(x, true)) != MUON_OK) return st;
+    if (T > 0 && lse == nullptr) return fail(MUON_ERR_NULL, "lse is NULL");
+    if (misaligned(lse, 4)) return fail(MUON_ERR_ALIGN, "lse is not 4-byte aligned");
+    AttentionArgs a = attention_args(m);
+    const size_t need = attention_workspace(a, true, nullptr);
+    if ((st = check_workspace(workspace, workspace_bytes, need, 16)) != MUON_OK) return st;
+    if (T == 0 || a.sequences == 0) return MUON_OK;
+    std::vector<Span> flat = {span_of(lse, T * H * 4, "lse")};
+    if (m->offsets != nullptr) flat.push_back(span_of(m->offsets, (static_cast<int64_t>(m->sequences) + 1) * 4, "offsets"));
+    if ((st = check_heads_apart(outs, ins, {span_of(workspace, static_cast<int64_t>(need), "workspace")}, flat)) != MUON_OK) return st;
+    if (static_cast<int64_t>(a.tiles) * H > 0x7fffffffLL) return fail(MUON_ERR_BAD_SHAPE, "too many tokens and heads for a launch");
+    attention_workspace(a, true, static_cast<char*>(workspace));
+    a.q = heads_arg(q);
+    a.k = heads_arg(k);
+    a.v = heads_arg(v);
+    a.o = heads_arg(o);
+    a.d_o = heads_arg(d_o);
+    a.dq = heads_arg(dq);
+    a.dk = heads_arg(dk);
+    a.dv = heads_arg(dv);
+    a.lse = lse;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (a.list != nullptr) MUON_LAUNCH("attention_list", s, launch_attention_list(a, s));
+    MUON_LAUNCH("attention_delta", s, launch_attention_delta(a, s));
+    MUON_LAUNCH("attention_dkv", s, launch_attention_dkv(a, s));
+    MUON_LAUNCH("attention_dq", s, launch_attention_dq(a, s));
     return MUON_OK;
   });
 }

@@ -49,3 +49,63 @@ def clip(grads, max_norm, sumsq=None):
     norm = np.sqrt(total)
     factor = min(1.0, max_norm / (norm + 1e-6))
     return norm, [g * factor for g in grads]
+
+
+def _sequences(offsets, tokens):
+    """(first, end) of each sequence: clamped, an offset that falls counts as the largest before it."""
+    if offsets is None:
+        return [(0, tokens)]
+    at = np.maximum.accumulate(np.clip(np.asarray(offsets, np.int64), 0, tokens))
+    return list(zip(at[:-1], at[1:]))
+
+
+def _hidden(n, causal, window):
+    far = np.arange(n)[:, None] - np.arange(n)
+    hidden = np.zeros((n, n), bool)
+    if causal:
+        hidden |= far < 0
+        if window:
+            hidden |= far >= window
+    return hidden
+
+
+def attention_heads(q, k, v, offsets=None, causal=True, window=0, scale=None):
+    """Per sequence and query head: (rows, head, key head, scores, probabilities, lse)."""
+    q, k, v = (np.asarray(t, np.float64) for t in (q, k, v))
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    group = q.shape[1] // k.shape[1]
+    for b, e in _sequences(offsets, q.shape[0]):
+        if e <= b:
+            continue
+        hidden = _hidden(e - b, causal, window)
+        for h in range(q.shape[1]):
+            s = np.where(hidden, -np.inf, scale * (q[b:e, h] @ k[b:e, h // group].T))
+            top = s.max(axis=1, keepdims=True)
+            p = np.exp(s - top)
+            total = p.sum(axis=1, keepdims=True)
+            yield slice(b, e), h, h // group, s, p / total, (top + np.log(total))[:, 0]
+
+
+def attention(q, k, v, **how):
+    """(out, lse); zeros outside the sequences."""
+    q, v = np.asarray(q, np.float64), np.asarray(v, np.float64)
+    out, lse = np.zeros(q.shape), np.zeros((q.shape[1], q.shape[0]))
+    for rows, h, kv, _, p, l in attention_heads(q, k, v, **how):
+        out[rows, h] = p @ v[rows, kv]
+        lse[h, rows] = l
+    return out, lse
+
+
+def attention_backward(do, q, k, v, scale=None, **how):
+    """(dq, dk, dv); zeros outside the sequences."""
+    do, q, k, v = (np.asarray(t, np.float64) for t in (do, q, k, v))
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(k.shape)
+    for rows, h, kv, _, p, _ in attention_heads(q, k, v, scale=scale, **how):
+        g = do[rows, h]
+        dv[rows, kv] += p.T @ g
+        dp = g @ v[rows, kv].T
+        ds = p * (dp - np.sum(p * dp, axis=1, keepdims=True))
+        dq[rows, h] = scale * (ds @ k[rows, kv])
+        dk[rows, kv] += scale * (ds.T @ q[rows, h])
+    return dq, dk, dv
