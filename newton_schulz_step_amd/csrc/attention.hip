@@ -68,7 +68,6 @@ template <int DP> struct Tile {
   static constexpr int CHUNKS = DP / 8, PITCH = DP * 2, BYTES = kStage * PITCH;
   static constexpr int KS = DP / 16;    // steps of a contraction over the columns
   static constexpr int DB = DP / 32;    // blocks of 32 columns
-  static constexpr int LOADS = BYTES / 1024 / kWaves;   // loads of a wave
   static __device__ __forceinline__ int swizzle(int r) {
     return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
   }
@@ -90,16 +89,17 @@ template <int DP> struct Tile {
 
 // The loads of one operand's tiles straight to LDS: columns behind `dim` and rows behind the
 // last one arrive as zeros (no bytes there).
-template <int DP> struct TileLoads {
-  int at[Tile<DP>::LOADS];
+template <int DP, int WAVES> struct TileLoads {
+  static constexpr int LOADS = Tile<DP>::BYTES / 1024 / WAVES;
+  int at[LOADS];
   int stride, dim;   // bytes between rows, elements
   __device__ __forceinline__ void init(int64_t token_stride, int d) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     stride = static_cast<int>(token_stride * 2);
     dim = d;
 #pragma unroll
-    for (int i = 0; i < Tile<DP>::LOADS; ++i) {
-      const int place = (wave * Tile<DP>::LOADS + i) * 64 + lane;
+    for (int i = 0; i < LOADS; ++i) {
+      const int place = (wave * LOADS + i) * 64 + lane;
       const int r = place / Tile<DP>::CHUNKS, c = (place % Tile<DP>::CHUNKS) ^ Tile<DP>::swizzle(r);
       at[i] = c * 8 < d ? r * stride + c * 16 : static_cast<int>(0x80000000u);
     }
@@ -110,8 +110,8 @@ template <int DP> struct TileLoads {
     rows = min(rows, kStage);
     const auto rsrc = MUON_HEAD_RSRC(from, rows > 0 ? (rows - 1) * stride + dim * 2 : 0);
 #pragma unroll
-    for (int i = 0; i < Tile<DP>::LOADS; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(to + (wave * Tile<DP>::LOADS + i) * 1024), 16, at[i], 0, 0, 0);
+    for (int i = 0; i < LOADS; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(to + (wave * LOADS + i) * 1024), 16, at[i], 0, 0, 0);
   }
 };
 
@@ -343,8 +343,18 @@ __global__ __launch_bounds__(kListThreads) void attention_list_kernel(AttentionA
 __device__ __forceinline__ bool all_seen(const AttentionArgs& a, int len, int r0, int r1, int k0, int k1) {
   return k1 < len && (!a.causal || (k1 <= r0 && r1 - k0 < a.window));
 }
-__device__ __forceinline__ bool seen(const AttentionArgs& a, int len, int row, int key) {
-  return key < len && (!a.causal || (key <= row && row - key < a.window));
+// The keys that a row sees, or the rows that see a key: low .. low + span.
+struct Sight {
+  int low;
+  uint32_t span;
+  __device__ __forceinline__ bool operator()(int x) const { return static_cast<uint32_t>(x - low) <= span; }
+};
+__device__ __forceinline__ Sight sight_of_row(const AttentionArgs& a, int len, int row) {
+  const int low = a.causal ? max(row - a.window + 1, 0) : 0, high = a.causal ? min(row, len - 1) : len - 1;
+  return {low, static_cast<uint32_t>(max(high - low, 0))};   // rows behind the end: any key, so that no sum is empty
+}
+__device__ __forceinline__ Sight sight_of_key(const AttentionArgs& a, int key) {
+  return {a.causal ? key : 0, a.causal ? static_cast<uint32_t>(a.window) - 1 : 0x7fffffffu};
 }
 
 // ---------------------------------------------------------------------------
@@ -373,7 +383,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
   const int last = min(p.row + kAttentionRows, p.len) - 1;   // row of the workgroup
   const int begin = a.causal ? max(0, p.row - a.window + 1) / kStage : 0;
   const int end = (a.causal ? last : p.len - 1) / kStage + 1;
-  TileLoads<DP> lk, lv;
+  TileLoads<DP, kWaves> lk, lv;
   lk.init(a.k.token_stride, a.dim);
   lv.init(a.v.token_stride, a.dim);
   auto issue = [&](int t, int buf) {
@@ -383,6 +393,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
   };
   const int ro = TL::row_offset(), co = TL::column_offset();
   const float c = a.scale * kLog2e;
+  const Sight sight = sight_of_row(a, p.len, row);
   f32x16 acc[TL::DB];
 #pragma unroll
   for (int b = 0; b < TL::DB; ++b)
@@ -390,30 +401,23 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
     for (int e = 0; e < 16; ++e) acc[b][e] = 0.0f;
   float m = -__builtin_huge_valf(), sum = 0.0f;   // the maximum that exponents refer to; this lane's part of the sum
 
-  issue(begin, begin & 1);
-  for (int t = begin; t < end; ++t) {
-    arrived();
-    if (t + 1 < end) issue(t + 1, (t + 1) & 1);
-    const int j0 = t * kStage;
-    // the wave has no row, or none that sees these keys
-    if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
-    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
+  auto step = [&](bool masked, MUON_LDS const char* kt, int j0) {
     MUON_LDS const char* vt = kt + TL::BYTES;
     f32x16 s[2];
 #pragma unroll
     for (int jb = 0; jb < 2; ++jb) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[jb][e] = 0.0f;
+      s[jb] = f32x16{};
 #pragma unroll
       for (int ks = 0; ks < TL::KS; ++ks)
         s[jb] = H::mfma(row_part<T>(kt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), qf[ks], s[jb]);
     }
-    if (!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1)) {
+    if (masked) {
+      asm volatile("");   // stays a branch
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (!seen(a, p.len, row, j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3))) s[jb][e] = -__builtin_huge_valf();
+          s[jb][e] = sight(j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3)) ? s[jb][e] : -__builtin_huge_valf();
     }
     float top = s[0][0];
 #pragma unroll
@@ -446,6 +450,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(vt, co, jb * 2 + kk, b), w, acc[b]);
       }
     }
+  };
+
+  issue(begin, begin & 1);
+  for (int t = begin; t < end; ++t) {
+    arrived();
+    if (t + 1 < end) issue(t + 1, (t + 1) & 1);
+    const int j0 = t * kStage;
+    // the wave has no row, or none that sees these keys
+    if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
+    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
+    step(!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1), kt, j0);
   }
   sum = twin_sum(sum);
   if (a.lse_out != nullptr && h == 0 && row < p.len) a.lse_out[p.head * a.tokens + p.start + row] = m * a.scale + logf(sum);
@@ -539,7 +554,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
   const int last = min(p.row + kAttentionRows, p.len) - 1;
   const int begin = a.causal ? max(0, p.row - a.window + 1) / kStage : 0;
   const int end = (a.causal ? last : p.len - 1) / kStage + 1;
-  TileLoads<DP> lk, lv;
+  TileLoads<DP, kWaves> lk, lv;
   lk.init(a.k.token_stride, a.dim);
   lv.init(a.v.token_stride, a.dim);
   auto issue = [&](int t, int buf) {
@@ -549,6 +564,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
   };
   const int ro = TL::row_offset(), co = TL::column_offset();
   const float c = a.scale * kLog2e;
+  const Sight sight = sight_of_row(a, p.len, row);
   f32x16 acc[TL::DB];
 #pragma unroll
   for (int b = 0; b < TL::DB; ++b)
@@ -556,30 +572,22 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
     for (int e = 0; e < 16; ++e) acc[b][e] = 0.0f;
   ColumnScale<T> cs;
 
-  issue(begin, begin & 1);
-  for (int t = begin; t < end; ++t) {
-    arrived();
-    if (t + 1 < end) issue(t + 1, (t + 1) & 1);
-    const int j0 = t * kStage;
-    if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
-    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
+  auto step = [&](bool masked, MUON_LDS const char* kt, int j0) {
     MUON_LDS const char* vt = kt + TL::BYTES;
-    const bool whole = all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1);
 #pragma unroll
     for (int jb = 0; jb < 2; ++jb) {
-      f32x16 s, d;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = d[e] = 0.0f;
+      f32x16 s = {}, d = {};
 #pragma unroll
       for (int ks = 0; ks < TL::KS; ++ks) {
         s = H::mfma(row_part<T>(kt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), qf[ks], s);
         d = H::mfma(row_part<T>(vt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), gf[ks], d);
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (d[e] - delta);
-        if (!whole && !seen(a, p.len, row, j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3))) w = 0.0f;
-        s[e] = w;
+      for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (d[e] - delta);
+      if (masked) {
+      asm volatile("");   // stays a branch
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = sight(j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3)) ? s[e] : 0.0f;
       }
       cs.apply(s, acc);
 #pragma unroll
@@ -589,6 +597,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
         for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(kt, co, jb * 2 + kk, b), w, acc[b]);
       }
     }
+  };
+
+  issue(begin, begin & 1);
+  for (int t = begin; t < end; ++t) {
+    arrived();
+    if (t + 1 < end) issue(t + 1, (t + 1) & 1);
+    const int j0 = t * kStage;
+    if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
+    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
+    step(!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1), kt, j0);
   }
   arrived();
   char* o = static_cast<char*>(a.dq.data) + (p.start * a.dq.token_stride + p.head * a.dq.head_stride) * 2;
@@ -596,36 +614,49 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
 #endif
 }
 
-// dK and dV: 128 keys per workgroup, the queries of all heads of the group in tiles of 64.
+// dK and dV: 128 keys per workgroup, the queries of all heads of the group in tiles of 64. Eight
+// waves, two per 32 keys, each with half of a tile's rows and sums of its own, joined at the
+// end: two waves per SIMD hide each other's exponentials, which one wave with all rows could
+// not. The keys' rows stay in registers, the values' in LDS, where the registers end.
 // Rows behind the sequence arrive as zeros (Q, dO, delta and the log-sum-exp), and add nothing.
+constexpr int kKeyWaves = 8;
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kKeyWaves * 64, 2) void attention_dkv_kernel(AttentionArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
   using H = Half<T>;
   using TL = Tile<DP>;
-  constexpr int BUF = 2 * TL::BYTES + 1024;   // Q, dO, then log-sum-exp and delta of the 64 rows
-  __shared__ __align__(1024) char smem[2 * BUF];
-  MUON_LDS char* lds = (MUON_LDS char*)smem;
+  constexpr int BUF = 2 * TL::BYTES + 512;                 // Q, dO, then log-sum-exp and delta of the 64 rows
+  constexpr int PART = TL::DB * 16 * 256;                  // a wave's sums
+  constexpr int BYTES = 2 * TL::BYTES + 2 * BUF > 8 * PART ? 2 * TL::BYTES + 2 * BUF : 8 * PART;
+  __shared__ __align__(1024) char smem[BYTES];
+  MUON_LDS char* values = (MUON_LDS char*)smem;
+  MUON_LDS char* lds = values + 2 * TL::BYTES;
   const Place p = place_of(a, a.kv_heads, true);
   if (p.row >= p.len) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave & 3, ib = wave >> 2;
   const char* k = static_cast<const char*>(a.k.data) + (p.start * a.k.token_stride + p.head * a.k.head_stride) * 2;
   const char* v = static_cast<const char*>(a.v.data) + (p.start * a.v.token_stride + p.head * a.v.head_stride) * 2;
-  const int k0 = p.row + wave * kWaveRows, key = k0 + (lane & 31);
-  typename H::v8 kf[TL::KS], vf[TL::KS];
+  const int k0 = p.row + kg * kWaveRows, key = k0 + (lane & 31);
+  typename H::v8 kf[TL::KS];
   load_rows<T, DP>(kf, k, key, key < p.len, a.k.token_stride, a.dim);
-  load_rows<T, DP>(vf, v, key, key < p.len, a.v.token_stride, a.dim);
 
   const int last = min(p.row + kAttentionRows, p.len) - 1;   // key of the workgroup
   const int begin = a.causal ? p.row / kStage : 0;
   const int rows_end = a.causal && a.window < p.len - last ? last + a.window : p.len;   // rows before it see a key
   const int tiles = (rows_end - 1) / kStage + 1 - begin;
-  TileLoads<DP> lq, lg;
+  TileLoads<DP, kKeyWaves> lq, lg, lv;
   lq.init(a.q.token_stride, a.dim);
   lg.init(a.d_o.token_stride, a.dim);
-  auto issue = [&](int n, int buf) {   // tile n of all heads'
-    const int hq = p.head * a.group + n / tiles, i = (begin + n % tiles) * kStage, rows = p.len - i;
+  lv.init(a.v.token_stride, a.dim);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = p.row + i * kStage;
+    lv.issue(v + static_cast<int64_t>(j) * lv.stride, p.len - j, values + i * TL::BYTES);
+  }
+  // tile `t` of head `hq`
+  auto issue = [&](int hq, int t, int buf) {
+    const int i = (begin + t) * kStage, rows = p.len - i;
     MUON_LDS char* to = lds + buf * BUF;
     lq.issue(static_cast<const char*>(a.q.data) + ((p.start + i) * a.q.token_stride + hq * a.q.head_stride) * 2, rows, to);
     lg.issue(static_cast<const char*>(a.d_o.data) + ((p.start + i) * a.d_o.token_stride + hq * a.d_o.head_stride) * 2, rows,
@@ -640,81 +671,111 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttentionArg
   const float c = a.scale * kLog2e;
   // probabilities in fp16 carry 2^8, so that small ones keep their bits
   constexpr float PUP = H::narrow ? 256.0f : 1.0f;
+  const Sight sight = sight_of_key(a, key);
   f32x16 dk[TL::DB], dv[TL::DB];
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b) dk[b] = dv[b] = f32x16{};
+  ColumnScale<T> cs;
+
+  auto step = [&](bool masked, MUON_LDS const char* buf, int i0) {
+    MUON_LDS const char* qt = buf + ib * 32 * TL::PITCH;
+    MUON_LDS const char* gt = qt + TL::BYTES;
+    MUON_LDS const char* st = buf + 2 * TL::BYTES + ib * 128 + h * 16;
+    MUON_LDS const char* vt = values + kg * 32 * TL::PITCH;
+    f32x16 s = {}, d = {};
+#pragma unroll
+    for (int ks = 0; ks < TL::KS; ++ks) {
+      s = H::mfma(row_part<T>(qt, ro ^ (ks * 32)), kf[ks], s);
+      d = H::mfma(row_part<T>(gt, ro ^ (ks * 32)), row_part<T>(vt, ro ^ (ks * 32)), d);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const f32x4 l = *reinterpret_cast<MUON_LDS const f32x4*>(st + u * 32);
+      const f32x4 x = *reinterpret_cast<MUON_LDS const f32x4*>(st + 256 + u * 32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = __builtin_amdgcn_exp2f(fmaf(s[4 * u + e], c, -l[e]));
+        d[4 * u + e] = w * (d[4 * u + e] - x[e]);
+        s[4 * u + e] = H::narrow ? w * PUP : w;
+      }
+    }
+    if (masked) {
+      asm volatile("");   // stays a branch
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const bool in = sight(i0 + 8 * (e >> 2) + 4 * h + (e & 3));
+        s[e] = in ? s[e] : 0.0f;
+        d[e] = in ? d[e] : 0.0f;
+      }
+    }
+    cs.apply(d, dk);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const auto wp = operand<T>(s, kk), wd = operand<T>(d, kk);
+#pragma unroll
+      for (int b = 0; b < TL::DB; ++b) {
+        dv[b] = H::mfma(column_part<T, DP>(gt, co, kk, b), wp, dv[b]);
+        dk[b] = H::mfma(column_part<T, DP>(qt, co, kk, b), wd, dk[b]);
+      }
+    }
+  };
+
+  const int all = tiles * a.group;
+  int hq = p.head * a.group, t = 0;   // of the tile that is loaded next
+  auto next = [&](int buf) {
+    issue(hq, t, buf);
+    if (++t == tiles) {
+      t = 0;
+      ++hq;
+    }
+  };
+  next(0);
+  int now = 0;   // the present tile of its head
+  for (int n = 0; n < all; ++n) {
+    arrived();
+    if (n + 1 < all) next((n + 1) & 1);
+    const int i0 = (begin + now) * kStage + ib * 32;
+    if (++now == tiles) now = 0;
+    if (k0 >= p.len || i0 >= p.len || (a.causal && (i0 + 31 < k0 || i0 - (k0 + kWaveRows - 1) >= a.window))) continue;
+    MUON_LDS const char* buf = lds + (n & 1) * BUF;
+    step(!all_seen(a, 0x7fffffff, i0, i0 + 31, k0, k0 + kWaveRows - 1), buf, i0);
+  }
+  // a pair of waves: the first one joins dK, the second one dV
+  arrived();
+  const float down = a.scale * cs.down;
+  MUON_LDS float* part = (MUON_LDS float*)(values + (kg * 2 + ib) * PART) + lane;
 #pragma unroll
   for (int b = 0; b < TL::DB; ++b)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dk[b][e] = dv[b][e] = 0.0f;
-  ColumnScale<T> cs;
-
-  const int all = tiles * a.group;
-  issue(0, 0);
-  for (int n = 0; n < all; ++n) {
-    arrived();
-    if (n + 1 < all) issue(n + 1, (n + 1) & 1);
-    const int i0 = (begin + n % tiles) * kStage;
-    if (k0 >= p.len || (a.causal && (i0 + kStage - 1 < k0 || i0 - (k0 + kWaveRows - 1) >= a.window))) continue;
-    MUON_LDS const char* qt = lds + (n & 1) * BUF;
-    MUON_LDS const char* gt = qt + TL::BYTES;
-    MUON_LDS const char* st = gt + TL::BYTES;
-    const bool whole = all_seen(a, 0x7fffffff, i0, i0 + kStage - 1, k0, k0 + kWaveRows - 1);
-#pragma unroll
-    for (int ib = 0; ib < 2; ++ib) {
-      f32x16 s, d;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = d[e] = 0.0f;
-#pragma unroll
-      for (int ks = 0; ks < TL::KS; ++ks) {
-        s = H::mfma(row_part<T>(qt, (ro ^ (ks * 32)) + ib * 32 * TL::PITCH), kf[ks], s);
-        d = H::mfma(row_part<T>(gt, (ro ^ (ks * 32)) + ib * 32 * TL::PITCH), vf[ks], d);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const f32x4 l = *reinterpret_cast<MUON_LDS const f32x4*>(st + (ib * 32 + u * 8 + h * 4) * 4);
-        const f32x4 x = *reinterpret_cast<MUON_LDS const f32x4*>(st + 256 + (ib * 32 + u * 8 + h * 4) * 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float w = __builtin_amdgcn_exp2f(fmaf(s[4 * u + e], c, -l[e]));
-          float y = w * (d[4 * u + e] - x[e]);
-          if (!whole && !seen(a, 0x7fffffff, i0 + ib * 32 + u * 8 + h * 4 + e, key)) w = y = 0.0f;
-          d[4 * u + e] = y;
-          s[4 * u + e] = w * PUP;
-        }
-      }
-      cs.apply(d, dk);
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const auto wp = operand<T>(s, kk), wd = operand<T>(d, kk);
-#pragma unroll
-        for (int b = 0; b < TL::DB; ++b) {
-          dv[b] = H::mfma(column_part<T, DP>(gt, co, ib * 2 + kk, b), wp, dv[b]);
-          dk[b] = H::mfma(column_part<T, DP>(qt, co, ib * 2 + kk, b), wd, dk[b]);
-        }
-      }
+    for (int e = 0; e < 16; ++e) {
+      dk[b][e] *= down;
+      part[(b * 16 + e) * 64] = ib == 0 ? dv[b][e] : dk[b][e];
     }
-  }
-  arrived();
-  MUON_LDS char* own = lds + wave * kWaveRows * TL::PITCH;
-  store_rows<T, DP>(dk, a.scale * cs.down, own,
-                    static_cast<char*>(a.dk.data) + (p.start * a.dk.token_stride + p.head * a.dk.head_stride) * 2, k0, p.len,
-                    a.dk.token_stride, a.dim);
-  store_rows<T, DP>(dv, 1.0f / PUP, own,
-                    static_cast<char*>(a.dv.data) + (p.start * a.dv.token_stride + p.head * a.dv.head_stride) * 2, k0, p.len,
-                    a.dv.token_stride, a.dim);
+  __syncthreads();
+  const MUON_LDS float* other = (const MUON_LDS float*)(values + (kg * 2 + 1 - ib) * PART) + lane;
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dk[b][e] = (ib == 0 ? dk[b][e] : dv[b][e]) + other[(b * 16 + e) * 64];
+  __syncthreads();
+  const HeadsArg& out = ib == 0 ? a.dk : a.dv;
+  store_rows<T, DP>(dk, ib == 0 ? 1.0f : 1.0f / PUP, values + wave * kWaveRows * TL::PITCH,
+                    static_cast<char*>(out.data) + (p.start * out.token_stride + p.head * out.head_stride) * 2, k0, p.len,
+                    out.token_stride, a.dim);
 #endif
 }
 
 // ---------------------------------------------------------------------------
 
-#define MUON_ATTENTION(kernel, heads)                                                                   \
+#define MUON_ATTENTION(kernel, heads, threads)                                                          \
   do {                                                                                                  \
     const dim3 grid = flat_grid(static_cast<int64_t>(a.tiles) * (heads));                               \
     if (a.dtype == MUON_DTYPE_BF16) {                                                                   \
-      if (a.dim <= 64) hipLaunchKernelGGL((kernel<__bf16, 64>), grid, dim3(kThreads), 0, s, a);         \
-      else hipLaunchKernelGGL((kernel<__bf16, 128>), grid, dim3(kThreads), 0, s, a);                    \
+      if (a.dim <= 64) hipLaunchKernelGGL((kernel<__bf16, 64>), grid, dim3(threads), 0, s, a);         \
+      else hipLaunchKernelGGL((kernel<__bf16, 128>), grid, dim3(threads), 0, s, a);                    \
     } else {                                                                                            \
-      if (a.dim <= 64) hipLaunchKernelGGL((kernel<_Float16, 64>), grid, dim3(kThreads), 0, s, a);       \
-      else hipLaunchKernelGGL((kernel<_Float16, 128>), grid, dim3(kThreads), 0, s, a);                  \
+      if (a.dim <= 64) hipLaunchKernelGGL((kernel<_Float16, 64>), grid, dim3(threads), 0, s, a);       \
+      else hipLaunchKernelGGL((kernel<_Float16, 128>), grid, dim3(threads), 0, s, a);                  \
     }                                                                                                   \
     return hipGetLastError();                                                                           \
   } while (0)
@@ -723,14 +784,14 @@ hipError_t launch_attention_list(const AttentionArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(attention_list_kernel, dim3(1), dim3(kListThreads), 0, s, a);
   return hipGetLastError();
 }
-hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_kernel, a.heads); }
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_kernel, a.heads, kThreads); }
 hipError_t launch_attention_delta(const AttentionArgs& a, hipStream_t s) {
   const dim3 grid = flat_grid((a.tokens * a.heads + 15) / 16);
   if (a.dtype == MUON_DTYPE_BF16) hipLaunchKernelGGL((attention_delta_kernel<MUON_DTYPE_BF16>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((attention_delta_kernel<MUON_DTYPE_F16>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
-hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dq_kernel, a.heads); }
-hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dkv_kernel, a.kv_heads); }
+hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dq_kernel, a.heads, kThreads); }
+hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dkv_kernel, a.kv_heads, kKeyWaves * 64); }
 
 }  // namespace muon
