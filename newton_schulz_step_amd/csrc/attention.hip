@@ -140,15 +140,11 @@ __device__ __forceinline__ typename Half<T>::v8 column_part(MUON_LDS const char*
 // adds up like noise over the keys, while all sums stay in fp32.
 template <typename T>
 __device__ __forceinline__ typename Half<T>::v8 operand(const f32x16& x, int k) {
-  float v[8];
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  f32x8 v;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = x[8 * k + e];
-  T o[8];
-  rne<T, 8>(v, o);
-  typename Half<T>::v8 r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = o[e];
-  return r;
+  return __builtin_convertvector(v, typename Half<T>::v8);
 }
 
 // The right operand of a lane's row: 8 columns per step, 16 apart.
@@ -357,8 +353,24 @@ __device__ __forceinline__ Sight sight_of_key(const AttentionArgs& a, int key) {
   return {a.causal ? key : 0, a.causal ? static_cast<uint32_t>(a.window) - 1 : 0x7fffffffu};
 }
 
+// What the scheduler is asked for: MFMAS matrix instructions, each with the LDS reads of the one
+// AHEAD places on, and with so many exponentials and other vector instructions behind it. A wave
+// issues in order: what stands between matrix instructions runs while those do.
+template <int MFMAS, int AHEAD, int READS, int EXPS, int OTHERS>
+__device__ __forceinline__ void interleave() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * READS, 0);
+#pragma unroll
+  for (int i = 0; i < MFMAS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (i + AHEAD < MFMAS) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    if constexpr (EXPS > 0) __builtin_amdgcn_sched_group_barrier(0x400, EXPS, 0);
+    if constexpr (OTHERS > 0) __builtin_amdgcn_sched_group_barrier(0x002, OTHERS, 0);
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Forward: 128 queries per workgroup, keys and values in tiles of 64, two in LDS. The running
+// Forward: 128 queries per workgroup, keys and values in tiles of 64, two of each in LDS. The
+// scores of tile t + 1 are formed while the exponentials of tile t are taken. The running
 // maximum that exponents refer to follows the true one only when it is 2^8 behind: the
 // exponentials stay below 2^8, and the sums are scaled again a few times per row at most.
 template <typename T, int DP>
@@ -366,7 +378,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
   using H = Half<T>;
   using TL = Tile<DP>;
-  __shared__ __align__(1024) char smem[4 * TL::BYTES];
+  __shared__ __align__(1024) char smem[4 * TL::BYTES];   // keys, keys, values, values
   MUON_LDS char* lds = (MUON_LDS char*)smem;
   const Place p = place_of(a, a.heads, false);
   if (p.row >= p.len) return;
@@ -377,33 +389,35 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
   const char* k = static_cast<const char*>(a.k.data) + (p.start * a.k.token_stride + kv * a.k.head_stride) * 2;
   const char* v = static_cast<const char*>(a.v.data) + (p.start * a.v.token_stride + kv * a.v.head_stride) * 2;
   const int r0 = p.row + wave * kWaveRows, row = r0 + (lane & 31);
-  typename H::v8 qf[TL::KS];
-  load_rows<T, DP>(qf, q, row, row < p.len, a.q.token_stride, a.dim);
-
-  const int last = min(p.row + kAttentionRows, p.len) - 1;   // row of the workgroup
+  // tiles that the workgroup's rows see, and how many of them are not behind the wave's rows
+  const int last = min(p.row + kAttentionRows, p.len) - 1;
   const int begin = a.causal ? max(0, p.row - a.window + 1) / kStage : 0;
-  const int end = (a.causal ? last : p.len - 1) / kStage + 1;
+  const int tiles = (a.causal ? last : p.len - 1) / kStage + 1 - begin;
+  const int own = r0 >= p.len ? 0 : a.causal ? min(tiles, (r0 + kWaveRows - 1) / kStage + 1 - begin) : tiles;
   TileLoads<DP, kWaves> lk, lv;
   lk.init(a.k.token_stride, a.dim);
   lv.init(a.v.token_stride, a.dim);
-  auto issue = [&](int t, int buf) {
-    const int j = t * kStage;
-    lk.issue(k + static_cast<int64_t>(j) * lk.stride, p.len - j, lds + buf * 2 * TL::BYTES);
-    lv.issue(v + static_cast<int64_t>(j) * lv.stride, p.len - j, lds + (buf * 2 + 1) * TL::BYTES);
+  auto issue_keys = [&](int t) {
+    const int j = (begin + t) * kStage;
+    lk.issue(k + static_cast<int64_t>(j) * lk.stride, p.len - j, lds + (t & 1) * TL::BYTES);
   };
+  auto issue_values = [&](int t) {
+    const int j = (begin + t) * kStage;
+    lv.issue(v + static_cast<int64_t>(j) * lv.stride, p.len - j, lds + (2 + (t & 1)) * TL::BYTES);
+  };
+  issue_keys(0);
+  typename H::v8 qf[TL::KS];
+  load_rows<T, DP>(qf, q, row, row < p.len, a.q.token_stride, a.dim);
   const int ro = TL::row_offset(), co = TL::column_offset();
   const float c = a.scale * kLog2e;
   const Sight sight = sight_of_row(a, p.len, row);
   f32x16 acc[TL::DB];
 #pragma unroll
-  for (int b = 0; b < TL::DB; ++b)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[b][e] = 0.0f;
+  for (int b = 0; b < TL::DB; ++b) acc[b] = f32x16{};
   float m = -__builtin_huge_valf(), sum = 0.0f;   // the maximum that exponents refer to; this lane's part of the sum
+  float top;                                      // the row's maximum in the tile whose exponentials come next
 
-  auto step = [&](bool masked, MUON_LDS const char* kt, int j0) {
-    MUON_LDS const char* vt = kt + TL::BYTES;
-    f32x16 s[2];
+  auto scores = [&](f32x16 (&s)[2], MUON_LDS const char* kt) {
 #pragma unroll
     for (int jb = 0; jb < 2; ++jb) {
       s[jb] = f32x16{};
@@ -411,7 +425,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
       for (int ks = 0; ks < TL::KS; ++ks)
         s[jb] = H::mfma(row_part<T>(kt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), qf[ks], s[jb]);
     }
-    if (masked) {
+  };
+  auto mask = [&](f32x16 (&s)[2], int t) {
+    const int j0 = (begin + t) * kStage;
+    if (!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1)) {
       asm volatile("");   // stays a branch
 #pragma unroll
       for (int jb = 0; jb < 2; ++jb)
@@ -419,12 +436,21 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         for (int e = 0; e < 16; ++e)
           s[jb][e] = sight(j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3)) ? s[jb][e] : -__builtin_huge_valf();
     }
-    float top = s[0][0];
+  };
+  auto largest = [&](const f32x16 (&s)[2]) {
+    float x = s[0][0];
 #pragma unroll
     for (int jb = 0; jb < 2; ++jb)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[jb][e]);
-    top = twin_max(top);
+      for (int e = 0; e < 16; ++e) x = fmaxf(x, s[jb][e]);
+    return twin_max(x);
+  };
+  // Tile t: the exponentials of its scores `s` and their product with the values; meanwhile, with
+  // `more`, the scores of tile t + 1.
+  auto step = [&](auto more, auto parity, int t, f32x16 (&s)[2], f32x16 (&next)[2]) {
+    constexpr bool MORE = decltype(more)::value;
+    MUON_LDS const char* kt = lds + (1 - decltype(parity)::value) * TL::BYTES;
+    MUON_LDS const char* vt = lds + (2 + decltype(parity)::value) * TL::BYTES;
     if (__any((top - m) * c > 8.0f)) {   // also the first keys, after m = -inf
       const float to = fmaxf(m, top);
       const float keep = to == -__builtin_huge_valf() ? 1.0f : exp2f((m - to) * c);
@@ -436,6 +462,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         for (int e = 0; e < 16; ++e) acc[b][e] *= keep;
     }
     const float mc = m == -__builtin_huge_valf() ? 0.0f : m * c;   // no key seen so far: every term is 0
+    if constexpr (MORE) scores(next, kt);
+    typename H::v8 w[4];
 #pragma unroll
     for (int jb = 0; jb < 2; ++jb) {
 #pragma unroll
@@ -443,25 +471,63 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
         s[jb][e] = __builtin_amdgcn_exp2f(fmaf(s[jb][e], c, -mc));
         sum += s[jb][e];
       }
+      w[2 * jb] = operand<T>(s[jb], 0);
+      w[2 * jb + 1] = operand<T>(s[jb], 1);
+    }
+    if constexpr (MORE) {
+      interleave<2 * TL::KS, 4, 1, 32 / (2 * TL::KS), 80 / (2 * TL::KS)>();
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const auto w = operand<T>(s[jb], kk);
+      for (int kk = 0; kk < 4; ++kk) asm volatile("" : "+v"(w[kk]));   // here, not behind the branch of the mask
+      asm volatile("" : "+v"(sum));
+      mask(next, t + 1);
+    }
 #pragma unroll
-        for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(vt, co, jb * 2 + kk, b), w, acc[b]);
-      }
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(vt, co, kk, b), w[kk], acc[b]);
+    if constexpr (MORE) {
+      top = largest(next);
+      interleave<4 * TL::DB, 3, 2, 0, 1>();
     }
   };
 
-  issue(begin, begin & 1);
-  for (int t = begin; t < end; ++t) {
-    arrived();
-    if (t + 1 < end) issue(t + 1, (t + 1) & 1);
-    const int j0 = t * kStage;
-    // the wave has no row, or none that sees these keys
-    if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
-    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
-    step(!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1), kt, j0);
+  // Before step t tile t's values and tile t + 1's keys arrive; the places that they leave free
+  // take the next ones.
+  arrived();
+  issue_values(0);
+  if (tiles > 1) issue_keys(1);
+  f32x16 s0[2], s1[2];
+  if (own > 0) {
+    scores(s0, lds);
+    mask(s0, 0);
+    top = largest(s0);
   }
+  auto turn = [&](int t) {
+    arrived();
+    if (t + 1 < tiles) issue_values(t + 1);
+    if (t + 2 < tiles) issue_keys(t + 2);
+  };
+  const std::integral_constant<int, 0> even{};
+  const std::integral_constant<int, 1> odd{};
+  int t = 0;
+  for (; t + 2 < own; t += 2) {
+    turn(t);
+    step(std::true_type(), even, t, s0, s1);
+    turn(t + 1);
+    step(std::true_type(), odd, t + 1, s1, s0);
+  }
+  if (t + 1 < own) {
+    turn(t);
+    step(std::true_type(), even, t, s0, s1);
+    turn(t + 1);
+    step(std::false_type(), odd, t + 1, s1, s0);
+    t += 2;
+  } else if (t < own) {
+    turn(t);
+    step(std::false_type(), even, t, s0, s1);
+    t += 1;
+  }
+  for (; t < tiles; ++t) turn(t);   // the other waves' tiles
   sum = twin_sum(sum);
   if (a.lse_out != nullptr && h == 0 && row < p.len) a.lse_out[p.head * a.tokens + p.start + row] = m * a.scale + logf(sum);
   arrived();   // the tiles are read: their place takes the results
