@@ -20,7 +20,6 @@
 
 #include "attention.hpp"
 #include "fp8.hpp"
-#include "rows.hpp"
 
 namespace muon {
 
@@ -537,27 +536,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// Gradient. First, per row and head, delta and the log-sum-exp in units of log 2: 16 lanes per row.
-template <int DT>
-__global__ __launch_bounds__(256) void attention_delta_kernel(AttentionArgs a) {
-  const int lane = threadIdx.x & 15;
-  const int64_t item = static_cast<int64_t>(flat_block()) * 16 + (threadIdx.x >> 4);
-  const int64_t t = item / a.heads;
-  const int h = static_cast<int>(item - t * a.heads);
-  const bool in = t < a.tokens && lane * 8 < a.dim;
-  float x[8], y[8];
-  read8<DT>(a.d_o.data, in ? t * a.d_o.token_stride + h * a.d_o.head_stride + lane * 8 : 0, in ? 8 : 0, x);
-  read8<DT>(a.o.data, in ? t * a.o.token_stride + h * a.o.head_stride + lane * 8 : 0, in ? 8 : 0, y);
-  float d = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) d += x[e] * y[e];
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) d += __shfl_xor(d, o, 64);
-  if (lane == 0 && t < a.tokens) {
-    a.delta[h * a.tokens + t] = d;
-    a.lse2[h * a.tokens + t] = a.lse[h * a.tokens + t] * kLog2e;
-  }
-}
+// Gradient.
 
 // Score gradients in fp16 would leave its range at either end: they carry a power of two per
 // column, found from the first ones and lowered when they grow, which the column's sums
@@ -593,7 +572,8 @@ template <typename T> struct ColumnScale {
   }
 };
 
-// dQ: 128 queries per workgroup, keys and values in tiles of 64.
+// dQ: 128 queries per workgroup, keys and values in tiles of 64. Each row's delta and log-sum-exp in
+// units of log 2 are formed on the way, for dK and dV.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
@@ -615,7 +595,22 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
   load_rows<T, DP>(qf, q, row, row < p.len, a.q.token_stride, a.dim);
   load_rows<T, DP>(gf, g, row, row < p.len, a.d_o.token_stride, a.dim);
   const int64_t stat = p.head * a.tokens + p.start + min(row, p.len - 1);
-  const float lse2 = a.lse2[stat], delta = a.delta[stat];
+  const float lse2 = a.lse[stat] * kLog2e;
+  float delta = 0.0f;
+  {
+    typename H::v8 of[TL::KS];
+    load_rows<T, DP>(of, static_cast<const char*>(a.o.data) + (p.start * a.o.token_stride + p.head * a.o.head_stride) * 2, row,
+                     row < p.len, a.o.token_stride, a.dim);
+#pragma unroll
+    for (int ks = 0; ks < TL::KS; ++ks)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = fmaf(static_cast<float>(gf[ks][e]), static_cast<float>(of[ks][e]), delta);
+  }
+  delta = twin_sum(delta);
+  if (h == 0 && row < p.len) {
+    a.lse2[stat] = lse2;
+    a.delta[stat] = delta;
+  }
 
   const int last = min(p.row + kAttentionRows, p.len) - 1;
   const int begin = a.causal ? max(0, p.row - a.window + 1) / kStage : 0;
@@ -851,12 +846,6 @@ hipError_t launch_attention_list(const AttentionArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_kernel, a.heads, kThreads); }
-hipError_t launch_attention_delta(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid = flat_grid((a.tokens * a.heads + 15) / 16);
-  if (a.dtype == MUON_DTYPE_BF16) hipLaunchKernelGGL((attention_delta_kernel<MUON_DTYPE_BF16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attention_delta_kernel<MUON_DTYPE_F16>), grid, dim3(256), 0, s, a);
-  return hipGetLastError();
-}
 hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dq_kernel, a.heads, kThreads); }
 hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dkv_kernel, a.kv_heads, kKeyWaves * 64); }
 

@@ -31,8 +31,7 @@ struct AttentionArgs {
 };
 hipError_t launch_attention_list(const AttentionArgs& a, hipStream_t s);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);
-hipError_t launch_attention_delta(const AttentionArgs& a, hipStream_t s);
-hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s);
-hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s);
+hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s);    // also lse2 and delta
+hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s);   // behind it
 
 }  // namespace muon

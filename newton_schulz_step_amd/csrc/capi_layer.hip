@@ -691,9 +691,8 @@ int muon_attention_backward(const muon_attention_t* m, const muon_heads_t* d_o, 
     a.lse = lse;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (a.list != nullptr) MUON_LAUNCH("attention_list", s, launch_attention_list(a, s));
-    MUON_LAUNCH("attention_delta", s, launch_attention_delta(a, s));
-    MUON_LAUNCH("attention_dkv", s, launch_attention_dkv(a, s));
     MUON_LAUNCH("attention_dq", s, launch_attention_dq(a, s));
+    MUON_LAUNCH("attention_dkv", s, launch_attention_dkv(a, s));
     return MUON_OK;
   });
 }
