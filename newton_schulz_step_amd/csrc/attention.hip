@@ -20,6 +20,7 @@
 
 #include "attention.hpp"
 #include "fp8.hpp"
+#include "rows.hpp"
 
 namespace muon {
 
@@ -64,7 +65,7 @@ __device__ __forceinline__ float twin_sum(float x) {
 // one with four chunks of four consecutive rows per half wave; in both the swizzle spreads the
 // lanes that are served together over all banks.
 template <int DP> struct Tile {
-  static constexpr int CHUNKS = DP / 8, PITCH = DP * 2, BYTES = kStage * PITCH;
+  static constexpr int CHUNKS = DP / 8, PITCH = DP * 2, BYTES = kStage * PITCH;   // of kStage rows
   static constexpr int KS = DP / 16;    // steps of a contraction over the columns
   static constexpr int DB = DP / 32;    // blocks of 32 columns
   static __device__ __forceinline__ int swizzle(int r) {
@@ -88,8 +89,8 @@ template <int DP> struct Tile {
 
 // The loads of one operand's tiles straight to LDS: columns behind `dim` and rows behind the
 // last one arrive as zeros (no bytes there).
-template <int DP, int WAVES> struct TileLoads {
-  static constexpr int LOADS = Tile<DP>::BYTES / 1024 / WAVES;
+template <int DP, int WAVES, int ROWS = kStage> struct TileLoads {
+  static constexpr int LOADS = ROWS * Tile<DP>::PITCH / 1024 / WAVES;
   int at[LOADS];
   int stride, dim;   // bytes between rows, elements
   __device__ __forceinline__ void init(int64_t token_stride, int d) {
@@ -106,7 +107,7 @@ template <int DP, int WAVES> struct TileLoads {
   // `rows` rows from `from` on (none or fewer than none: zeros)
   __device__ __forceinline__ void issue(const char* from, int rows, MUON_LDS char* to) const {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    rows = min(rows, kStage);
+    rows = min(rows, ROWS);
     const auto rsrc = MUON_HEAD_RSRC(from, rows > 0 ? (rows - 1) * stride + dim * 2 : 0);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
@@ -633,15 +634,19 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
     for (int e = 0; e < 16; ++e) acc[b][e] = 0.0f;
   ColumnScale<T> cs;
 
-  auto step = [&](bool masked, MUON_LDS const char* kt, int j0) {
+  auto step = [&](bool masked, int buf, int j0) {
+    MUON_LDS const char* kt = lds;
     MUON_LDS const char* vt = kt + TL::BYTES;
+    // places in LDS with the tile's in them, made anew for each tile (registers)
+    int rk = ro + buf * 2 * TL::BYTES, ck = co + buf * 2 * TL::BYTES;
+    asm volatile("" : "+v"(rk), "+v"(ck));
 #pragma unroll
     for (int jb = 0; jb < 2; ++jb) {
       f32x16 s = {}, d = {};
 #pragma unroll
       for (int ks = 0; ks < TL::KS; ++ks) {
-        s = H::mfma(row_part<T>(kt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), qf[ks], s);
-        d = H::mfma(row_part<T>(vt, (ro ^ (ks * 32)) + jb * 32 * TL::PITCH), gf[ks], d);
+        s = H::mfma(row_part<T>(kt, (rk ^ (ks * 32)) + jb * 32 * TL::PITCH), qf[ks], s);
+        d = H::mfma(row_part<T>(vt, (rk ^ (ks * 32)) + jb * 32 * TL::PITCH), gf[ks], d);
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (d[e] - delta);
@@ -655,7 +660,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
       for (int kk = 0; kk < 2; ++kk) {
         const auto w = operand<T>(s, kk);
 #pragma unroll
-        for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(kt, co, jb * 2 + kk, b), w, acc[b]);
+        for (int b = 0; b < TL::DB; ++b) acc[b] = H::mfma(column_part<T, DP>(kt, ck, jb * 2 + kk, b), w, acc[b]);
       }
     }
   };
@@ -666,8 +671,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
     if (t + 1 < end) issue(t + 1, (t + 1) & 1);
     const int j0 = t * kStage;
     if (r0 >= p.len || (a.causal && (j0 > r0 + kWaveRows - 1 || j0 + kStage - 1 <= r0 - a.window))) continue;
-    MUON_LDS const char* kt = lds + (t & 1) * 2 * TL::BYTES;
-    step(!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1), kt, j0);
+    step(!all_seen(a, p.len, r0, r0 + kWaveRows - 1, j0, j0 + kStage - 1), t & 1, j0);
   }
   arrived();
   char* o = static_cast<char*>(a.dq.data) + (p.start * a.dq.token_stride + p.head * a.dq.head_stride) * 2;
@@ -675,59 +679,84 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
 #endif
 }
 
-// dK and dV: 128 keys per workgroup, the queries of all heads of the group in tiles of 64. Eight
-// waves, two per 32 keys, each with half of a tile's rows and sums of its own, joined at the
-// end: two waves per SIMD hide each other's exponentials, which one wave with all rows could
-// not. The keys' rows stay in registers, the values' in LDS, where the registers end.
+// dK and dV: 128 keys per workgroup, the queries of all heads of the group in tiles. The keys' rows
+// stay in registers, the values' in LDS, where the registers end.
+// With HALVES = 1 four waves own 32 keys each and take tiles of 32 rows: two workgroups fit a CU, and
+// one's exponentials, first loads and results pass behind the other's products. With HALVES = 2 two
+// waves share 32 keys, each with half of a tile of 64 rows and sums of its own, joined at the end:
+// one workgroup per CU that is done in half the time, for fewer workgroups than two per CU fill
+// evenly (with causal the longest take twice the average). Bfloat16, dimension 128: 2432 workgroups 219 us
+// with 2, 190 with 1; 512 of them 83 us with 2, 110 with 1.
+// Where there are fewer still, a key tile's queries are cut into parts, whose sums
+// attention_join_kernel adds in order (8 workgroups of 1000 tokens: 216 us, in 8 parts 60).
 // Rows behind the sequence arrive as zeros (Q, dO, delta and the log-sum-exp), and add nothing.
-constexpr int kKeyWaves = 8;
-template <typename T, int DP>
-__global__ __launch_bounds__(kKeyWaves * 64, 2) void attention_dkv_kernel(AttentionArgs a) {
+template <typename T, int DP, int HALVES>
+__global__ __launch_bounds__(kThreads * HALVES, 2) void attention_dkv_kernel(AttentionArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
   using H = Half<T>;
   using TL = Tile<DP>;
-  constexpr int BUF = 2 * TL::BYTES + 512;                 // Q, dO, then log-sum-exp and delta of the 64 rows
+  constexpr int ROWS = kWaveRows * HALVES, WAVES = kWaves * HALVES;
+  constexpr int BYTES = ROWS * TL::PITCH;
+  constexpr int BUF = 2 * BYTES + 512;                     // Q, dO, then log-sum-exp and delta of the rows
+  constexpr int VALUES = kAttentionRows * TL::PITCH;
   constexpr int PART = TL::DB * 16 * 256;                  // a wave's sums
-  constexpr int BYTES = 2 * TL::BYTES + 2 * BUF > 8 * PART ? 2 * TL::BYTES + 2 * BUF : 8 * PART;
-  __shared__ __align__(1024) char smem[BYTES];
+  constexpr int USED = VALUES + 2 * BUF, JOINED = HALVES == 2 ? WAVES * PART : 0;
+  __shared__ __align__(1024) char smem[USED > JOINED ? USED : JOINED];
   MUON_LDS char* values = (MUON_LDS char*)smem;
-  MUON_LDS char* lds = values + 2 * TL::BYTES;
-  const Place p = place_of(a, a.kv_heads, true);
+  MUON_LDS char* lds = values + VALUES;
+  Place p = place_of(a, a.kv_heads * a.parts, true);
   if (p.row >= p.len) return;
+  const int part = p.head % a.parts;
+  p.head /= a.parts;
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave & 3, ib = wave >> 2;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave % kWaves, half = wave / kWaves;
   const char* k = static_cast<const char*>(a.k.data) + (p.start * a.k.token_stride + p.head * a.k.head_stride) * 2;
   const char* v = static_cast<const char*>(a.v.data) + (p.start * a.v.token_stride + p.head * a.v.head_stride) * 2;
   const int k0 = p.row + kg * kWaveRows, key = k0 + (lane & 31);
-  typename H::v8 kf[TL::KS];
-  load_rows<T, DP>(kf, k, key, key < p.len, a.k.token_stride, a.dim);
 
   const int last = min(p.row + kAttentionRows, p.len) - 1;   // key of the workgroup
-  const int begin = a.causal ? p.row / kStage : 0;
+  const int begin = a.causal ? p.row / ROWS : 0;
   const int rows_end = a.causal && a.window < p.len - last ? last + a.window : p.len;   // rows before it see a key
-  const int tiles = (rows_end - 1) / kStage + 1 - begin;
-  TileLoads<DP, kKeyWaves> lq, lg, lv;
+  const int tiles = (rows_end - 1) / ROWS + 1 - begin;
+  TileLoads<DP, WAVES, ROWS> lq, lg;
   lq.init(a.q.token_stride, a.dim);
   lg.init(a.d_o.token_stride, a.dim);
-  lv.init(a.v.token_stride, a.dim);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int j = p.row + i * kStage;
-    lv.issue(v + static_cast<int64_t>(j) * lv.stride, p.len - j, values + i * TL::BYTES);
-  }
   // tile `t` of head `hq`
   auto issue = [&](int hq, int t, int buf) {
-    const int i = (begin + t) * kStage, rows = p.len - i;
+    const int i = (begin + t) * ROWS, rows = p.len - i;
     MUON_LDS char* to = lds + buf * BUF;
     lq.issue(static_cast<const char*>(a.q.data) + ((p.start + i) * a.q.token_stride + hq * a.q.head_stride) * 2, rows, to);
     lg.issue(static_cast<const char*>(a.d_o.data) + ((p.start + i) * a.d_o.token_stride + hq * a.d_o.head_stride) * 2, rows,
-             to + TL::BYTES);
+             to + BYTES);
     if (wave < 2) {
       const float* from = (wave == 0 ? a.lse2 : a.delta) + hq * a.tokens + p.start + i;
-      const auto rsrc = MUON_HEAD_RSRC(reinterpret_cast<const char*>(from), min(rows, kStage) * 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(to + 2 * TL::BYTES + wave * 256), 4, lane * 4, 0, 0, 0);
+      const auto rsrc = MUON_HEAD_RSRC(reinterpret_cast<const char*>(from), min(rows, ROWS) * 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MUON_LDS void*)(to + 2 * BYTES + wave * 256), 4, lane * 4, 0, 0, 0);
     }
   };
+  {
+    TileLoads<DP, WAVES, ROWS> lv;
+    lv.init(a.v.token_stride, a.dim);
+#pragma unroll
+    for (int i = 0; i < kAttentionRows / ROWS; ++i) {
+      const int j = p.row + i * ROWS;
+      lv.issue(v + static_cast<int64_t>(j) * lv.stride, p.len - j, values + i * BYTES);
+    }
+  }
+  // tiles of all heads, one head after the other; this part's
+  const int64_t all = static_cast<int64_t>(tiles) * a.group;
+  const int from = static_cast<int>(all * part / a.parts), to = static_cast<int>(all * (part + 1) / a.parts);
+  int hq = p.head * a.group + from / tiles, ahead = from % tiles;   // of the tile that is loaded next
+  auto next = [&](int buf) {
+    issue(hq, ahead, buf);
+    if (++ahead == tiles) {
+      ahead = 0;
+      ++hq;
+    }
+  };
+  if (from < to) next(from & 1);
+  typename H::v8 kf[TL::KS];
+  load_rows<T, DP>(kf, k, key, key < p.len, a.k.token_stride, a.dim);
   const int ro = TL::row_offset(), co = TL::column_offset();
   const float c = a.scale * kLog2e;
   // probabilities in fp16 carry 2^8, so that small ones keep their bits
@@ -738,16 +767,20 @@ __global__ __launch_bounds__(kKeyWaves * 64, 2) void attention_dkv_kernel(Attent
   for (int b = 0; b < TL::DB; ++b) dk[b] = dv[b] = f32x16{};
   ColumnScale<T> cs;
 
-  auto step = [&](bool masked, MUON_LDS const char* buf, int i0) {
-    MUON_LDS const char* qt = buf + ib * 32 * TL::PITCH;
-    MUON_LDS const char* gt = qt + TL::BYTES;
-    MUON_LDS const char* st = buf + 2 * TL::BYTES + ib * 128 + h * 16;
-    MUON_LDS const char* vt = values + kg * 32 * TL::PITCH;
+  auto step = [&](bool masked, int buf, int i0) {
+    MUON_LDS const char* qt = lds;
+    MUON_LDS const char* gt = qt + BYTES;
+    MUON_LDS const char* st = lds + buf * BUF + 2 * BYTES + half * kWaveRows * 4 + h * 16;
+    // places in LDS with the tile's in them, made anew for each tile: kept from tile to tile, those
+    // of all steps would fill the registers
+    int rq = ro + buf * BUF + half * kWaveRows * TL::PITCH, cq = co + buf * BUF + half * kWaveRows * TL::PITCH;
+    int rv = ro + kg * kWaveRows * TL::PITCH;
+    asm volatile("" : "+v"(rq), "+v"(cq), "+v"(rv));
     f32x16 s = {}, d = {};
 #pragma unroll
     for (int ks = 0; ks < TL::KS; ++ks) {
-      s = H::mfma(row_part<T>(qt, ro ^ (ks * 32)), kf[ks], s);
-      d = H::mfma(row_part<T>(gt, ro ^ (ks * 32)), row_part<T>(vt, ro ^ (ks * 32)), d);
+      s = H::mfma(row_part<T>(qt, rq ^ (ks * 32)), kf[ks], s);
+      d = H::mfma(row_part<T>(gt, rq ^ (ks * 32)), row_part<T>(values, rv ^ (ks * 32)), d);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -775,68 +808,108 @@ __global__ __launch_bounds__(kKeyWaves * 64, 2) void attention_dkv_kernel(Attent
       const auto wp = operand<T>(s, kk), wd = operand<T>(d, kk);
 #pragma unroll
       for (int b = 0; b < TL::DB; ++b) {
-        dv[b] = H::mfma(column_part<T, DP>(gt, co, kk, b), wp, dv[b]);
-        dk[b] = H::mfma(column_part<T, DP>(qt, co, kk, b), wd, dk[b]);
+        dv[b] = H::mfma(column_part<T, DP>(gt, cq, kk, b), wp, dv[b]);
+        dk[b] = H::mfma(column_part<T, DP>(qt, cq, kk, b), wd, dk[b]);
       }
     }
   };
 
-  const int all = tiles * a.group;
-  int hq = p.head * a.group, t = 0;   // of the tile that is loaded next
-  auto next = [&](int buf) {
-    issue(hq, t, buf);
-    if (++t == tiles) {
-      t = 0;
-      ++hq;
+  int now = from % tiles;   // the present tile of its head
+  for (int n = from; n < to; ++n) {
+    arrived();
+    if (n + 1 < to) next((n + 1) & 1);
+    const int i0 = (begin + now) * ROWS + half * kWaveRows;
+    if (++now == tiles) now = 0;
+    if (k0 >= p.len || i0 >= p.len || (a.causal && (i0 + kWaveRows - 1 < k0 || i0 - (k0 + kWaveRows - 1) >= a.window))) continue;
+    step(!all_seen(a, 0x7fffffff, i0, i0 + kWaveRows - 1, k0, k0 + kWaveRows - 1), n & 1, i0);
+  }
+  const float xk = a.scale * cs.down, xv = 1.0f / PUP;
+#pragma unroll
+  for (int b = 0; b < TL::DB; ++b) {
+    dk[b] *= xk;
+    dv[b] *= xv;
+  }
+  arrived();   // the tiles are read: their place takes the results
+  if constexpr (HALVES == 2) {
+    // a pair of waves: the first one joins dK, the second one dV (in dk)
+    MUON_LDS float* mine = (MUON_LDS float*)(values + (kg * 2 + half) * PART) + lane;
+#pragma unroll
+    for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mine[(b * 16 + e) * 64] = half == 0 ? dv[b][e] : dk[b][e];
+    __syncthreads();
+    const MUON_LDS float* other = (const MUON_LDS float*)(values + (kg * 2 + 1 - half) * PART) + lane;
+#pragma unroll
+    for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) dk[b][e] = (half == 0 ? dk[b][e] : dv[b][e]) + other[(b * 16 + e) * 64];
+    __syncthreads();
+  }
+  // dK (which = 0) or dV of the wave's keys
+  auto store = [&](const f32x16(&x)[TL::DB], int which) {
+    if (a.parts > 1) {
+      if (key >= p.len) return;
+      const int64_t row = static_cast<int64_t>(part * 2 + which) * a.tokens + p.start + key;
+      float* to = a.partial + (row * a.kv_heads + p.head) * a.dim;
+#pragma unroll
+      for (int b = 0; b < TL::DB; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int at = b * 32 + g * 8 + h * 4;
+          if (at < a.dim) *reinterpret_cast<f32x4*>(to + at) = f32x4{x[b][4 * g], x[b][4 * g + 1], x[b][4 * g + 2], x[b][4 * g + 3]};
+        }
+    } else {
+      const HeadsArg& out = which == 0 ? a.dk : a.dv;
+      store_rows<T, DP>(x, 1.0f, values + wave * kWaveRows * TL::PITCH,
+                        static_cast<char*>(out.data) + (p.start * out.token_stride + p.head * out.head_stride) * 2, k0, p.len,
+                        out.token_stride, a.dim);
     }
   };
-  next(0);
-  int now = 0;   // the present tile of its head
-  for (int n = 0; n < all; ++n) {
-    arrived();
-    if (n + 1 < all) next((n + 1) & 1);
-    const int i0 = (begin + now) * kStage + ib * 32;
-    if (++now == tiles) now = 0;
-    if (k0 >= p.len || i0 >= p.len || (a.causal && (i0 + 31 < k0 || i0 - (k0 + kWaveRows - 1) >= a.window))) continue;
-    MUON_LDS const char* buf = lds + (n & 1) * BUF;
-    step(!all_seen(a, 0x7fffffff, i0, i0 + 31, k0, k0 + kWaveRows - 1), buf, i0);
+  if constexpr (HALVES == 2) {
+    store(dk, half);
+  } else {
+    store(dk, 0);
+    store(dv, 1);
   }
-  // a pair of waves: the first one joins dK, the second one dV
-  arrived();
-  const float down = a.scale * cs.down;
-  MUON_LDS float* part = (MUON_LDS float*)(values + (kg * 2 + ib) * PART) + lane;
-#pragma unroll
-  for (int b = 0; b < TL::DB; ++b)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      dk[b][e] *= down;
-      part[(b * 16 + e) * 64] = ib == 0 ? dv[b][e] : dk[b][e];
-    }
-  __syncthreads();
-  const MUON_LDS float* other = (const MUON_LDS float*)(values + (kg * 2 + 1 - ib) * PART) + lane;
-#pragma unroll
-  for (int b = 0; b < TL::DB; ++b)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) dk[b][e] = (ib == 0 ? dk[b][e] : dv[b][e]) + other[(b * 16 + e) * 64];
-  __syncthreads();
-  const HeadsArg& out = ib == 0 ? a.dk : a.dv;
-  store_rows<T, DP>(dk, ib == 0 ? 1.0f : 1.0f / PUP, values + wave * kWaveRows * TL::PITCH,
-                    static_cast<char*>(out.data) + (p.start * out.token_stride + p.head * out.head_stride) * 2, k0, p.len,
-                    out.token_stride, a.dim);
 #endif
+}
+
+// The parts' sums in order, eight columns per thread. The sequences' tokens are one range.
+template <int DT>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
+  const int per = a.dim / 8;
+  const int64_t n = a.tokens * a.kv_heads * per, item = static_cast<int64_t>(flat_block()) * 256 + threadIdx.x;
+  if (item >= 2 * n) return;
+  const HeadsArg& out = item < n ? a.dk : a.dv;
+  const int64_t at = item < n ? item : item - n;
+  const int c = static_cast<int>(at % per) * 8, head = static_cast<int>(at / per % a.kv_heads);
+  const int64_t token = at / per / a.kv_heads;
+  if (a.list != nullptr) {
+    const int4 last = a.sequence_list[a.sequences - 1];
+    if (token < a.sequence_list[0].x || token >= last.x + last.y) return;
+  }
+  float v[8] = {};
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) {
+    float x[8];
+    read8<MUON_DTYPE_F32>(a.partial, 8 * (2 * p * n + item), 8, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += x[e];
+  }
+  write8<DT>(out.data, token * out.token_stride + head * out.head_stride + c, 8, v);
 }
 
 // ---------------------------------------------------------------------------
 
-#define MUON_ATTENTION(kernel, heads, threads)                                                          \
+#define MUON_ATTENTION(kernel, heads)                                                                   \
   do {                                                                                                  \
     const dim3 grid = flat_grid(static_cast<int64_t>(a.tiles) * (heads));                               \
     if (a.dtype == MUON_DTYPE_BF16) {                                                                   \
-      if (a.dim <= 64) hipLaunchKernelGGL((kernel<__bf16, 64>), grid, dim3(threads), 0, s, a);         \
-      else hipLaunchKernelGGL((kernel<__bf16, 128>), grid, dim3(threads), 0, s, a);                    \
+      if (a.dim <= 64) hipLaunchKernelGGL((kernel<__bf16, 64>), grid, dim3(kThreads), 0, s, a);         \
+      else hipLaunchKernelGGL((kernel<__bf16, 128>), grid, dim3(kThreads), 0, s, a);                    \
     } else {                                                                                            \
-      if (a.dim <= 64) hipLaunchKernelGGL((kernel<_Float16, 64>), grid, dim3(threads), 0, s, a);       \
-      else hipLaunchKernelGGL((kernel<_Float16, 128>), grid, dim3(threads), 0, s, a);                  \
+      if (a.dim <= 64) hipLaunchKernelGGL((kernel<_Float16, 64>), grid, dim3(kThreads), 0, s, a);       \
+      else hipLaunchKernelGGL((kernel<_Float16, 128>), grid, dim3(kThreads), 0, s, a);                  \
     }                                                                                                   \
     return hipGetLastError();                                                                           \
   } while (0)
@@ -845,8 +918,39 @@ hipError_t launch_attention_list(const AttentionArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(attention_list_kernel, dim3(1), dim3(kListThreads), 0, s, a);
   return hipGetLastError();
 }
-hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_kernel, a.heads, kThreads); }
-hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dq_kernel, a.heads, kThreads); }
-hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dkv_kernel, a.kv_heads, kKeyWaves * 64); }
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_kernel, a.heads); }
+hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dq_kernel, a.heads); }
+template <int HALVES>
+static hipError_t launch_dkv(const AttentionArgs& a, hipStream_t s) {
+  const dim3 grid = flat_grid(static_cast<int64_t>(a.tiles) * a.kv_heads * a.parts), block(kThreads * HALVES);
+  if (a.dtype == MUON_DTYPE_BF16) {
+    if (a.dim <= 64) hipLaunchKernelGGL((attention_dkv_kernel<__bf16, 64, HALVES>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_dkv_kernel<__bf16, 128, HALVES>), grid, block, 0, s, a);
+  } else {
+    if (a.dim <= 64) hipLaunchKernelGGL((attention_dkv_kernel<_Float16, 64, HALVES>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_dkv_kernel<_Float16, 128, HALVES>), grid, block, 0, s, a);
+  }
+  return hipGetLastError();
+}
+hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s) {
+  return a.halves == 2 ? launch_dkv<2>(a, s) : launch_dkv<1>(a, s);
+}
+hipError_t launch_attention_join(const AttentionArgs& a, hipStream_t s) {
+  const dim3 grid = flat_grid((a.tokens * a.kv_heads * (a.dim / 8) * 2 + 255) / 256);
+  if (a.dtype == MUON_DTYPE_BF16) hipLaunchKernelGGL((attention_join_kernel<MUON_DTYPE_BF16>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attention_join_kernel<MUON_DTYPE_F16>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// How dK and dV are shared out, by the number of key tiles (see the kernel): from 1024 on HALVES = 1,
+// below 2; parts where there are fewer than 256, one CU each, as many as give 512 workgroups, with
+// at least 512 rows to a part.
+void plan_attention_dkv(AttentionArgs& a) {
+  const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(a.tiles) * a.kv_heads);
+  a.halves = groups >= 1024 ? 1 : 2;
+  a.parts = 1;
+  if (groups < 256)
+    a.parts = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({32, (512 + groups - 1) / groups, a.tokens * a.group / 512})));
+}
 
 }  // namespace muon

@@ -26,6 +26,8 @@ struct AttentionArgs {
   int32_t sequences, tiles;    // tiles: of the list, or of the one sequence
   int32_t heads, kv_heads, group, dim;
   int32_t causal, window;      // window >= 1
+  int32_t halves, parts;       // see attention_dkv_kernel
+  float* partial;              // parts x (dK, dV) x tokens x kv_heads x dim, where parts > 1
   int32_t dtype;
   float scale;
 };
@@ -33,5 +35,7 @@ hipError_t launch_attention_list(const AttentionArgs& a, hipStream_t s);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);
 hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s);    // also lse2 and delta
 hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s);   // behind it
+void plan_attention_dkv(AttentionArgs& a);
+hipError_t launch_attention_join(const AttentionArgs& a, hipStream_t s);   // where there are several parts
 
 }  // namespace muon

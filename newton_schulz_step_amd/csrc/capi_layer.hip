@@ -321,6 +321,10 @@ static size_t attention_workspace(AttentionArgs& a, bool backward, char* base) {
     const size_t rows = static_cast<size_t>(a.tokens) * static_cast<size_t>(a.heads) * sizeof(float);
     a.lse2 = reinterpret_cast<float*>(take(rows));
     a.delta = reinterpret_cast<float*>(take(rows));
+    plan_attention_dkv(a);
+    if (a.parts > 1)
+      a.partial = reinterpret_cast<float*>(take(static_cast<size_t>(a.parts) * 2 * static_cast<size_t>(a.tokens) *
+                                                static_cast<size_t>(a.kv_heads) * static_cast<size_t>(a.dim) * sizeof(float)));
   }
   return at;
 }
@@ -678,7 +682,8 @@ int muon_attention_backward(const muon_attention_t* m, const muon_heads_t* d_o, 
     std::vector<Span> flat = {span_of(lse, T * H * 4, "lse")};
     if (m->offsets != nullptr) flat.push_back(span_of(m->offsets, (static_cast<int64_t>(m->sequences) + 1) * 4, "offsets"));
     if ((st = check_heads_apart(outs, ins, {span_of(workspace, static_cast<int64_t>(need), "workspace")}, flat)) != MUON_OK) return st;
-    if (static_cast<int64_t>(a.tiles) * H > 0x7fffffffLL) return fail(MUON_ERR_BAD_SHAPE, "too many tokens and heads for a launch");
+    if (static_cast<int64_t>(a.tiles) * H > 0x7fffffffLL || T * K * D > (int64_t(1) << 38))
+      return fail(MUON_ERR_BAD_SHAPE, "too many tokens and heads for a launch");
     attention_workspace(a, true, static_cast<char*>(workspace));
     a.q = heads_arg(q);
     a.k = heads_arg(k);
@@ -693,6 +698,7 @@ int muon_attention_backward(const muon_attention_t* m, const muon_heads_t* d_o, 
     if (a.list != nullptr) MUON_LAUNCH("attention_list", s, launch_attention_list(a, s));
     MUON_LAUNCH("attention_dq", s, launch_attention_dq(a, s));
     MUON_LAUNCH("attention_dkv", s, launch_attention_dkv(a, s));
+    if (a.parts > 1) MUON_LAUNCH("attention_join", s, launch_attention_join(a, s));
     return MUON_OK;
   });
 }
