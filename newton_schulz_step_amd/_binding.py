@@ -7,6 +7,7 @@ if the library is missing.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import operator
@@ -216,7 +217,7 @@ def load() -> ctypes.CDLL:
         lib.muon_embedding.argtypes = [pe, vp, vp, i32, i64, vp]
         lib.muon_embedding_backward.argtypes = [pe, vp, i32, i64, vp, i32, vp, sz, vp]
         lib.muon_embedding_backward_workspace_size.argtypes = [pe, psz]
-        lib.muon_grad_sumsq.argtypes = [vp, i32, i32, vp, vp, sz, vp]   # the tensors as a c_int64 array
+        lib.muon_grad_sumsq.argtypes = [vp, i32, i32, vp, vp, sz, vp]   # the tensors by address
         lib.muon_grad_sumsq_workspace_size.argtypes = [vp, i32, psz]
         lib.muon_grad_clip.argtypes = [vp, vp, i32, vp, ctypes.c_float, vp, vp]
         pa, ph3 = ctypes.POINTER(AttentionRows), ctypes.POINTER(Heads)
@@ -303,11 +304,14 @@ def _torch():
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if t.dtype not in m:
+    global _TORCH_DT
+    if _TORCH_DT is None:
+        torch = _torch()
+        _TORCH_DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _TORCH_DT.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported tensor dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _ptr(t) -> Optional[int]:
@@ -1188,36 +1192,41 @@ def embedding_backward(dy, ids, vocab: int, scale: float = 1.0, out=None, out_dt
     return out
 
 
-_CLIP_CODES = None
+_TENSOR_CALLS = None
 
 
 def _tensor_list(tensors, name):
-    """muon_tensor_t records of contiguous tensors on one GPU, as a c_int64 array of three per
-    tensor, their number, and the GPU's index."""
-    global _CLIP_CODES
-    if _CLIP_CODES is None:
+    """muon_tensor_t records of contiguous tensors on one GPU, as an array of three 64-bit words
+    per tensor, their number, and the GPU's index. Steps with many tensors spend their time
+    here, so attributes are fetched by one call each."""
+    global _TENSOR_CALLS
+    if _TENSOR_CALLS is None:
         torch = _torch()
-        _CLIP_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    codes, flat, dev = _CLIP_CODES, [], None
-    for t in tensors:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        d = t.get_device()
-        if d != dev:
-            if dev is not None or d < 0:
-                raise ValueError(f"{name} must share one GPU")
-            dev = d
-        if t.dtype not in codes:
-            raise TypeError(f"unsupported tensor dtype {t.dtype}")
-        flat += (t.data_ptr(), t.numel(), codes[t.dtype])
-    return (ctypes.c_int64 * max(len(flat), 1))(*flat), len(flat) // 3, dev
+        t = torch.Tensor
+        _TENSOR_CALLS = (t.is_contiguous, t.get_device, t.data_ptr, t.numel, operator.attrgetter("dtype"),
+                         {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    contiguous, device, pointer, numel, dtype, codes = _TENSOR_CALLS
+    if not all(map(contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    devices = set(map(device, tensors))
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError(f"{name} must share one GPU")
+    words = array.array("q", bytes(24 * len(tensors)))
+    words[0::3] = array.array("q", map(pointer, tensors))
+    words[1::3] = array.array("q", map(numel, tensors))
+    try:
+        words[2::3] = array.array("q", map(codes.__getitem__, map(dtype, tensors)))
+    except KeyError as e:
+        raise TypeError(f"unsupported tensor dtype {e.args[0]}") from None
+    return words, len(tensors), devices.pop() if devices else None
 
 
 def _sumsq(arr, n, sumsq, accumulate, ws, on):
     need = ctypes.c_size_t(0)
-    _check(load().muon_grad_sumsq_workspace_size(arr, n, ctypes.byref(need)))
+    at = arr.buffer_info()[0]
+    _check(load().muon_grad_sumsq_workspace_size(at, n, ctypes.byref(need)))
     ws = on.scratch(need.value, ws)
-    _check(load().muon_grad_sumsq(arr, n, int(bool(accumulate)), _flat(sumsq), _flat(ws),
+    _check(load().muon_grad_sumsq(at, n, int(bool(accumulate)), _flat(sumsq), _flat(ws),
                                   0 if ws is None else ws.numel() * ws.element_size(), on.handle))
 
 
@@ -1227,6 +1236,7 @@ def grad_sumsq(grads: Sequence, out=None, accumulate: bool = False, ws=None, str
     types. accumulate adds to out. Ranks with different shards add up their sums and pass the
     total to clip_gradients."""
     torch = _torch()
+    grads = list(grads)
     arr, n, index = _tensor_list(grads, "grads")
     if n == 0:
         raise ValueError("grad_sumsq needs at least one tensor")
@@ -1247,12 +1257,13 @@ def clip_gradients(grads: Sequence, max_norm: float, sumsq=None, out: Optional[S
     dimensions. sumsq: the float64 sum of squares to go by, where it is not that of these
     tensors alone (other ranks' shards)."""
     torch = _torch()
+    grads = list(grads)
     arr, n, index = _tensor_list(grads, "grads")
     if n == 0:
         raise ValueError("clip_gradients needs at least one tensor")
     outs = arr
     if out is not None:
-        outs, m, other = _tensor_list(out, "out")
+        outs, m, other = _tensor_list(list(out), "out")
         if m != n:
             raise ValueError(f"{m} outputs for {n} tensors")
         if other != index:
@@ -1265,7 +1276,8 @@ def clip_gradients(grads: Sequence, max_norm: float, sumsq=None, out: Optional[S
         else:
             sumsq = _given(sumsq, (), torch.float64, on, "sumsq")
         norm = _given(norm, (), torch.float32, on, "norm")
-        _check(load().muon_grad_clip(arr, outs, n, _flat(sumsq), max_norm, _flat(norm), on.handle))
+        _check(load().muon_grad_clip(arr.buffer_info()[0], outs.buffer_info()[0], n, _flat(sumsq), max_norm, _flat(norm),
+                                     on.handle))
     return norm
 
 

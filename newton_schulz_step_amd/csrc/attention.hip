@@ -240,18 +240,22 @@ __device__ __forceinline__ Place place_of(const AttentionArgs& a, int heads, boo
   return p;
 }
 
-// A workgroup of the list: prefix sums over the sequences' tiles, then the tiles by work.
-constexpr int kListThreads = 1024, kListClasses = 256;
+// The list, by one workgroup: prefix sums over the sequences' tiles, then the tiles by work. The first
+// 1024 sequences stay in LDS, where bisection looks for a tile's; the sequences go to memory too,
+// for the join and for bisection among more of them.
+constexpr int kListThreads = 1024, kListWaves = kListThreads / 64, kListClasses = 256;
 
 __global__ __launch_bounds__(kListThreads) void attention_list_kernel(AttentionArgs a) {
-  __shared__ int wave_top[kListThreads / 64], wave_sum_[kListThreads / 64];
+  __shared__ int wave_top[kListWaves], wave_sum[kListWaves];
   __shared__ int count[kListClasses];
+  __shared__ int4 near[kListThreads];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int tokens = static_cast<int>(a.tokens);
   int top = min(max(a.offsets[0], 0), tokens), tiles = 0;   // of the sequences so far
   if (t < kListClasses) count[t] = 0;
   for (int s0 = 0; s0 < a.sequences; s0 += kListThreads) {
     const int s = s0 + t;
+    const int waves = min(kListWaves, (a.sequences - s0 + 63) / 64);   // that have sequences
     // an offset that falls counts as the largest before it
     int end = s < a.sequences ? min(max(a.offsets[s + 1], 0), tokens) : 0;
     int incl = end;
@@ -263,7 +267,7 @@ __global__ __launch_bounds__(kListThreads) void attention_list_kernel(AttentionA
     if (lane == 63) wave_top[wave] = incl;
     __syncthreads();
     int before = top, all = top;
-    for (int w = 0; w < kListThreads / 64; ++w) {
+    for (int w = 0; w < waves; ++w) {
       if (w < wave) before = max(before, wave_top[w]);
       all = max(all, wave_top[w]);
     }
@@ -277,14 +281,18 @@ __global__ __launch_bounds__(kListThreads) void attention_list_kernel(AttentionA
       const int up = __shfl_up(sum, o, 64);
       if (lane >= o) sum += up;
     }
-    if (lane == 63) wave_sum_[wave] = sum;
+    if (lane == 63) wave_sum[wave] = sum;
     __syncthreads();
     int first = tiles + sum - n, total = tiles;
-    for (int w = 0; w < kListThreads / 64; ++w) {
-      if (w < wave) first += wave_sum_[w];
-      total += wave_sum_[w];
+    for (int w = 0; w < waves; ++w) {
+      if (w < wave) first += wave_sum[w];
+      total += wave_sum[w];
     }
-    if (s < a.sequences) a.sequence_list[s] = int4{start, end - start, first, 0};
+    if (s < a.sequences) {
+      const int4 e{start, end - start, first, 0};
+      a.sequence_list[s] = e;
+      if (s0 == 0) near[t] = e;
+    }
     top = all;
     tiles = total;
     __syncthreads();
@@ -292,22 +300,29 @@ __global__ __launch_bounds__(kListThreads) void attention_list_kernel(AttentionA
   __threadfence_block();
   __syncthreads();
   // each tile's sequence by bisection, its work in classes
+  const bool few = a.sequences <= kListThreads;
   auto tile_of = [&](int x, int& cls) {
     int lo = 0, hi = a.sequences - 1;   // the last sequence that begins at or before tile x and has tiles
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.sequence_list[mid].z <= x) lo = mid;
+      if ((few ? near[mid].z : a.sequence_list[mid].z) <= x) lo = mid;
       else hi = mid - 1;
     }
-    const int4 s = a.sequence_list[lo];
+    const int4 s = few ? near[lo] : a.sequence_list[lo];
     const int tile = x - s.z;
     const int64_t keys = a.causal ? min<int64_t>((tile + 1) * static_cast<int64_t>(kAttentionRows), a.window + kAttentionRows) : s.y;
     cls = kListClasses - 1 - static_cast<int>(min<int64_t>(kListClasses - 1, keys * kListClasses / (a.tokens + kAttentionRows)));
     return int4{s.x, s.y, tile, 0};
   };
+  int4 own{};   // the thread's first tile
+  int own_class = 0;
   for (int x = t; x < tiles; x += kListThreads) {
     int cls;
-    tile_of(x, cls);
+    const int4 e = tile_of(x, cls);
+    if (x == t) {
+      own = e;
+      own_class = cls;
+    }
     atomicAdd(&count[cls], 1);
   }
   __syncthreads();
@@ -328,8 +343,9 @@ __global__ __launch_bounds__(kListThreads) void attention_list_kernel(AttentionA
   __syncthreads();
   // the order within a class does not matter: every tile has its own results
   for (int x = t; x < tiles; x += kListThreads) {
-    int cls;
-    const int4 e = tile_of(x, cls);
+    int cls = own_class;
+    int4 e = own;
+    if (x != t) e = tile_of(x, cls);
     a.list[atomicAdd(&count[cls], 1)] = e;
   }
   for (int x = tiles + t; x < a.tiles; x += kListThreads) a.list[x] = int4{0, 0, 0, 0};

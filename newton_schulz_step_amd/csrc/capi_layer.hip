@@ -115,6 +115,7 @@ static EmbeddingArgs embedding_args(const muon_embedding_t* e) {
   a.bits = (bits + a.passes - 1) / a.passes;
   a.blocks = sort_blocks(e->tokens);
   a.per_block = (e->tokens + a.blocks - 1) / a.blocks;
+  a.chunk = e->tokens <= 4096 ? 8 : 32;
   return a;
 }
 
@@ -133,7 +134,7 @@ static size_t embedding_workspace(EmbeddingArgs& a, char* base) {
   }
   a.hist = reinterpret_cast<int32_t*>(take(a.blocks > 1 ? static_cast<size_t>(a.blocks) * kSortBins * 4 : 0));
   a.touched = reinterpret_cast<uint8_t*>(take(static_cast<size_t>(a.vocab)));
-  const size_t chunks = static_cast<size_t>((a.tokens + kEmbeddingChunk - 1) / kEmbeddingChunk);
+  const size_t chunks = static_cast<size_t>((a.tokens + a.chunk - 1) / a.chunk);
   a.partial = reinterpret_cast<float*>(take(2 * chunks * static_cast<size_t>(a.cols) * 4));
   return at;
 }
@@ -493,7 +494,7 @@ int muon_embedding_backward(const muon_embedding_t* e, const void* dy, int32_t d
                             {matrix_span(dy, dtype, e->tokens, e->cols, ld_dy, "dy"),
                              span_of(e->ids, e->tokens * e->id_bytes, "ids")})) != MUON_OK)
       return st;
-    const int64_t chunks = (e->tokens + kEmbeddingChunk - 1) / kEmbeddingChunk;
+    const int64_t chunks = (e->tokens + a.chunk - 1) / a.chunk;
     if (chunks * ((e->cols + 511) / 512) + e->vocab > 0x7fffffffLL)
       return fail(MUON_ERR_BAD_SHAPE, "too many tokens and columns for a launch");
     embedding_workspace(a, static_cast<char*>(workspace));

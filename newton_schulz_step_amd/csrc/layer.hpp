@@ -54,9 +54,9 @@ struct EmbeddingArgs {
   int64_t per_block;
   uint8_t* touched;          // a byte per row of the table (NULL: not wanted)
   float* partial;            // 2 per chunk x cols
+  int32_t chunk;             // sorted tokens that one wave sums: 8 or 32
 };
 constexpr int kSortBins = 256;
-constexpr int kEmbeddingChunk = 32;   // sorted tokens that one wave sums
 int32_t sort_blocks(int64_t n);
 hipError_t launch_embedding(int dtype, const EmbeddingArgs& a, hipStream_t s);
 // One block: the whole sort. Several: a pass's counts, then its placing.

@@ -24,6 +24,12 @@ template <int XT> struct Raw8 {
       for (int e = 0; e < 8; ++e) u[e] = e < n ? p[e] : static_cast<unsigned short>(0);
     }
   }
+  // the same for what is read once: past the caches (norm of 8192 x 4096 bf16 rows: 46 -> 41 us; fp32 the same
+  // either way)
+  __device__ __forceinline__ void load_once(const void* x, int64_t i, int n) {
+    if (n >= 8) u = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(static_cast<const unsigned short*>(x) + i));
+    else load(x, i, n);
+  }
   __device__ __forceinline__ float get(int e) const {
     return XT == MUON_DTYPE_BF16 ? bf16_bits_to_f32(u[e]) : f16_bits_to_f32(u[e]);
   }
@@ -45,6 +51,7 @@ template <> struct Raw8<MUON_DTYPE_F32> {
       }
     }
   }
+  __device__ __forceinline__ void load_once(const void* x, int64_t i, int n) { load(x, i, n); }
   __device__ __forceinline__ float get(int e) const { return e < 4 ? a[e] : b[e - 4]; }
   __device__ __forceinline__ void fresh() {}
 };
