@@ -124,6 +124,53 @@ def test_forward_and_gradient(lib, lens, dim, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [40, 64, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 40)])
+def test_many_key_tiles(lib, causal, window, dim, dtype):
+    """From 1024 key tiles on dK and dV take workgroups of four waves, without parts."""
+    lens = [1] * 60 + [130, 0, 33, 64, 200]
+    off, hoff = offsets_of(lens), np.cumsum([0] + lens)
+    q, k, v, do = make(dim, sum(lens), 32, 16, dim, dtype, loud=2.0)
+    assert (sum(lens) // 128 + len(lens)) * 16 >= 1024
+    how = dict(causal=causal, window=window)
+    out, lse = lib.attention(q, k, v, offsets=off, **how)
+    check_forward(q, k, v, out, lse, dtype, offsets=hoff, **how)
+    got = lib.attention_backward(do, q, k, v, out, lse, offsets=off, **how)
+    check_backward(do, q, k, v, out, got, dtype, offsets=hoff, **how)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_parts_of_few_key_tiles(lib, dtype):
+    """Few key tiles: their queries are summed in parts, some of which hold no row that sees a key."""
+    for tokens, heads, kv, how in ((1300, 8, 1, {}), (600, 16, 1, dict(window=70)), (520, 4, 2, dict(causal=False))):
+        q, k, v, do = make(tokens, tokens, heads, kv, 64, dtype)
+        out, lse = lib.attention(q, k, v, **how)
+        check_backward(do, q, k, v, out, lib.attention_backward(do, q, k, v, out, lse, **how), dtype, **how)
+
+
+def test_far_offsets(lib):
+    """Elements beyond 2^31 of one tensor."""
+    import torch
+    stride = 1 << 22
+    base = torch.empty(700 * stride, dtype=torch.bfloat16, device="cuda")   # 5.9 GB
+    q, k, v, do = make(5, 700, 2, 2, 64, "bf16")
+
+    def far(x, at):
+        t = base.as_strided(x.shape, (stride, 64, 1), at)
+        t.copy_(x)
+        return t
+    out, lse = lib.attention(q, k, v)
+    want = lib.attention_backward(do, q, k, v, out, lse)
+    fo = base.as_strided(q.shape, (stride, 64, 1), 4096)
+    fq, fk, fv, fdo = (far(x, 512 * i) for i, x in enumerate((q, k, v, do)))
+    _, flse = lib.attention(fq, fk, fv, out=fo)
+    assert torch.equal(fo, out) and torch.equal(flse, lse)
+    grads = [base.as_strided(q.shape, (stride, 64, 1), 8192 + 512 * i) for i in range(3)]
+    lib.attention_backward(fdo, fq, fk, fv, fo, flse, dq=grads[0], dk=grads[1], dv=grads[2])
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 200, 5000])
 def test_windows(lib, window, dtype):
     q, k, v, do = make(window, 450, 2, 2, 64, dtype)

@@ -353,6 +353,34 @@ def test_clip_into_the_packed_gradients_and_by_shards(lib):
     assert (packed[64 * 48:64 * 48 + 64] == 7).all()
 
 
+# ----------------------------------------------------------------------------- far offsets
+
+def test_elements_beyond_2_31(lib):
+    import torch
+    rows, ld = 40, 1 << 26   # 5.4 GB of bf16
+    base, other, third = (torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    x = torch.randn(rows, 300, device="cuda").bfloat16()
+    view = base.as_strided((rows, 300), (ld, 1), 8)
+    view.copy_(x)
+    out = other.as_strided((rows, 300), (ld, 1), 4096)
+    want = lib.rms_norm(x)
+    assert torch.equal(lib.rms_norm(view, out=out).y, want.y)
+    dx = third.as_strided((rows, 300), (ld, 1), 8192)
+    assert torch.equal(lib.rms_norm_backward(out, view, None, want.rstd, dx=dx)[0],
+                       lib.rms_norm_backward(want.y, x, None, want.rstd)[0])
+    ids = torch.randint(0, rows, (500,), device="cuda")
+    assert torch.equal(lib.embedding(ids, view), lib.embedding(ids, x))
+    dy = torch.randn(500, 300, device="cuda").bfloat16()
+    table = third.as_strided((rows, 300), (ld, 1), 12288)
+    assert torch.equal(lib.embedding_backward(dy, ids, rows, out=table), lib.embedding_backward(dy, ids, rows, out_dtype=torch.bfloat16))
+    base.zero_()
+    base[::1 << 20] = 2.0   # 2560 of 2.7e9 elements
+    n = base[::1 << 20].numel()
+    norm = lib.clip_gradients([base[:-3]], 1.0)
+    assert norm.item() == np.float32(2.0 * np.sqrt(n))
+    assert torch.equal(base[::1 << 20], torch.full((n,), 2.0, device="cuda").mul_(1.0 / norm.double()).bfloat16())
+
+
 # ----------------------------------------------------------------------------- streams, graphs
 
 def operators(lib):
@@ -376,12 +404,44 @@ def operators(lib):
     def clip():
         outs = [torch.empty_like(t) for t in grads]
         return [lib.clip_gradients(grads, 3.0, out=outs)] + outs
-    return {"norm": norm, "norm gradient": lambda: lib.rms_norm_backward(dy, x, w, rstd, dsum=r),
+    q, k = n(500, 8, 64).bfloat16(), n(500, 2, 64).bfloat16()
+    off = torch.tensor([0, 120, 500], dtype=torch.int32, device="cuda")
+    o, lse = lib.attention(q, k, k, offsets=off)
+    return {"attention": lambda: lib.attention(q, k, k, offsets=off),
+            "attention gradient": lambda: lib.attention_backward(o, q, k, k, o, lse, offsets=off),
+            "norm": norm, "norm gradient": lambda: lib.rms_norm_backward(dy, x, w, rstd, dsum=r),
             "embedding": lambda: [lib.embedding(ids, table, scale=2.0)],
             "embedding gradient": lambda: [lib.embedding_backward(de, ids, 700)], "clip": clip}
 
 
-NAMES = ["norm", "norm gradient", "embedding", "embedding gradient", "clip"]
+def test_three_threads_at_once(lib):
+    """Threads on one stream and on streams of their own: no call sees another one's workspace."""
+    import threading
+
+    import torch
+    runs = operators(lib)
+    want = {n: [t.clone() for t in f()] for n, f in runs.items()}
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(own):
+        stream = torch.cuda.Stream() if own else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                for n, f in runs.items():
+                    got = f()
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[n])):
+                        bad.append(n)
+    threads = [threading.Thread(target=work, args=(i == 2,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
+NAMES = ["norm", "norm gradient", "embedding", "embedding gradient", "clip", "attention", "attention gradient"]
 
 
 @pytest.mark.parametrize("name", NAMES)
