@@ -675,7 +675,7 @@ int muon_grad_sumsq_workspace_size(const muon_tensor_t* grads, int32_t n, size_t
 /* Scale n tensors by the norm that *sumsq (device) stands for:
  *   norm = sqrt(*sumsq);  factor = min(1, max_norm / (norm + 1e-6)), in 64 bits;
  *   outs[i] = grads[i] * factor (the factor and the product in fp32), rounded to
- *   outs[i]'s type.
+ *   outs[i]'s type. With max_norm infinite the factor is 1, whatever the norm.
  * outs: n tensors of the same numels, of any of the types: NULL or the same
  * memory and type for scaling in place (not written where the factor is 1), or
  * others, such as the entries of a packed gradient buffer. norm: device
@@ -692,6 +692,7 @@ int muon_grad_clip(const muon_tensor_t* grads, const muon_tensor_t* outs, int32_
 #define MUON_ATTENTION_MAX_TOKENS (1 << 30)
 #define MUON_ATTENTION_MAX_HEADS 1024
 #define MUON_ATTENTION_MAX_DIM 128
+#define MUON_ATTENTION_MAX_SCALE 1e30f
 
 /* Heads of all tokens, 16-bit elements: element (token, head, column) at
  * data + token * token_stride + head * head_stride + column (strides in
@@ -720,7 +721,7 @@ typedef struct {
   int32_t dtype;          /* BF16 | F16, of all operands */
   int32_t causal;
   int32_t window;
-  float scale;            /* > 0, of the scores */
+  float scale;            /* of the scores, in (0, MUON_ATTENTION_MAX_SCALE] */
 } muon_attention_t;
 
 /* o = softmax(scale * q k^T) v per sequence and head; scores, their softmax and
@@ -728,8 +729,8 @@ typedef struct {
  *   lse  device float32[heads x tokens] or NULL: the natural logarithm of each
  *        row's sum of exponentials, for the gradient.
  * Tokens outside every sequence are not read, and their rows of o and lse are not
- * written. Values must be finite: one that is not can reach every row of its
- * own sequence (never another sequence).
+ * written. Values and scores (times scale, times log2(e)) must be finite in fp32:
+ * one that is not can reach every row of its own sequence (never another sequence).
  *   workspace  device, muon_attention_workspace_size(a, 0) bytes, 16-byte
  *              aligned (NULL where that is 0: without offsets).
  * Errors: MUON_ERR_NULL, BAD_SHAPE, UNSUPPORTED (dtype, a window without causal),
@@ -744,8 +745,8 @@ int muon_attention(const muon_attention_t* a, const muon_heads_t* q, const muon_
  * dk and dv summed over the query heads that share them. P and dS are rounded to
  * dtype for their products (in F16 under powers of two that keep them in its
  * range), all sums are in fp32 in an order that the sizes alone decide. dq, dk
- * and dv may be interleaved, as the parts of one gradient of a joint projection
- * are. Workspace: muon_attention_workspace_size(a, 1). */
+ * and dv may be interleaved by token or by head, as the parts of one gradient of
+ * a joint projection are. Workspace: muon_attention_workspace_size(a, 1). */
 int muon_attention_backward(const muon_attention_t* a, const muon_heads_t* d_o, const muon_heads_t* q,
                             const muon_heads_t* k, const muon_heads_t* v, const muon_heads_t* o, const float* lse,
                             const muon_heads_t* dq, const muon_heads_t* dk, const muon_heads_t* dv, void* workspace,

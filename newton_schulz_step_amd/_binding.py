@@ -1252,8 +1252,8 @@ def grad_sumsq(grads: Sequence, out=None, accumulate: bool = False, ws=None, str
 def clip_gradients(grads: Sequence, max_norm: float, sumsq=None, out: Optional[Sequence] = None, norm=None, ws=None,
                    stream=None):
     """Scale the tensors by min(1, max_norm / (norm + 1e-6)) of their global norm
-    (muon_grad_clip), in place or into `out`: as many tensors of the same sizes, of any
-    types, such as views of the packed gradient buffer. Returns the norm: float32, no
+    (muon_grad_clip; 1 where max_norm is infinite), in place or into `out`: as many tensors of
+    the same sizes, of any types, such as views of the packed gradient buffer. Returns the norm: float32, no
     dimensions. sumsq: the float64 sum of squares to go by, where it is not that of these
     tensors alone (other ranks' shards)."""
     torch = _torch()

@@ -218,7 +218,8 @@ static int check_attention(const muon_attention_t* a) {
   if (a->dtype != MUON_DTYPE_BF16 && a->dtype != MUON_DTYPE_F16) return fail(MUON_ERR_UNSUPPORTED, "attention: dtype must be BF16 or F16");
   if (a->window < 0) return fail(MUON_ERR_BAD_SHAPE, "window must not be negative");
   if (a->window > 0 && !a->causal) return fail(MUON_ERR_UNSUPPORTED, "a window needs causal");
-  if (!std::isfinite(a->scale) || !(a->scale > 0.0f)) return fail(MUON_ERR_BAD_HYPER, "scale must be finite and greater than 0");
+  if (!(a->scale > 0.0f) || !(a->scale <= MUON_ATTENTION_MAX_SCALE))
+    return fail(MUON_ERR_BAD_HYPER, "scale must lie in (0, MUON_ATTENTION_MAX_SCALE]");
   if (misaligned(a->offsets, 4)) return fail(MUON_ERR_ALIGN, "offsets is not 4-byte aligned");
   return MUON_OK;
 }
@@ -236,11 +237,17 @@ struct HeadsSpan {
 
 static bool heads_meet(const HeadsSpan& a, const HeadsSpan& b) {
   if (!(a.lo() < b.hi() && b.lo() < a.hi())) return false;
-  // parts of the same rows, such as those of a joint projection
-  const int64_t pitch = a.t->token_stride;
-  if (b.t->token_stride != pitch || a.width() > pitch || b.width() > pitch || (b.lo() - a.lo()) % 2 != 0) return true;
-  const int64_t d = (((b.lo() - a.lo()) / 2) % pitch + pitch) % pitch;
-  return !(d >= a.width() && d + b.width() <= pitch);
+  // parts of the same rows, such as those of a joint projection: of a token's, or of each head's
+  const int64_t pitch = a.t->token_stride, head = a.t->head_stride, by = (b.lo() - a.lo()) / 2;
+  const bool one = a.tokens == 1;   // whose pitch does not matter
+  if ((!one && b.t->token_stride != pitch) || (b.lo() - a.lo()) % 2 != 0) return true;
+  auto apart = [&](int64_t wa, int64_t wb, int64_t every) {   // runs of wa and of wb elements, each once in `every`
+    const int64_t d = (by % every + every) % every;
+    return wa <= every && wb <= every && d >= wa && d + wb <= every;
+  };
+  if (!one && apart(a.width(), b.width(), pitch)) return false;
+  return !(a.heads > 1 && b.heads > 1 && b.t->head_stride == head && head > 0 && (one || pitch % head == 0) &&
+           apart(a.dim, b.dim, head));
 }
 
 static int check_heads(const HeadsSpan& x, bool output) {
@@ -683,7 +690,7 @@ int muon_attention_backward(const muon_attention_t* m, const muon_heads_t* d_o, 
     std::vector<Span> flat = {span_of(lse, T * H * 4, "lse")};
     if (m->offsets != nullptr) flat.push_back(span_of(m->offsets, (static_cast<int64_t>(m->sequences) + 1) * 4, "offsets"));
     if ((st = check_heads_apart(outs, ins, {span_of(workspace, static_cast<int64_t>(need), "workspace")}, flat)) != MUON_OK) return st;
-    if (static_cast<int64_t>(a.tiles) * H > 0x7fffffffLL || T * K * D > (int64_t(1) << 38))
+    if (static_cast<int64_t>(a.tiles) * H > 0x7fffffffLL || T * H > (int64_t(1) << 36) || T * K * D > (int64_t(1) << 38))
       return fail(MUON_ERR_BAD_SHAPE, "too many tokens and heads for a launch");
     attention_workspace(a, true, static_cast<char*>(workspace));
     a.q = heads_arg(q);

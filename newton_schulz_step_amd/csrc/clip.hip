@@ -109,7 +109,8 @@ __device__ __forceinline__ void scale_to(int dtype, const void* p, void* o, int6
 __global__ __launch_bounds__(kClipThreads) void grad_clip_kernel(ClipArgs a) {
   const double norm = sqrt(*a.sumsq);
   const double ratio = static_cast<double>(a.max_norm) / (norm + 1e-6);
-  const float factor = static_cast<float>(ratio > 1.0 ? 1.0 : ratio);   // NaN stays
+  const bool never = a.max_norm == __builtin_huge_valf();
+  const float factor = static_cast<float>(ratio > 1.0 || never ? 1.0 : ratio);   // NaN stays
   if (a.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = static_cast<float>(norm);
   // last chunks first: those that the norm read last may still lie in the last-level cache
   const int b = static_cast<int>(gridDim.x - 1 - blockIdx.x);

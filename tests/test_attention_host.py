@@ -54,7 +54,7 @@ def test_refusals_of_both(lib, call):
         assert call(lib, rows(**bad)) == nss.ERR_BAD_SHAPE, bad
     for bad in (dict(dtype=0), dict(dtype=3), dict(causal=0, window=5)):
         assert call(lib, rows(**bad)) == nss.ERR_UNSUPPORTED, bad
-    for scale in (0.0, -1.0, float("nan"), float("inf")):
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert call(lib, rows(scale=scale)) == nss.ERR_BAD_HYPER
     assert call(lib, rows(offsets=at(9) + 2, sequences=3)) == nss.ERR_ALIGN
     for n in ("q", "k", "v", "o"):
@@ -102,6 +102,20 @@ def test_overlaps(lib):
     assert backward(lib, dq=heads(6, **part[0]), dk=heads(6, **part[1]), dv=heads(6, **part[3])) == nss.ERR_OVERLAP
     other = heads(6, ts=776, data=at(6) + 2 * 512)                                # another pitch
     assert backward(lib, dq=heads(6, **part[0]), dk=other) == nss.ERR_OVERLAP
+
+
+def test_overlaps_of_parts_of_heads(lib):
+    """dq, dk, dv of every head next to each other; a column too near, a pitch that is no multiple of the heads', heads
+    at other distances: refused."""
+    def call(dk=64, dv=128, ts=8 * 192, hs=(192, 192, 192), tokens=100):
+        part = [B.Heads(at(6) + 2 * c, ts, h) for c, h in zip((0, dk, dv), hs)]
+        return backward(lib, rows(kv_heads=8, tokens=tokens), dq=part[0], dk=part[1], dv=part[2], ws=at(6))
+    # where they are apart, the workspace, which begins at dq, is what is refused
+    for good in (dict(), dict(tokens=1), dict(tokens=1, ts=64)):
+        assert call(**good) == nss.ERR_OVERLAP and b"workspace" in lib.muon_last_error(), good
+    for bad in (dict(dk=56), dict(dv=136), dict(dv=64), dict(ts=8 * 192 + 8), dict(hs=(192, 192, 200), ts=8 * 200),
+                dict(tokens=1, dk=56)):
+        assert call(**bad) == nss.ERR_OVERLAP and b"workspace" not in lib.muon_last_error(), bad
 
 
 def test_binding_refusals():

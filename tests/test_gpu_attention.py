@@ -243,6 +243,23 @@ def test_layouts_and_rows_outside(lib):
     assert torch.equal(lib.attention(q, wide, v)[0], lib.attention(q, wide.contiguous(), v)[0])
 
 
+@pytest.mark.parametrize("T", [1, 77])
+def test_joint_projection_by_head(lib, T):
+    """q, k and v of every head next to each other, and so their gradients."""
+    import torch
+    H, D = 8, 64
+    q, k, v, do = make(8, T, H, H, D, "bf16")
+    out, lse = lib.attention(q, k, v)
+    grads = lib.attention_backward(do, q, k, v, out, lse)
+    joint = torch.stack((q, k, v), dim=2)   # [T, H, 3, D]
+    parts = [joint[:, :, i] for i in range(3)]
+    assert all(torch.equal(x, y) for x, y in zip(lib.attention(*parts), (out, lse)))
+    djoint = torch.full_like(joint, 5.0)
+    lib.attention_backward(do, *parts, out, lse, dq=djoint[:, :, 0], dk=djoint[:, :, 1], dv=djoint[:, :, 2])
+    for i in range(3):
+        assert torch.equal(djoint[:, :, i], grads[i])
+
+
 def test_offsets_out_of_order_and_range(lib):
     import torch
     q, k, v, do = make(6, 260, 2, 2, 64, "bf16")

@@ -338,6 +338,21 @@ def test_clip_norms_that_are_not_finite(lib):
     assert np.isnan(lib.clip_gradients(h, 1.0).item()) and torch.isnan(h[1]).all()
 
 
+def test_clip_without_limit(lib):
+    """An infinite max_norm leaves every value as it is, and still gives the norm; zero leaves zeros."""
+    import torch
+    for bad in (3.0, float("inf"), float("nan")):
+        g = torch.ones(5000, device="cuda")
+        g[77] = bad
+        out = torch.zeros(5000, device="cuda")
+        assert np.array_equal(lib.clip_gradients([g], float("inf"), out=[out]).item(), np.sqrt(host(g).__pow__(2).sum()).astype(np.float32),
+                              equal_nan=True)
+        assert np.array_equal(host(out), host(g), equal_nan=True)
+    g = torch.ones(5000, device="cuda")
+    lib.clip_gradients([g], 0.0)
+    assert (g == 0).all()
+
+
 def test_clip_into_the_packed_gradients_and_by_shards(lib):
     import torch
     rng = np.random.default_rng(2)
