@@ -732,7 +732,8 @@ typedef struct {
  * written. Values and scores (times scale, times log2(e)) must be finite in fp32:
  * one that is not can reach every row of its own sequence (never another sequence).
  *   workspace  device, muon_attention_workspace_size(a, 0) bytes, 16-byte
- *              aligned (NULL where that is 0: without offsets).
+ *              aligned (NULL where that is 0: without offsets, or with few
+ *              sequences).
  * Errors: MUON_ERR_NULL, BAD_SHAPE, UNSUPPORTED (dtype, a window without causal),
  * ALIGN, OVERLAP, BAD_HYPER (scale), WORKSPACE. */
 int muon_attention(const muon_attention_t* a, const muon_heads_t* q, const muon_heads_t* k, const muon_heads_t* v,

@@ -7,6 +7,7 @@
 namespace muon {
 
 constexpr int kAttentionRows = 128;   // queries, or keys, of a workgroup
+constexpr int kAttentionFew = 64;     // sequences, one per lane
 
 // Element (token, head, column) at data + token * token_stride + head * head_stride + column.
 struct HeadsArg {
@@ -22,9 +23,10 @@ struct AttentionArgs {
   int64_t tokens;
   const int32_t* offsets;      // NULL: one sequence
   int4* sequence_list;         // per sequence: first token, tokens, first tile
-  int4* list;                  // per tile: first token, tokens, tile; NULL: one sequence
+  int4* list;                  // per tile: first token, tokens, tile; NULL: one sequence, or few
   int32_t sequences, tiles;    // tiles: of the list, or of the one sequence
   int32_t heads, kv_heads, group, dim;
+  int32_t few;                 // up to kAttentionFew sequences: no list
   int32_t causal, window;      // window >= 1
   int32_t halves, parts;       // see attention_dkv_kernel
   float* partial;              // parts x (dK, dV) x tokens x kv_heads x dim, where parts > 1

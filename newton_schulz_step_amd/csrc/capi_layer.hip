@@ -302,6 +302,7 @@ static AttentionArgs attention_args(const muon_attention_t* m) {
   const int64_t tiles = m->offsets != nullptr ? m->tokens / kAttentionRows + std::min<int64_t>(m->sequences, m->tokens)
                                               : (m->tokens + kAttentionRows - 1) / kAttentionRows;
   a.tiles = static_cast<int32_t>(tiles);
+  a.few = m->offsets != nullptr && m->sequences <= kAttentionFew;
   a.heads = m->heads;
   a.kv_heads = m->kv_heads;
   a.group = m->heads / m->kv_heads;
@@ -321,7 +322,7 @@ static size_t attention_workspace(AttentionArgs& a, bool backward, char* base) {
     at += (bytes + 15) / 16 * 16;
     return p;
   };
-  if (a.offsets != nullptr) {
+  if (a.offsets != nullptr && !a.few) {
     a.sequence_list = reinterpret_cast<int4*>(take(static_cast<size_t>(a.sequences) * sizeof(int4)));
     a.list = reinterpret_cast<int4*>(take(static_cast<size_t>(a.tiles) * sizeof(int4)));
   }

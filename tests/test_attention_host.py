@@ -66,9 +66,9 @@ def test_refusals_of_both(lib, call):
         assert call(lib, **{n: heads(0, ts=(1 << 22) + 8)}) == nss.ERR_BAD_SHAPE
         assert call(lib, **{n: heads(0, hs=-64)}) == nss.ERR_BAD_SHAPE
     assert call(lib, lse=at(4) + 2) == nss.ERR_ALIGN
-    assert call(lib, rows(offsets=at(9), sequences=3), ws=None) == nss.ERR_NULL
-    assert call(lib, rows(offsets=at(9), sequences=3), ws_bytes=15) == nss.ERR_WORKSPACE
-    assert call(lib, rows(offsets=at(9), sequences=3), ws=at(5) + 8) == nss.ERR_ALIGN
+    assert call(lib, rows(offsets=at(9), sequences=65), ws=None) == nss.ERR_NULL
+    assert call(lib, rows(offsets=at(9), sequences=65), ws_bytes=15) == nss.ERR_WORKSPACE
+    assert call(lib, rows(offsets=at(9), sequences=65), ws=at(5) + 8) == nss.ERR_ALIGN
     assert call(lib, rows(tokens=0)) == nss.OK
 
 
@@ -88,8 +88,8 @@ def test_overlaps(lib):
     assert forward(lib, o=heads(0)) == nss.ERR_OVERLAP
     assert forward(lib, o=heads(0, data=at(2) + 64)) == nss.ERR_OVERLAP
     assert forward(lib, lse=at(3) + 128) == nss.ERR_OVERLAP
-    assert forward(lib, rows(offsets=at(9), sequences=3), ws=at(0)) == nss.ERR_OVERLAP
-    assert forward(lib, rows(offsets=at(9), sequences=3), ws=at(9)) == nss.ERR_OVERLAP
+    assert forward(lib, rows(offsets=at(9), sequences=65), ws=at(0)) == nss.ERR_OVERLAP
+    assert forward(lib, rows(offsets=at(9), sequences=65), ws=at(9)) == nss.ERR_OVERLAP
     assert forward(lib, rows(offsets=at(3), sequences=3)) == nss.ERR_OVERLAP
     assert forward(lib, o=heads(3, ts=64, hs=64)) == nss.ERR_BAD_SHAPE          # heads on top of tokens
     assert forward(lib, o=heads(3, ts=512, hs=32)) == nss.ERR_BAD_SHAPE

@@ -260,6 +260,36 @@ def test_joint_projection_by_head(lib, T):
         assert torch.equal(djoint[:, :, i], grads[i])
 
 
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 40)])
+@pytest.mark.parametrize("sequences", [1, 2, 63, 64, 65, 200, 1100])
+def test_number_of_sequences(lib, sequences, causal, window):
+    """Tiles are found in each wave for up to 64 sequences, listed beforehand for more: the same rows with empty
+    sequences in between are the same work."""
+    import torch
+    rng = np.random.default_rng(sequences)
+    lens = rng.integers(0, max(3, 1500 // sequences), sequences)
+    lens[sequences // 2] = 300
+    T = int(lens.sum()) + 6
+    off = np.concatenate([[3], 3 + np.cumsum(lens)])
+    q, k, v, do = make(sequences, T, 3, 1, 40, "bf16")
+    how = dict(causal=causal, window=window)
+
+    def run(at):
+        at = torch.from_numpy(np.asarray(at, np.int32)).to("cuda")
+        kept = [torch.full_like(t, 9.0) for t in (q, q, k, k)]
+        lse = torch.full((3, T), 9.0, device="cuda")
+        lib.attention(q, k, v, offsets=at, out=kept[0], lse=lse, **how)
+        lib.attention_backward(do, q, k, v, kept[0], lse, offsets=at, dq=kept[1], dk=kept[2], dv=kept[3], **how)
+        return kept, lse
+    kept, lse = run(off)
+    assert all((t[:3] == 9).all() and (t[T - 3:] == 9).all() for t in kept)
+    at = slice(3, T - 3)
+    check_forward(q[at], k[at], v[at], kept[0][at], lse[:, at], "bf16", offsets=off - 3, **how)
+    check_backward(do[at], q[at], k[at], v[at], kept[0][at], [t[at] for t in kept[1:]], "bf16", offsets=off - 3, **how)
+    other, other_lse = run(np.concatenate([off, np.full(70, off[-1] - 2)]))   # they fall: empty
+    assert torch.equal(lse, other_lse) and all(torch.equal(x, y) for x, y in zip(kept[:2], other[:2]))
+
+
 def test_offsets_out_of_order_and_range(lib):
     import torch
     q, k, v, do = make(6, 260, 2, 2, 64, "bf16")
