@@ -115,7 +115,7 @@ static EmbeddingArgs embedding_args(const muon_embedding_t* e) {
   a.bits = (bits + a.passes - 1) / a.passes;
   a.blocks = sort_blocks(e->tokens);
   a.per_block = (e->tokens + a.blocks - 1) / a.blocks;
-  a.chunk = e->tokens <= 4096 ? 8 : 32;
+  a.chunk = e->tokens <= (e->cols <= 2048 ? 8192 : 4096) ? 8 : 32;
   return a;
 }
 

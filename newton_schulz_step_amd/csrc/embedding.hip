@@ -2,10 +2,10 @@
 //
 //   y[t] = scale table[id_t];   dtable[v] (+)= scale sum over t with id_t = v of dy[t]
 // The gradient sorts the tokens by id (stable, so a row's tokens keep their order), sums
-// chunks of 32 sorted tokens, and joins the sums of rows whose tokens span several chunks:
+// chunks of 32 or 8 sorted tokens, and joins the sums of rows whose tokens span several chunks:
 // a fixed order of sums without floating-point atomics, however often a token occurs.
 // Bound by memory: dy once, the table's rows once. 16384 tokens, 32000 x 4096 fp32, every row written:
-// 155 us (4.3 TB/s; a large copy reaches 5.1).
+// 150 us (4.4 TB/s; a large copy reaches 5.1), of which the sort 20.
 #include <algorithm>
 
 #include "fp8.hpp"
@@ -56,11 +56,11 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbeddingArgs a, int til
 // starts) and of those before it, and places its slots in order, 64 of a wave at a time,
 // ranked with ballots. Few tokens take one block and one launch for all passes.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int64_t kSortBlock = 2048;    // slots of a block, unless that makes too many blocks
+constexpr int64_t kSortBlock = 1024;    // slots of a block, unless that makes too many blocks (2048: 1.7 us more per pass)
 constexpr int32_t kSortBlocks = 256;
 
 int32_t sort_blocks(int64_t n) {
-  if (n <= 2 * kSortBlock) return 1;
+  if (n <= 4 * kSortBlock) return 1;
   return static_cast<int32_t>(std::min<int64_t>((n + kSortBlock - 1) / kSortBlock, kSortBlocks));
 }
 
@@ -192,9 +192,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_all_kernel(EmbeddingArgs a)
 // Sums. A wave takes a chunk of sorted tokens and 512 columns. A row whose tokens lie in one chunk is
 // finished there. A chunk leaves the sum of a row that began before it in its first partial row,
 // and that of one that begins in it and goes on in the second; the next launch joins them, and
-// clears the rows without a token where every row of the table is written. Chunks of 32, and of 8 for
-// up to 4096 tokens, whose waves would be too few to keep the memory busy (1000 tokens x 2048 bf16
-// columns: 20 us with 32, 8 with 8).
+// clears the rows without a token where every row of the table is written. Chunks of 32; of 8 for few
+// tokens, whose waves would be too few to keep the memory busy, while with many tokens the rows of
+// frequent ones span so many chunks that joining them costs more. Added to an fp32 table, chunks of 8 and of
+// 32, whole calls in us: 1000 tokens x 2048 20 and 32, 4200 x 4096 48 and 53, 8192 x 1024 43 and 48, 8192 x 2048 51
+// and 52, 8192 x 4096 72 and 62, 16384 x 512 54 and 49.
 struct SumArgs {
   EmbeddingArgs e;
   const int* keys;

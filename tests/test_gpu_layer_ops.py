@@ -203,7 +203,7 @@ def make_ids(rng, tokens, vocab, kind):
 
 @pytest.mark.parametrize("tokens,vocab,cols", [(1, 1, 1), (7, 3, 9), (33, 1, 40), (64, 255, 8), (65, 256, 512), (100, 300, 513),
                                                (1000, 70000, 65), (4096, 32000, 130), (4097, 1000, 2049), (9000, 511, 96),
-                                               (16384, 40, 24)])
+                                               (16384, 40, 24), (4097, 300, 520), (8192, 3000, 40), (8193, 3000, 40)])
 @pytest.mark.parametrize("kind", ["even", "hot", "one", "mixed", "none"])
 def test_embedding_and_gradient(lib, tokens, vocab, cols, kind):
     import torch
@@ -219,8 +219,8 @@ def test_embedding_and_gradient(lib, tokens, vocab, cols, kind):
         close(host(y), want, (HALF[yt] + U) * np.abs(want) + TINY[yt])
         g = lib.embedding_backward(dy, tid, vocab, scale=scale, out_dtype=dt(gt))
         want, mag, count = L.embedding_backward(host(dy), ids, vocab, s32)
-        # a chunk's tokens in turn, then the chunks, the product and the sum with what is there
-        steps = np.minimum(count, 32) + np.ceil(count / 32) + 4
+        # a chunk's tokens in turn (8 or 32), then the chunks, the product and the sum with what is there
+        steps = np.maximum(np.minimum(count, 32) + np.ceil(count / 32), np.minimum(count, 8) + np.ceil(count / 8)) + 4
         tol = HALF[gt] * np.abs(want) + steps[:, None] * U * mag + TINY[gt]
         close(host(g), want, tol)
         assert torch.equal(g, lib.embedding_backward(dy, tid, vocab, scale=scale, out_dtype=dt(gt)))
