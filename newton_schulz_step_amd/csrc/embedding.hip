@@ -34,19 +34,18 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbeddingArgs a, int til
   const int row = __builtin_amdgcn_readfirstlane(token_row(a, t));
   const bool there = row < a.vocab;
   Raw8<TT> x[4];
-  int n[4];
+  Eight c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    n[i] = static_cast<int>(max<int64_t>(0, min<int64_t>(8, a.cols - c0 - i * 512)));
-    const bool any = there && n[i] > 0;
-    x[i].load(a.table, any ? row * a.ld_table + c0 + i * 512 : 0, any ? n[i] : 0);
+    c[i] = Eight(c0 + i * 512, a.cols);
+    x[i].load(a.table, there ? row * a.ld_table + c[i].at : 0, there ? c[i].n : 0);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = there ? x[i].get(e) * a.scale : 0.0f;
-    write8<YT>(a.y, t * a.ld_y + c0 + i * 512, n[i], v);
+    write_own<YT>(a.y, t * a.ld_y, c[i], v);
   }
 }
 
@@ -206,13 +205,13 @@ struct SumArgs {
 };
 
 template <int WT>
-__device__ __forceinline__ void finish_row(const EmbeddingArgs& a, int64_t row, int64_t c, int n, const float (&sum)[8]) {
+__device__ __forceinline__ void finish_row(const EmbeddingArgs& a, int64_t row, const Eight& c, const float (&sum)[8]) {
   float v[8];
-  const int64_t at = row * a.ld_table + c;
-  if (a.accumulate) read8<WT>(a.dtable, at, n, v);
+  const int64_t at = row * a.ld_table;
+  if (a.accumulate) read8<WT>(a.dtable, at + c.at, c.n, v);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = (a.accumulate ? v[e] : 0.0f) + a.scale * sum[e];
-  write8<WT>(a.dtable, at, n, v);
+  write_own<WT>(a.dtable, at, c, v);
 }
 
 template <int DT, int WT, int CHUNK>
@@ -223,8 +222,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs s) {
   const int64_t item = static_cast<int64_t>(flat_block()) * 4 + (threadIdx.x >> 6);
   if (item >= s.chunks * s.tiles) return;
   const int64_t chunk = item / s.tiles;
-  const int64_t c = (item - chunk * s.tiles) * 512 + lane * 8;
-  const int n = static_cast<int>(max<int64_t>(0, min<int64_t>(8, a.cols - c)));
+  const Eight c((item - chunk * s.tiles) * 512 + lane * 8, a.cols);
   const int64_t first = chunk * CHUNK;
   const int count = static_cast<int>(min<int64_t>(CHUNK, a.tokens - first));
   // keys of the chunk in lanes 0 .. count - 1, those around it for the runs that leave it
@@ -241,7 +239,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs s) {
     for (int j = 0; j < AHEAD; ++j) {
       const int k = __builtin_amdgcn_readlane(key, j0 + j);   // lanes behind the end hold no row
       const int64_t t = __builtin_amdgcn_readlane(slot, j0 + j);
-      x[j].load_once(a.dy, k < none ? t * a.ld_y + c : 0, k < none ? n : 0);
+      x[j].load_once(a.dy, k < none ? t * a.ld_y + c.at : 0, k < none ? c.n : 0);
     }
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
@@ -252,8 +250,8 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs s) {
       const bool at_end = j0 + j == count - 1;
       const int next = at_end ? after : __builtin_amdgcn_readlane(key, (j0 + j + 1) & 63);
       if (next == k && !at_end) continue;
-      if (began && next != k) finish_row<WT>(a, k, c, n, sum);
-      else write8<MUON_DTYPE_F32>(a.partial, (2 * chunk + (began ? 1 : 0)) * a.cols + c, n, sum);
+      if (began && next != k) finish_row<WT>(a, k, c, sum);
+      else write_own<MUON_DTYPE_F32>(a.partial, (2 * chunk + (began ? 1 : 0)) * a.cols, c, sum);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
       began = true;
@@ -296,10 +294,9 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(SumArgs s) {
   const int64_t first = chunk * CHUNK, end = first + CHUNK;
   const int key = s.keys[end - 1];
   if (key >= a.vocab || s.keys[end] != key || (first > 0 && s.keys[first - 1] == key)) return;
-  const int64_t c = (item - chunk * s.tiles) * 512 + lane * 8;
-  const int n = static_cast<int>(max<int64_t>(0, min<int64_t>(8, a.cols - c)));
+  const Eight c((item - chunk * s.tiles) * 512 + lane * 8, a.cols);
   float sum[8];
-  read8<MUON_DTYPE_F32>(a.partial, (2 * chunk + 1) * a.cols + c, n, sum);
+  read8<MUON_DTYPE_F32>(a.partial, (2 * chunk + 1) * a.cols + c.at, c.n, sum);
   for (int64_t d0 = chunk + 1; d0 < s.chunks; d0 += 64) {
     // the chunks that begin with this row's tokens
     const int64_t mine = d0 + lane;
@@ -308,7 +305,7 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(SumArgs s) {
     for (int d = 0; d < run; d += 4) {
       float v[4][8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) read8<MUON_DTYPE_F32>(a.partial, 2 * (d0 + d + u) * a.cols + c, d + u < run ? n : 0, v[u]);
+      for (int u = 0; u < 4; ++u) read8<MUON_DTYPE_F32>(a.partial, 2 * (d0 + d + u) * a.cols + c.at, d + u < run ? c.n : 0, v[u]);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -316,7 +313,7 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(SumArgs s) {
     }
     if (run < 64) break;
   }
-  finish_row<WT>(a, key, c, n, sum);
+  finish_row<WT>(a, key, c, sum);
 }
 
 // ---------------------------------------------------------------------------

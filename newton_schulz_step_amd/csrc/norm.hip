@@ -7,7 +7,7 @@
 // Sums are in fp32, in a fixed order. Bound by memory: every row is read once into registers,
 // a team of 1, 4 or 8 waves per row, eight columns per lane and load. 8192 x 4096 bf16 rows
 // with residual, sum and 8-bit output: 41 us (5.7 TB/s; a large copy reaches 5.1); gradient of
-// 16383 x 2048 with the residual stream's: 54 us (5.0 TB/s), of which 5 join the weight's.
+// 16383 x 2048 with the residual stream's: 52 us (5.2 TB/s), of which 5 join the weight's.
 #include "fp8.hpp"
 #include "layer.hpp"
 #include "quant8.hpp"
@@ -48,10 +48,24 @@ __device__ __forceinline__ float team_sum(float v, float* scratch) {
   return v;
 }
 
+// How rows end: filling the team's registers (every lane's columns are its own: 41 and 52 us in the cases
+// above, 41.6 and 54 with the tests that other rows take), anywhere behind the eighth column, or before it.
+enum Ends { kWhole, kTail, kNarrow };
+template <Ends ENDS>
+__device__ __forceinline__ Eight lane_columns(int64_t c, int64_t cols) {
+  Eight r(c, cols);
+  if constexpr (ENDS == kWhole) {
+    r.at = static_cast<int>(c);
+    r.skip = 0;
+  }
+  if constexpr (ENDS != kNarrow) r.n = 8;
+  return r;
+}
+
 template <int WAVES> constexpr int kNormRows = WAVES < 4 ? 4 / WAVES : 1;   // rows of a workgroup
 template <int WAVES> constexpr int kNormThreads = kNormRows<WAVES> * WAVES * 64;
 
-template <int XT, int WAVES, int V>
+template <int XT, int WAVES, int V, Ends ENDS>
 __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_kernel(NormArgs a) {
   constexpr int TEAM = WAVES * 64;
   __shared__ float scratch[WAVES];
@@ -61,18 +75,17 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_kernel(NormArgs 
 
   Raw8<XT> x[V], r[V];
   float w[V][8], v[V][8];
-  int n[V];
+  Eight c[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int64_t c = (static_cast<int64_t>(i) * TEAM + lane) * 8;
-    n[i] = static_cast<int>(max<int64_t>(0, min<int64_t>(8, a.cols - c)));
-    x[i].load_once(a.x, n[i] > 0 ? row * a.ld_x + c : 0, n[i]);
-    if (a.residual != nullptr) r[i].load_once(a.residual, n[i] > 0 ? row * a.ld_residual + c : 0, n[i]);
+    c[i] = lane_columns<ENDS>((static_cast<int64_t>(i) * TEAM + lane) * 8, a.cols);
+    x[i].load_once(a.x, row * a.ld_x + c[i].at, c[i].n);
+    if (a.residual != nullptr) r[i].load_once(a.residual, row * a.ld_residual + c[i].at, c[i].n);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (a.weight != nullptr) {
-      read8_as(a.weight_dtype, a.weight, (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], w[i]);
+      read8_as(a.weight_dtype, a.weight, c[i].at, c[i].n, w[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[i][e] = 1.0f;
@@ -88,7 +101,11 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_kernel(NormArgs 
       for (int e = 0; e < 8; ++e) v[i][e] += r[i].get(e);
       round8<XT>(v[i]);
     }
-    if (a.sum != nullptr) write8<XT>(a.sum, row * a.ld_sum + (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], v[i]);
+    if (a.sum != nullptr) write_own<XT>(a.sum, row * a.ld_sum, c[i], v[i]);
+    if (c[i].skip > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = e < c[i].skip ? 0.0f : v[i][e];
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum += v[i][e] * v[i][e];
   }
@@ -99,11 +116,19 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_kernel(NormArgs 
   for (int i = 0; i < V; ++i) {
     const int64_t chunk = static_cast<int64_t>(i) * TEAM + lane;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = e < n[i] ? v[i][e] * rstd * w[i][e] : 0.0f;
+    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rstd * w[i][e];
     round8<XT>(v[i]);
-    if (a.y != nullptr) write8<XT>(a.y, row * a.ld_y + chunk * 8, n[i], v[i]);
+    if (a.y != nullptr) write_own<XT>(a.y, row * a.ld_y, c[i], v[i]);
     if (a.q != nullptr) {
       // 16 neighbouring lanes hold a block of 128; what is behind the last column is zeros
+      if (c[i].skip > 0) {
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] = (c[i].skip & o) == 0 ? v[i][e] : e + o < 8 ? v[i][e + o] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = chunk * 8 + e < a.cols ? v[i][e] : 0.0f;
       float m = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(v[i][e]));
@@ -124,26 +149,28 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_kernel(NormArgs 
 
 // Workgroups walk over rows, so that a lane's columns of the weight gradient are summed in
 // registers; what is left is a row of partial sums per workgroup, joined by norm_weight_kernel.
-template <int XT, int WAVES, int V>
+template <int XT, int WAVES, int V, Ends ENDS>
 __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_backward_kernel(NormArgs a) {
   constexpr int TEAM = WAVES * 64, ROWS = kNormRows<WAVES>;
   __shared__ float scratch[WAVES];
   __shared__ float joined[ROWS > 1 ? TEAM * V * 8 : 1];
   const int team = threadIdx.x / TEAM, lane = threadIdx.x % TEAM;
-  int n[V];
+  Eight c[V];
   float w[V][8], acc[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int64_t c = (static_cast<int64_t>(i) * TEAM + lane) * 8;
-    n[i] = static_cast<int>(max<int64_t>(0, min<int64_t>(8, a.cols - c)));
+    c[i] = lane_columns<ENDS>((static_cast<int64_t>(i) * TEAM + lane) * 8, a.cols);
     if (a.weight != nullptr) {
-      read8_as(a.weight_dtype, a.weight, c, n[i], w[i]);
+      read8_as(a.weight_dtype, a.weight, c[i].at, c[i].n, w[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[i][e] = 1.0f;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+    for (int e = 0; e < 8; ++e) {
+      w[i][e] = e < c[i].skip ? 0.0f : w[i][e];   // for the sum over the row
+      acc[i][e] = 0.0f;
+    }
   }
   const float inv = 1.0f / static_cast<float>(a.cols);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + team; row < a.rows;
@@ -151,10 +178,9 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_backward_kernel(
     Raw8<XT> dy[V], s[V], ds[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int64_t c = (static_cast<int64_t>(i) * TEAM + lane) * 8;
-      dy[i].load_once(a.dy, n[i] > 0 ? row * a.ld_dy + c : 0, n[i]);
-      s[i].load_once(a.x, n[i] > 0 ? row * a.ld_x + c : 0, n[i]);
-      if (a.dsum != nullptr) ds[i].load_once(a.dsum, n[i] > 0 ? row * a.ld_dsum + c : 0, n[i]);
+      dy[i].load_once(a.dy, row * a.ld_dy + c[i].at, c[i].n);
+      s[i].load_once(a.x, row * a.ld_x + c[i].at, c[i].n);
+      if (a.dsum != nullptr) ds[i].load_once(a.dsum, row * a.ld_dsum + c[i].at, c[i].n);
     }
     const float rstd = a.rstd_in[row];
     float dot = 0.0f;
@@ -177,7 +203,7 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_backward_kernel(
 #pragma unroll
           for (int e = 0; e < 8; ++e) d[e] += ds[i].get(e);
         }
-        write8<XT>(a.dx, row * a.ld_dx + (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], d);
+        write_own<XT>(a.dx, row * a.ld_dx, c[i], d);
       }
     }
   }
@@ -200,7 +226,7 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void rms_norm_backward_kernel(
   }
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    write8<MUON_DTYPE_F32>(a.partial, blockIdx.x * a.cols + (static_cast<int64_t>(i) * TEAM + lane) * 8, n[i], acc[i]);
+    write_own<MUON_DTYPE_F32>(a.partial, blockIdx.x * a.cols, c[i], acc[i]);
 }
 
 // 64 columns per workgroup, its 16 waves share the partial rows.
@@ -228,7 +254,8 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(NormArgs a, int32_t b
   }
 }
 
-// The smallest team whose registers hold a row (of whole blocks of 128).
+// The smallest team whose registers hold a row (of whole blocks of 128). With three loads per lane beside two
+// and four: gradient of 8192 x 5120 52 us instead of 75, norm of 4096 x 11008 61 instead of 70.
 template <int W, int V> struct Team {
   static constexpr int waves = W, loads = V;
 };
@@ -236,9 +263,12 @@ template <typename F>
 static hipError_t with_team(int64_t cols, F&& f) {
   if (cols <= 512) return f(Team<1, 1>());
   if (cols <= 1024) return f(Team<1, 2>());
+  if (cols <= 1536) return f(Team<1, 3>());
   if (cols <= 2048) return f(Team<1, 4>());
   if (cols <= 4096) return f(Team<4, 2>());
+  if (cols <= 6144) return f(Team<4, 3>());
   if (cols <= 8192) return f(Team<4, 4>());
+  if (cols <= 12288) return f(Team<8, 3>());
   return f(Team<8, 4>());
 }
 
@@ -246,8 +276,10 @@ template <int XT>
 static hipError_t launch_forward(const NormArgs& a, hipStream_t s) {
   return with_team(a.cols, [&](auto team) {
     constexpr int W = decltype(team)::waves, V = decltype(team)::loads;
-    hipLaunchKernelGGL((rms_norm_kernel<XT, W, V>), flat_grid((a.rows + kNormRows<W> - 1) / kNormRows<W>),
-                       dim3(kNormThreads<W>), 0, s, a);
+    const dim3 grid = flat_grid((a.rows + kNormRows<W> - 1) / kNormRows<W>), block(kNormThreads<W>);
+    if (a.cols == W * V * 512) hipLaunchKernelGGL((rms_norm_kernel<XT, W, V, kWhole>), grid, block, 0, s, a);
+    else if (a.cols >= 8) hipLaunchKernelGGL((rms_norm_kernel<XT, W, V, kTail>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((rms_norm_kernel<XT, 1, 1, kNarrow>), grid, block, 0, s, a);
     return hipGetLastError();
   });
 }
@@ -266,8 +298,10 @@ template <int XT>
 static hipError_t launch_backward(const NormArgs& a, hipStream_t s) {
   return with_team(a.cols, [&](auto team) {
     constexpr int W = decltype(team)::waves, V = decltype(team)::loads;
-    hipLaunchKernelGGL((rms_norm_backward_kernel<XT, W, V>), dim3(norm_blocks(a.rows, a.cols)), dim3(kNormThreads<W>), 0,
-                       s, a);
+    const dim3 grid = dim3(norm_blocks(a.rows, a.cols)), block(kNormThreads<W>);
+    if (a.cols == W * V * 512) hipLaunchKernelGGL((rms_norm_backward_kernel<XT, W, V, kWhole>), grid, block, 0, s, a);
+    else if (a.cols >= 8) hipLaunchKernelGGL((rms_norm_backward_kernel<XT, W, V, kTail>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((rms_norm_backward_kernel<XT, 1, 1, kNarrow>), grid, block, 0, s, a);
     return hipGetLastError();
   });
 }

@@ -59,4 +59,28 @@ __device__ __forceinline__ void write8(void* p, int64_t i, int n, const float (&
     if (e < n) store1<DT>(p, i + e, v[e]);
 }
 
+// A lane's eight columns of a row, from column c on, without a branch of its own at the row's end:
+// where fewer than eight are left they are the row's last eight, the first `skip` of them another
+// lane's (8: all of them). Rows of fewer than eight columns are the first lane's. A branch there makes every
+// load wait for the one before it (norm's gradient, 8192 x 4088 bf16: 57 us, 46 without).
+struct Eight {
+  int at, skip, n;   // n elements from column `at` on, the same n for all lanes
+  __device__ __forceinline__ Eight() {}
+  __device__ __forceinline__ Eight(int64_t c, int64_t cols)
+      : at(static_cast<int>(max<int64_t>(0, min(c, cols - 8)))), skip(static_cast<int>(min<int64_t>(8, c - at))),
+        n(static_cast<int>(min<int64_t>(8, cols))) {}
+};
+
+// The lane's own elements of v to the row that begins at element `row`.
+template <int DT>
+__device__ __forceinline__ void write_own(void* p, int64_t row, const Eight& c, const float (&v)[8]) {
+  if (c.skip == 0 && c.n == 8) {
+    write8<DT>(p, row + c.at, 8, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e >= c.skip && e < c.n) store1<DT>(p, row + c.at + e, v[e]);
+  }
+}
+
 }  // namespace muon

@@ -61,7 +61,8 @@ def sum_of(got, x, r, dtype):
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (5, 64), (2, 127), (9, 129), (130, 512), (4, 513), (5, 1024),
                                        (6, 2047), (33, 2048), (3, 2049), (7, 4096), (2, 8191), (3, 8192), (2, 11008),
-                                       (2, 16383), (3, 16384)])
+                                       (2, 16383), (3, 16384), (6, 8), (9, 1536), (5, 1531), (4, 4097), (3, 6144), (2, 6137),
+                                       (3, 8193), (2, 12288), (2, 12287)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_norm(lib, rows, cols, dtype):
     import torch
@@ -88,7 +89,8 @@ def test_norm(lib, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 300), (5, 64), (4, 129), (130, 512), (7, 1000), (3500, 1536),
-                                       (65, 2048), (5, 2049), (900, 4096), (3, 8191), (2, 16384)])
+                                       (65, 2048), (5, 2049), (900, 4096), (3, 8191), (2, 16384), (3, 7), (6, 8), (9, 1536),
+                                       (900, 1531), (4, 4097), (3, 6144), (800, 6137), (3, 8193), (2, 12288), (2, 12287)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_norm_gradient(lib, rows, cols, dtype):
     rng = np.random.default_rng([rows, cols, 1])
