@@ -60,16 +60,17 @@ __device__ __forceinline__ float twin_sum(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiles in LDS: rows of DP elements in 16-byte chunks, chunk c of row r at place c ^ swizzle(r).
+// Tiles in LDS: rows of 64 or 128 elements, DP of them used, in 16-byte chunks, chunk c of row r at place c ^ swizzle(r).
 // A row operand is read with one row per lane and the same chunk in all of them, a transposed
 // one with four chunks of four consecutive rows per half wave; in both the swizzle spreads the
 // lanes that are served together over all banks.
 template <int DP> struct Tile {
-  static constexpr int CHUNKS = DP / 8, PITCH = DP * 2, BYTES = kStage * PITCH;   // of kStage rows
+  static constexpr int WIDE = DP > 64 ? 128 : 64;   // elements of a row in LDS
+  static constexpr int CHUNKS = WIDE / 8, PITCH = WIDE * 2, BYTES = kStage * PITCH;   // of kStage rows
   static constexpr int KS = DP / 16;    // steps of a contraction over the columns
   static constexpr int DB = DP / 32;    // blocks of 32 columns
   static __device__ __forceinline__ int swizzle(int r) {
-    return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    return WIDE == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
   }
   // Byte offset of row `lane % 32`'s chunk lane / 32; step ks is at ^ (ks * 32).
   static __device__ __forceinline__ int row_offset() {
@@ -1001,36 +1002,42 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
 
 // ---------------------------------------------------------------------------
 
-#define MUON_ATTENTION(kernel, heads)                                                                   \
-  do {                                                                                                  \
-    const dim3 grid = flat_grid(static_cast<int64_t>(a.tiles) * (heads));                               \
-    if (a.dtype == MUON_DTYPE_BF16) {                                                                   \
-      if (a.dim <= 64) hipLaunchKernelGGL((kernel<__bf16, 64>), grid, dim3(kThreads), 0, s, a);         \
-      else hipLaunchKernelGGL((kernel<__bf16, 128>), grid, dim3(kThreads), 0, s, a);                    \
-    } else {                                                                                            \
-      if (a.dim <= 64) hipLaunchKernelGGL((kernel<_Float16, 64>), grid, dim3(kThreads), 0, s, a);       \
-      else hipLaunchKernelGGL((kernel<_Float16, 128>), grid, dim3(kThreads), 0, s, a);                  \
-    }                                                                                                   \
-    return hipGetLastError();                                                                           \
-  } while (0)
+// Kernels for heads of up to 32, 64, 96 and 128 columns (8192 tokens, 16 heads, causal, bfloat16, forward and
+// gradient: dimension 32 143 and 406 us, 165 and 511 by the one for 64; 96 228 and 735, 257 and 845 by the one for 128).
+template <typename F>
+static hipError_t with_dim(const AttentionArgs& a, F&& f) {
+  auto of = [&](auto type) {
+    if (a.dim <= 32) f(type, std::integral_constant<int, 32>());
+    else if (a.dim <= 64) f(type, std::integral_constant<int, 64>());
+    else if (a.dim <= 96) f(type, std::integral_constant<int, 96>());
+    else f(type, std::integral_constant<int, 128>());
+    return hipGetLastError();
+  };
+  return a.dtype == MUON_DTYPE_BF16 ? of(static_cast<__bf16>(0.0f)) : of(static_cast<_Float16>(0.0f));
+}
 
 hipError_t launch_attention_list(const AttentionArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(attention_list_kernel, dim3(1), dim3(kListThreads), 0, s, a);
   return hipGetLastError();
 }
-hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_kernel, a.heads); }
-hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) { MUON_ATTENTION(attention_dq_kernel, a.heads); }
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
+  return with_dim(a, [&](auto type, auto dim) {
+    hipLaunchKernelGGL((attention_kernel<decltype(type), decltype(dim)::value>), flat_grid(static_cast<int64_t>(a.tiles) * a.heads),
+                       dim3(kThreads), 0, s, a);
+  });
+}
+hipError_t launch_attention_dq(const AttentionArgs& a, hipStream_t s) {
+  return with_dim(a, [&](auto type, auto dim) {
+    hipLaunchKernelGGL((attention_dq_kernel<decltype(type), decltype(dim)::value>),
+                       flat_grid(static_cast<int64_t>(a.tiles) * a.heads), dim3(kThreads), 0, s, a);
+  });
+}
 template <int HALVES>
 static hipError_t launch_dkv(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid = flat_grid(static_cast<int64_t>(a.tiles) * a.kv_heads * a.parts), block(kThreads * HALVES);
-  if (a.dtype == MUON_DTYPE_BF16) {
-    if (a.dim <= 64) hipLaunchKernelGGL((attention_dkv_kernel<__bf16, 64, HALVES>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attention_dkv_kernel<__bf16, 128, HALVES>), grid, block, 0, s, a);
-  } else {
-    if (a.dim <= 64) hipLaunchKernelGGL((attention_dkv_kernel<_Float16, 64, HALVES>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attention_dkv_kernel<_Float16, 128, HALVES>), grid, block, 0, s, a);
-  }
-  return hipGetLastError();
+  return with_dim(a, [&](auto type, auto dim) {
+    hipLaunchKernelGGL((attention_dkv_kernel<decltype(type), decltype(dim)::value, HALVES>),
+                       flat_grid(static_cast<int64_t>(a.tiles) * a.kv_heads * a.parts), dim3(kThreads * HALVES), 0, s, a);
+  });
 }
 hipError_t launch_attention_dkv(const AttentionArgs& a, hipStream_t s) {
   return a.halves == 2 ? launch_dkv<2>(a, s) : launch_dkv<1>(a, s);

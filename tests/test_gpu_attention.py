@@ -107,7 +107,7 @@ LENS = [[1], [2], [31, 33], [64], [65], [127, 1, 0, 128], [129], [200, 0, 1, 77,
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("dim", [8, 40, 64, 72, 128])
+@pytest.mark.parametrize("dim", [8, 32, 40, 64, 72, 96, 104, 128])
 @pytest.mark.parametrize("lens", LENS, ids=lambda l: f"{len(l)}x{max(l)}")
 def test_forward_and_gradient(lib, lens, dim, dtype):
     tokens = int(np.sum(lens))
@@ -124,7 +124,7 @@ def test_forward_and_gradient(lib, lens, dim, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("dim", [40, 64, 128])
+@pytest.mark.parametrize("dim", [24, 40, 64, 80, 128])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 40)])
 def test_many_key_tiles(lib, causal, window, dim, dtype):
     """From 1024 key tiles on dK and dV take workgroups of four waves, without parts."""
