@@ -726,7 +726,8 @@ typedef struct {
 } muon_attention_t;
 
 /* o = softmax(scale * q k^T) v per sequence and head; scores, their softmax and
- * all sums in fp32, the probabilities rounded to dtype for their product with v.
+ * all sums in fp32, the probabilities rounded to dtype for their product with v
+ * (in F16 off by 2^-32 of the row's largest at least).
  *   lse  device float32[heads x tokens] or NULL: the natural logarithm of each
  *        row's sum of exponentials, for the gradient.
  * Tokens outside every sequence are not read, and their rows of o and lse are not

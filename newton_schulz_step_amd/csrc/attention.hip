@@ -462,6 +462,8 @@ __device__ __forceinline__ void interleave() {
 // scores of tile t + 1 are formed while the exponentials of tile t are taken. The running
 // maximum that exponents refer to follows the true one only when it is 2^8 behind: the
 // exponentials stay below 2^8, and the sums are scaled again a few times per row at most.
+// In fp16 they carry 2^7 more, up to 2^15 of the type's 2^16: without it each key with less than
+// 2^-25 of a row's maximum would add nothing to the product, though thousands of them count.
 // 8192 tokens, 32 query and 8 key heads of 128, causal, bfloat16: 508 us, 1080 TFLOP/s (a large library product
 // 1309 on the same GPU). Bound by power: the same call on zeros takes 418. Two tiles in LDS leave
 // room for two workgroups per CU at dimension 128, which 248 registers allow too.
@@ -506,6 +508,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
   f32x16 acc[TL::DB];
 #pragma unroll
   for (int b = 0; b < TL::DB; ++b) acc[b] = f32x16{};
+  constexpr float UP = H::narrow ? 7.0f : 0.0f, DOWN = H::narrow ? 0x1p-7f : 1.0f;
   float m = -__builtin_huge_valf(), sum = 0.0f;   // the maximum that exponents refer to; this lane's part of the sum
   float top;                                      // the row's maximum in the tile whose exponentials come next
 
@@ -553,7 +556,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[b][e] *= keep;
     }
-    const float mc = m == -__builtin_huge_valf() ? 0.0f : m * c;   // no key seen so far: every term is 0
+    const float mc = m == -__builtin_huge_valf() ? 0.0f : fmaf(m, c, -UP);   // no key seen so far: every term is 0
     if constexpr (MORE) scores(next, kt);
     typename H::v8 w[4];
 #pragma unroll
@@ -621,7 +624,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
   }
   for (; t < tiles; ++t) turn(t);   // the other waves' tiles
   sum = twin_sum(sum);
-  if (a.lse_out != nullptr && h == 0 && row < p.len) a.lse_out[p.head * a.tokens + p.start + row] = m * a.scale + logf(sum);
+  if (a.lse_out != nullptr && h == 0 && row < p.len) a.lse_out[p.head * a.tokens + p.start + row] = m * a.scale + logf(sum * DOWN);
   arrived();   // the tiles are read: their place takes the results
   char* o = static_cast<char*>(a.o.data) + (p.start * a.o.token_stride + p.head * a.o.head_stride) * 2;
   store_rows<T, DP>(acc, 1.0f / sum, lds + wave * kWaveRows * TL::PITCH, o, r0, p.len, a.o.token_stride, a.dim);
@@ -853,8 +856,9 @@ __global__ __launch_bounds__(kThreads * HALVES, 2) void attention_dkv_kernel(Att
   load_rows<T, DP>(kf, k, key, key < p.len, a.k.token_stride, a.dim);
   const int ro = TL::row_offset(), co = TL::column_offset();
   const float c = a.scale * kLog2e;
-  // probabilities in fp16 carry 2^8, so that small ones keep their bits
-  constexpr float PUP = H::narrow ? 256.0f : 1.0f;
+  // probabilities in fp16 carry 2^14, so that small ones keep their bits; they are 1 at most, but for the
+  // rounding of the log-sum-exp, and the type ends at 4
+  constexpr float PUP = H::narrow ? 16384.0f : 1.0f;
   const Sight sight = sight_of_key(a, key);
   f32x16 dk[TL::DB], dv[TL::DB];
 #pragma unroll
