@@ -675,8 +675,9 @@ int muon_grad_sumsq_workspace_size(const muon_tensor_t* grads, int32_t n, size_t
 
 /* Scale n tensors by the norm that *sumsq (device) stands for:
  *   norm = sqrt(*sumsq);  factor = min(1, max_norm / (norm + 1e-6)), in 64 bits;
- *   outs[i] = grads[i] * factor (the factor and the product in fp32), rounded to
- *   outs[i]'s type. With max_norm infinite the factor is 1, whatever the norm.
+ *   outs[i] = grads[i] * factor (the factor with fp32's 24 bits, the product in
+ *   fp32), rounded to outs[i]'s type. With max_norm infinite the factor is 1,
+ *   whatever the norm.
  * outs: n tensors of the same numels, of any of the types: NULL or the same
  * memory and type for scaling in place (not written where the factor is 1), or
  * others, such as the entries of a packed gradient buffer. norm: device

@@ -14,8 +14,7 @@
 
 namespace muon {
 
-// The tensor of workgroup b: the last one that does not begin behind it (empty ones begin
-// where the next one does).
+// The tensor of workgroup b: the last one that does not begin behind it (empty ones are not in the list).
 __device__ __forceinline__ int tensor_of(const ClipArgs& a, int b) {
   const int lane = threadIdx.x & 63;
   const unsigned long long lower = __ballot(lane < a.n && a.t[min(lane, a.n - 1)].first <= b);
@@ -78,8 +77,15 @@ __global__ __launch_bounds__(1024) void sum_partials_kernel(const double* partia
   }
 }
 
+// The factor as two floats: one below fp32's normal numbers would lose bits, so that 2^-100 of it is
+// apart there (1 otherwise). A value that the first product takes out of the normal numbers ends as 0.
+struct Factor {
+  float first, second;
+  __device__ __forceinline__ float of(float x) const { return x * first * second; }
+};
+
 template <int IT, int OT>
-__device__ __forceinline__ void chunk_scale(const void* p, void* o, int64_t lo, int64_t hi, float factor) {
+__device__ __forceinline__ void chunk_scale(const void* p, void* o, int64_t lo, int64_t hi, Factor factor) {
   for (int64_t i0 = lo + threadIdx.x * 8; i0 < hi; i0 += 4 * kClipStep) {
     Raw8<IT> x[4];
     int n[4];
@@ -93,14 +99,14 @@ __device__ __forceinline__ void chunk_scale(const void* p, void* o, int64_t lo, 
     for (int u = 0; u < 4; ++u) {
       float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = x[u].get(e) * factor;
+      for (int e = 0; e < 8; ++e) v[e] = factor.of(x[u].get(e));
       write8<OT>(o, i0 + u * kClipStep, n[u], v);
     }
   }
 }
 
 template <int IT>
-__device__ __forceinline__ void scale_to(int dtype, const void* p, void* o, int64_t lo, int64_t hi, float factor) {
+__device__ __forceinline__ void scale_to(int dtype, const void* p, void* o, int64_t lo, int64_t hi, Factor factor) {
   if (dtype == MUON_DTYPE_F32) chunk_scale<IT, MUON_DTYPE_F32>(p, o, lo, hi, factor);
   else if (dtype == MUON_DTYPE_BF16) chunk_scale<IT, MUON_DTYPE_BF16>(p, o, lo, hi, factor);
   else chunk_scale<IT, MUON_DTYPE_F16>(p, o, lo, hi, factor);
@@ -110,13 +116,15 @@ __global__ __launch_bounds__(kClipThreads) void grad_clip_kernel(ClipArgs a) {
   const double norm = sqrt(*a.sumsq);
   const double ratio = static_cast<double>(a.max_norm) / (norm + 1e-6);
   const bool never = a.max_norm == __builtin_huge_valf();
-  const float factor = static_cast<float>(ratio > 1.0 || never ? 1.0 : ratio);   // NaN stays
+  const double limited = ratio > 1.0 || never ? 1.0 : ratio;   // NaN stays
+  const bool small = limited < 0x1p-126;
+  const Factor factor{small ? 0x1p-100f : 1.0f, static_cast<float>(small ? limited * 0x1p100 : limited)};
   if (a.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = static_cast<float>(norm);
   // last chunks first: those that the norm read last may still lie in the last-level cache
   const int b = static_cast<int>(gridDim.x - 1 - blockIdx.x);
   if (b >= a.blocks) return;
   const ClipTensor& t = a.t[tensor_of(a, b)];
-  if (t.in == t.out && factor == 1.0f) return;
+  if (t.in == t.out && factor.second == 1.0f) return;
   const int64_t lo = static_cast<int64_t>(b - t.first) * a.chunk, hi = min(t.n, lo + a.chunk);
   if (t.in_dtype == MUON_DTYPE_F32) scale_to<MUON_DTYPE_F32>(t.out_dtype, t.in, t.out, lo, hi, factor);
   else if (t.in_dtype == MUON_DTYPE_BF16) scale_to<MUON_DTYPE_BF16>(t.out_dtype, t.in, t.out, lo, hi, factor);
