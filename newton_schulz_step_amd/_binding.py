@@ -1310,7 +1310,7 @@ def _attention_rows(q, k, v, offsets, causal, window, scale):
     tokens, heads, dim = q.shape
     return AttentionRows(tokens, _flat(offsets), 0 if offsets is None else offsets.numel() - 1, heads, k.shape[1], dim,
                          _dtype_code(q), int(bool(causal)), _i32(window, "window"),
-                         dim ** -0.5 if scale is None else scale)
+                         max(dim, 1) ** -0.5 if scale is None else scale)
 
 
 def _attention_workspace(a, backward):
