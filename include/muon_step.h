@@ -591,7 +591,8 @@ typedef struct {
 /* Root-mean-square norm of each row, with sums in fp32:
  *   s = x + residual, rounded to dtype (x itself without a residual);
  *   rstd = 1 / sqrt(mean(s^2) + eps);  y = s * rstd * weight, rounded to dtype.
- * A row whose squares add up to more than fp32 holds (values of 1e19) gets rstd 0.
+ * A row whose squares add up to more than fp32 holds (values of 1e19) gets rstd 0;
+ * with eps 0 a row of zeros, or of values whose squares are (1e-23), gets infinity.
  *   sum   device, dtype, rows x cols, pitch ld_sum: s, the stream that goes on
  *         past the layer; NULL: not wanted.
  *   y     device, dtype, rows x cols, pitch ld_y; NULL: not wanted.
@@ -643,7 +644,8 @@ typedef struct {
 int muon_embedding(const muon_embedding_t* e, const void* table, void* y, int32_t dtype, int64_t ld_y, void* stream);
 
 /* Its gradient: dtable[v] = scale * sum of dy[t] over the tokens with ids[t] = v,
- * summed in fp32 in an order that the ids alone decide, and rounded once; every
+ * summed in fp32 in an order that the ids, their number and cols decide (a part
+ * of the columns by itself may be summed in another), and rounded once; every
  * row is written, zeros where no token is. With `accumulate` the sum is added to
  * what is there, and rows without a token are left alone. dy: device, dtype,
  * tokens x cols, pitch ld_dy. Ids outside [0, vocab) have no gradient.
@@ -728,7 +730,7 @@ typedef struct {
 
 /* o = softmax(scale * q k^T) v per sequence and head; scores, their softmax and
  * all sums in fp32, the probabilities rounded to dtype for their product with v
- * (in F16 off by 2^-32 of the row's largest at least).
+ * (in F16 by half a step, or by 2^-32 of the row's largest where that is more).
  *   lse  device float32[heads x tokens] or NULL: the natural logarithm of each
  *        row's sum of exponentials, for the gradient.
  * Tokens outside every sequence are not read, and their rows of o and lse are not
@@ -748,9 +750,12 @@ int muon_attention(const muon_attention_t* a, const muon_heads_t* q, const muon_
  *   dv = P^T d_o,  dS = P (d_o v^T - delta),  dq = scale dS k,  dk = scale dS^T q,
  * dk and dv summed over the query heads that share them. P and dS are rounded to
  * dtype for their products (in F16 under powers of two that keep them in its
- * range), all sums are in fp32 in an order that the sizes alone decide. dq, dk
- * and dv may be interleaved by token or by head, as the parts of one gradient of
- * a joint projection are. Workspace: muon_attention_workspace_size(a, 1). */
+ * range), all sums are in fp32 in an order that the sizes and offsets decide. dq,
+ * dk and dv may be interleaved by token or by head, as the parts of one gradient
+ * of a joint projection are. Tokens outside every sequence are not read, and their
+ * rows of dq, dk and dv are not written: a product over all rows, such as the
+ * gradient of the projection, needs them cleared before.
+ * Workspace: muon_attention_workspace_size(a, 1). */
 int muon_attention_backward(const muon_attention_t* a, const muon_heads_t* d_o, const muon_heads_t* q,
                             const muon_heads_t* k, const muon_heads_t* v, const muon_heads_t* o, const float* lse,
                             const muon_heads_t* dq, const muon_heads_t* dk, const muon_heads_t* dv, void* workspace,

@@ -1237,7 +1237,7 @@ def grad_sumsq(grads: Sequence, out=None, accumulate: bool = False, ws=None, str
     total to clip_gradients."""
     torch = _torch()
     grads = list(grads)
-    arr, n, index = _tensor_list(grads, "grads")
+    arr, n, _ = _tensor_list(grads, "grads")
     if n == 0:
         raise ValueError("grad_sumsq needs at least one tensor")
     if accumulate and out is None:
@@ -1346,7 +1346,8 @@ def attention_backward(do, q, k, v, out, lse, offsets=None, causal: bool = True,
     """Gradient of attention (muon_attention_backward): (dq, dk, dv), from the gradient `do`
     of its output and what the forward call returned; offsets, causal, window and scale as
     in that call. dq, dk, dv: results to write into, such as the parts of the gradient of
-    a joint projection."""
+    a joint projection. Rows of tokens outside every sequence are not written (a new result
+    is not initialised there): give cleared ones where a product reads all rows."""
     torch = _torch()
     a = _attention_rows(q, k, v, offsets, causal, window, scale)
     for t, name in ((do, "do"), (out, "out")):
