@@ -465,7 +465,8 @@ __device__ __forceinline__ void interleave() {
 // In fp16 they carry 2^7 more, up to 2^15 of the type's 2^16: without it each key with less than
 // 2^-25 of a row's maximum would add nothing to the product, though thousands of them count.
 // 8192 tokens, 32 query and 8 key heads of 128, causal, bfloat16: 508 us, 1080 TFLOP/s (a large library product
-// 1309 on the same GPU). Bound by power: the same call on zeros takes 418. Two tiles in LDS leave
+// 1309 on the same GPU). Power holds the clock at 1.73 GHz, where zeros run at 2.4 (381 us); at either the matrix
+// units are busy in 56 to 57% of the cycles. Two tiles in LDS leave
 // room for two workgroups per CU at dimension 128, which 248 registers allow too.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a) {
@@ -670,8 +671,9 @@ template <typename T> struct ColumnScale {
 
 // dQ: 128 queries per workgroup, keys and values in tiles of 64. Each row's delta and log-sum-exp in
 // units of log 2 are formed on the way, for dK and dV. Three products per pair: 713 us for the forward
-// kernel's case (1160 TFLOP/s, power); 158 for 12 texts of 8191 tokens, 32 heads of 128, of which 78 are
-// the memory's at a copy's rate and half overlaps with the products.
+// kernel's case (1160 TFLOP/s; power, at 1.72 GHz, matrix units busy 61%); 150 to 158 for 12 texts of 8191 tokens, 32
+// heads of 128: 417 MB that L2 misses, 68 us as reads, and matrix units busy 27%, with 6 key tiles
+// per workgroup to hide one behind the other.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs the kernel's name only
@@ -748,7 +750,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionArgs
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse2)) * (d[e] - delta);
       if (masked) {
-      asm volatile("");   // stays a branch
+        asm volatile("");   // stays a branch
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = sight(j0 + jb * 32 + 8 * (e >> 2) + 4 * h + (e & 3)) ? s[e] : 0.0f;
       }

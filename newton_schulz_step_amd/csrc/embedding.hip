@@ -193,9 +193,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_all_kernel(EmbeddingArgs a)
 // and that of one that begins in it and goes on in the second; the next launch joins them, and
 // clears the rows without a token where every row of the table is written. Chunks of 32; of 8 for few
 // tokens, whose waves would be too few to keep the memory busy, while with many tokens the rows of
-// frequent ones span so many chunks that joining them costs more. Added to an fp32 table, chunks of 8 and of
-// 32, whole calls in us: 1000 tokens x 2048 20 and 32, 4200 x 4096 48 and 53, 8192 x 1024 43 and 48, 8192 x 2048 51
-// and 52, 8192 x 4096 72 and 62, 16384 x 512 54 and 49.
+// frequent ones span so many chunks that joining them costs more. The narrower the rows, the more tokens
+// it takes: whole calls in us with chunks of 8 and of 32, added to an fp32 table, 8192 x 1024 41 and 49, 12000 x
+// 1024 48 and 52, 8192 x 2048 48 and 52, 12000 x 2048 63 and 59, 5000 x 2560 40 and 49, 4200 x 4096 46 and 52, 8192 x
+// 4096 68 and 61, 3000 x 8192 50 and 53, 5000 x 8192 73 and 68, 2000 x 11008 45 and 53, 4096 x 11008 79 and
+// 74; into every row of 32000, 8192 x 2048 77 and 82, 4096 x 4096 128 and 134, 12000 x 4096 145 and 143. One limit for
+// all rows of more than 2048 columns stands in their middle: it leaves up to 20% at 2560 columns, 14% at 4096, 7% at 11008.
 struct SumArgs {
   EmbeddingArgs e;
   const int* keys;
