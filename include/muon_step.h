@@ -590,7 +590,8 @@ typedef struct {
 
 /* Root-mean-square norm of each row, with sums in fp32:
  *   s = x + residual, rounded to dtype (x itself without a residual);
- *   rstd = 1 / sqrt(mean(s^2) + eps);  y = s * rstd * weight, rounded to dtype.
+ *   rstd = 1 / sqrt(mean(s^2) + eps), rounded once from that sum;
+ *   y = s * rstd * weight, rounded to dtype.
  * A row whose squares add up to more than fp32 holds (values of 1e19) gets rstd 0;
  * with eps 0 a row of zeros, or of values whose squares are (1e-23), gets infinity.
  *   sum   device, dtype, rows x cols, pitch ld_sum: s, the stream that goes on

@@ -71,6 +71,7 @@ static int norm_common(const muon_norm_t* n, NormArgs& a, std::vector<Span>& ins
   a.rows = n->rows;
   a.cols = n->cols;
   a.eps = n->eps;
+  a.inv_cols = 1.0 / static_cast<double>(n->cols);
   return MUON_OK;
 }
 

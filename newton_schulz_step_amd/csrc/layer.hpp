@@ -14,6 +14,7 @@ struct NormArgs {
   int64_t rows, cols;
   int32_t weight_dtype;
   float eps;
+  double inv_cols;           // forward
   void* sum;                 // forward: optional outputs
   void* y;
   int64_t ld_sum, ld_y;
