@@ -613,7 +613,7 @@ int muon_rms_norm(const muon_norm_t* n, void* sum, int64_t ld_sum, void* y, int6
  *   dx       device, dtype, rows x cols: the gradient of s, which is that of x
  *            and that of the residual; NULL: not wanted.
  *   dweight  device, dweight_dtype[cols]: sum over the rows of dy * s * rstd, in
- *            fp32 in a fixed order, rounded once; with `accumulate` added to what
+ *            fp32 or more in a fixed order, rounded once; with `accumulate` added to what
  *            is there. NULL: not wanted.
  *   workspace  device, muon_rms_norm_backward_workspace_size() bytes, 4-byte
  *            aligned (needed for dweight only). */
