@@ -735,8 +735,9 @@ typedef struct {
  *   lse  device float32[heads x tokens] or NULL: the natural logarithm of each
  *        row's sum of exponentials, for the gradient.
  * Tokens outside every sequence are not read, and their rows of o and lse are not
- * written. Values and scores (times scale, times log2(e)) must be finite in fp32:
- * one that is not can reach every row of its own sequence (never another sequence).
+ * written. Values and scores (times scale, times log2(e)) must be finite in fp32,
+ * and so must sums of 2^8 times the values over the keys: one that is not can
+ * reach every row of its own sequence (never another sequence).
  *   workspace  device, muon_attention_workspace_size(a, 0) bytes, 16-byte
  *              aligned (NULL where that is 0: without offsets, or with few
  *              sequences).
