@@ -24,7 +24,7 @@
 
 namespace muon {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kWaveRows = 32;      // columns of the transposed tile that a wave owns
 constexpr int kStage = 64;         // rows of a tile in LDS
@@ -625,7 +625,11 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttentionArgs a)
   }
   for (; t < tiles; ++t) turn(t);   // the other waves' tiles
   sum = twin_sum(sum);
-  if (a.lse_out != nullptr && h == 0 && row < p.len) a.lse_out[p.head * a.tokens + p.start + row] = m * a.scale + logf(sum * DOWN);
+  if (a.lse_out != nullptr && h == 0 && row < p.len) {
+    // the exponents' reference was rounded: what a score of m had for an exponent beyond UP is in the sum
+    const float off = fmaf(m, c, -fmaf(m, c, -UP)) - UP;
+    a.lse_out[p.head * a.tokens + p.start + row] = m * a.scale + fmaf(off, -kLn2, logf(sum * DOWN));
+  }
   arrived();   // the tiles are read: their place takes the results
   char* o = static_cast<char*>(a.o.data) + (p.start * a.o.token_stride + p.head * a.o.head_stride) * 2;
   store_rows<T, DP>(acc, 1.0f / sum, lds + wave * kWaveRows * TL::PITCH, o, r0, p.len, a.o.token_stride, a.dim);
