@@ -4,7 +4,7 @@
 //   s = x + r, rounded to the rows' type;   rstd = (mean(s^2) + eps)^(-1/2);   y = s rstd w
 // With n = s rstd and g = dy w the gradient is
 //   dx = rstd (g - n mean(g n)) + ds,   dw = sum over rows of dy n.
-// Sums are in fp32, in a fixed order. Bound by memory: every row is read once into registers,
+// Sums are in fp32 or more, in a fixed order. Bound by memory: every row is read once into registers,
 // a team of 1, 4 or 8 waves per row, eight columns per lane and load. 8192 x 4096 bf16 rows
 // with residual, sum and 8-bit output: 41 us (5.7 TB/s; a large copy reaches 5.1); gradient of
 // 16383 x 2048 with the residual stream's: 52 us (5.2 TB/s), of which 5 join the weight's.
